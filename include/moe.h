@@ -141,6 +141,46 @@ int moe_unpack_expert(const moe_expert_shape* shape, const void* block,
 int moe_route(const float* logits, int T, int E, int k, int renorm,
               int32_t* ids, float* weights, int32_t* bad_tokens, void* stream);
 
+/* ---- scored routing -------------------------------------------------------
+ * moe_route for routers that score with a sigmoid, balance their experts with
+ * a bias or route over groups ("02 / A solução": the router picks the experts
+ * of each token; it stays out of the INT4 compression). Per token, E experts:
+ *   s_e = 1 / (1 + exp(-l_e))           (MOE_SCORE_SIGMOID), or
+ *         exp(l_e) / sum_i exp(l_i)     (MOE_SCORE_SOFTMAX);
+ *   v_e = s_e + bias_e orders the experts (without a bias, v_e = l_e: the same
+ *         order as by s_e, decided without rounding an exponential);
+ *   groups: n_groups runs of E / n_groups consecutive experts, each worth its
+ *         largest v (MOE_GROUP_MAX) or the sum of its two largest s + bias
+ *         (MOE_GROUP_TOP2; of the one, where it has one); the top_groups best
+ *         by (worth desc, index asc) stay;
+ *   ids   the k best experts of those groups by (v desc, index asc);
+ *   w_j = s[id_j] * scale, or s[id_j] / (sum_j' s[id_j'] + 1e-20) * scale if
+ *         renorm. The bias is no part of a weight.
+ * An expert whose logit or bias is -inf is never picked; picks for which no
+ * expert is left have id -1 and weight 0 (moe_expert_forward skips id -1).
+ * logits  device, logit_type MOE_F32 or MOE_F16, row t at logits + t * ld
+ *         elements (ld >= E)
+ * bias    device fp32 [E] or NULL
+ * ids, weights, bad_tokens as moe_route: a token is bad if a logit or a bias
+ *         is NaN or +inf, or if no expert can be picked.
+ * Limits: E <= 1024, k <= 32, 1 <= top_groups <= n_groups <= 32, n_groups
+ * dividing E, k <= top_groups * E / n_groups; scale finite. FP32 throughout.
+ */
+enum { MOE_SCORE_SOFTMAX = 0, MOE_SCORE_SIGMOID = 1 };
+enum { MOE_GROUP_MAX = 0, MOE_GROUP_TOP2 = 1 };
+enum { MOE_F32 = 0, MOE_F16 = 1 };
+typedef struct {
+  int32_t score;       /* MOE_SCORE_* */
+  int32_t n_groups;    /* 1: no groups */
+  int32_t top_groups;  /* groups kept per token */
+  int32_t group_rank;  /* MOE_GROUP_* */
+  int32_t renorm;      /* weights sum to scale */
+  float scale;         /* factor on every weight */
+} moe_route_cfg;
+int moe_route_scored(const moe_route_cfg* cfg, const void* logits, int logit_type, long long ld,
+                     int T, int E, int k, const float* bias, int32_t* ids, float* weights,
+                     int32_t* bad_tokens, void* stream);
+
 /* ---- token sort -----------------------------------------------------------
  * Groups the (token, choice) pairs p = t*k + j by expert for the grouped
  * executor ("04 / Resultados": compact experts computed in groups).
@@ -252,6 +292,14 @@ int moe_layer_forward(const moe_expert_shape* shape, const void* x, const float*
                       int E, int k, int renorm, int32_t* ids, float* weights, const void* pool,
                       const int32_t* slot_of, int n_slots, const void* y_shared, void* y,
                       void* workspace, size_t workspace_bytes, int path, void* stream);
+/* The same layer behind the scored router: moe_route_scored(cfg, ...), then
+ * moe_expert_forward(...), on `stream`. Arguments and limits as those two;
+ * all of them are checked before anything is enqueued. */
+int moe_layer_forward_scored(const moe_expert_shape* shape, const void* x, const moe_route_cfg* cfg,
+                             const void* logits, int logit_type, long long ld, int T, int E, int k,
+                             const float* bias, int32_t* ids, float* weights, const void* pool,
+                             const int32_t* slot_of, int n_slots, const void* y_shared, void* y,
+                             void* workspace, size_t workspace_bytes, int path, void* stream);
 /* ---- routed layer without any device allocation --------------------------
  * The pages have no counterpart to this call; it exists for callers that
  * cannot allocate device memory: plugins and serving runtimes whose host
@@ -310,6 +358,54 @@ size_t moe_shared_workspace_bytes(int T, int H, int Is);
 int moe_shared_forward(const void* x, int T, int H, int Is, const void* wg,
                        const void* wu, const void* wd, void* y, void* workspace,
                        size_t workspace_bytes, void* stream);
+
+/* ---- FP8 non-routed path --------------------------------------------------
+ * Block-scaled FP8 (E4M3): a code q of a block with FP32 scale s stands for
+ * q * s. Activations have a scale per 1 x 128 block (one token, 128 columns),
+ * weights per 128 x 128 block; the blocks at the right and lower edge are cut
+ * off where the matrix ends. (The pages keep the non-routed parts in FP16,
+ * moe_shared_forward; these calls serve checkpoints that ship them in FP8.)
+ *
+ * moe_quantize_fp8: per block, amax = max |x|, s = amax / 448 and
+ * q = E4M3(x * (448 / amax)), rounded to nearest even; every step in FP32.
+ * A block of zeros has s = 0 and codes 0; one that holds an infinity or NaN
+ * has s = NaN and codes NaN.
+ * x       device fp16 [rows][cols]
+ * q       device [rows][cols] out, one code per byte
+ * scales  device fp32 [ceil(rows / block_rows)][ceil(cols / 128)] out
+ * Limits: cols a multiple of 16 up to 65536; block_rows 1 or 128; x and q
+ * 16-byte aligned.
+ */
+int moe_quantize_fp8(const void* x, int rows, int cols, int block_rows, void* q, float* scales,
+                     void* stream);
+/* y = x W^T: y[t][n] = sum_b xs[t][b] * ws[n/128][b] * sum_{c in block b} xq[t][c] * wq[n][c]
+ * xq  device codes [T][K], xs device fp32 [T][ceil(K/128)]
+ * wq  device codes [N][K], ws device fp32 [ceil(N/128)][ceil(K/128)]
+ * y   device fp16 [T][N] out (round to nearest even)
+ * Products and sums in FP32; the sums of a block are scaled in FP32 as they
+ * join the total. workspace >= moe_matmul_fp8_workspace_bytes(T, N, K),
+ * 256-aligned, zero-filled before its first use; its first 4 bytes are the
+ * sticky error word (bit 2: a bounded device wait expired, y is not valid).
+ * Limits: T <= 2^20, N <= 65536, K a multiple of 16 up to 65536; xq, wq and y
+ * 16-byte aligned. Errors: MOE_ERR_ARG, MOE_ERR_CAPACITY, MOE_ERR_CUDA.
+ */
+size_t moe_matmul_fp8_workspace_bytes(int T, int N, int K);
+int moe_matmul_fp8(const void* xq, const float* xs, int T, const void* wq, const float* ws, int N,
+                   int K, void* y, void* workspace, size_t workspace_bytes, void* stream);
+/* moe_shared_forward with FP8 weights: x is quantised in 1 x 128 blocks,
+ * h = silu(W_g x) * (W_u x) is formed in FP32 and quantised the same way, and
+ * y = W_d h. Both products as moe_matmul_fp8.
+ * x device fp16 [T][H]; wg, wu device codes [Is][H] with scales sg, su
+ * [ceil(Is/128)][ceil(H/128)]; wd device codes [H][Is] with scales sd
+ * [ceil(H/128)][ceil(Is/128)]; y device fp16 [T][H] out.
+ * workspace >= moe_shared_fp8_workspace_bytes(T, H, Is), as above.
+ * Limits: T <= 2^20; H, Is positive multiples of 64 up to 65536; x, weights
+ * and y 16-byte aligned.
+ */
+size_t moe_shared_fp8_workspace_bytes(int T, int H, int Is);
+int moe_shared_forward_fp8(const void* x, int T, int H, int Is, const void* wg, const float* sg,
+                           const void* wu, const float* su, const void* wd, const float* sd,
+                           void* y, void* workspace, size_t workspace_bytes, void* stream);
 
 /* ---- residency manager ----------------------------------------------------
  * Per-layer GPU slot pools fed from a complete, immutable host source

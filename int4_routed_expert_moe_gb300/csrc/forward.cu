@@ -193,6 +193,30 @@ int moe_layer_forward(const moe_expert_shape* s, const void* x, const float* log
                             workspace, workspace_bytes, path, stream);
 }
 
+int moe_layer_forward_scored(const moe_expert_shape* s, const void* x, const moe_route_cfg* cfg, const void* logits,
+                             int logit_type, long long ld, int T, int E, int k, const float* bias, int32_t* ids,
+                             float* weights, const void* pool, const int32_t* slot_of, int n_slots,
+                             const void* y_shared, void* y, void* workspace, size_t workspace_bytes, int path,
+                             void* stream) {
+  moe::NvtxRange nvtx_range("moe_layer_forward_scored");
+  moe::clear_error();
+  int rc = moe::check_route_cfg("moe_layer_forward_scored", cfg, logits, logit_type, ld, T, E, k);
+  if (rc != MOE_OK) return rc;
+  if (T > 0 && !logits) return moe::fail(MOE_ERR_ARG, "moe_layer_forward_scored: NULL pointer");
+  // The experts' arguments are checked before anything is enqueued.
+  moe::ForwardArgs a;
+  rc = expert_args("moe_layer_forward_scored", s, x, T, ids, weights, k, E, pool, slot_of, n_slots, y_shared, y,
+                   workspace, path, stream, &a);
+  if (rc != MOE_OK) return rc == 1 ? MOE_OK : rc;
+  const size_t need = moe_forward_workspace_bytes(s, T, k, E, path);
+  if (workspace_bytes < need)
+    return moe::fail(MOE_ERR_CAPACITY, "moe_layer_forward_scored: workspace %zu < %zu bytes", workspace_bytes, need);
+  rc = moe_route_scored(cfg, logits, logit_type, ld, T, E, k, bias, ids, weights, nullptr, stream);
+  if (rc != MOE_OK) return rc;
+  return moe_expert_forward(s, x, T, ids, weights, k, E, pool, slot_of, n_slots, y_shared, y, workspace,
+                            workspace_bytes, path, stream);
+}
+
 int moe_workspace_clear_flags(void* workspace, void* stream) {
   moe::clear_error();
   if (!workspace) return moe::fail(MOE_ERR_ARG, "NULL workspace");

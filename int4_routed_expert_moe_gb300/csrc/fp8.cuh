@@ -1,0 +1,71 @@
+// E4M3 block scaling shared by the FP8 kernels.
+#pragma once
+
+#include <cuda_fp16.h>
+
+#include <cstdint>
+
+#include "device.cuh"
+
+namespace moe {
+namespace fp8 {
+
+constexpr int kBlock = 128;       // elements of K per scale
+constexpr float kMax = 448.0f;    // largest E4M3 value
+
+// Running maximum of |x| over eight FP16 values, as two 16-bit patterns: the
+// patterns of non-negative values order as the values do, infinities and NaN
+// above every finite one.
+__device__ __forceinline__ uint32_t amax_bits(const uint4& v, uint32_t m) {
+  m = __vmaxu2(m, v.x & 0x7fff7fffu);
+  m = __vmaxu2(m, v.y & 0x7fff7fffu);
+  m = __vmaxu2(m, v.z & 0x7fff7fffu);
+  return __vmaxu2(m, v.w & 0x7fff7fffu);
+}
+
+struct BlockScale {
+  float scale;  // amax / 448: what a code is multiplied by
+  float inv;    // 448 / amax: what a value is multiplied by
+};
+// A block of zeros has scale 0 and codes 0; a block that holds an infinity or
+// NaN has scale and codes NaN, so that what is computed from it says so.
+__device__ __forceinline__ BlockScale block_scale(float amax) {
+  BlockScale b;
+  if (!(amax < INFINITY)) {
+    b.scale = b.inv = __int_as_float(0x7fffffff);
+  } else {
+    b.scale = amax / kMax;
+    b.inv = amax > 0.0f ? kMax / amax : 0.0f;
+  }
+  return b;
+}
+__device__ __forceinline__ BlockScale block_scale(uint32_t amax_half_bits) {
+  return block_scale(__half2float(__ushort_as_half((unsigned short)amax_half_bits)));
+}
+
+// Two values to two E4M3 codes (a in the low byte), nearest even, saturating.
+__device__ __forceinline__ uint32_t encode2(float a, float b) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(b), "f"(a));
+  return r;
+}
+__device__ __forceinline__ uint32_t encode4(float a, float b, float c, float d) {
+  return encode2(a, b) | (encode2(c, d) << 16);
+}
+// Sixteen FP16 values times inv to sixteen codes.
+__device__ __forceinline__ uint4 encode16(const uint4 (&in)[2], float inv) {
+  uint32_t o[4];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const uint32_t w[4] = {in[i].x, in[i].y, in[i].z, in[i].w};
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const float2 a = __half22float2(u32_as_h2(w[2 * j])), b = __half22float2(u32_as_h2(w[2 * j + 1]));
+      o[2 * i + j] = encode4(a.x * inv, a.y * inv, b.x * inv, b.y * inv);
+    }
+  }
+  return make_uint4(o[0], o[1], o[2], o[3]);
+}
+
+}  // namespace fp8
+}  // namespace moe

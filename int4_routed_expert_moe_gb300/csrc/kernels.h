@@ -91,6 +91,14 @@ int fused_forward_routed(const ForwardArgs& a, const float* logits, int renorm, 
 size_t grouped_workspace_bytes(int H, int I, int T, int k, int E);
 int grouped_forward(const ForwardArgs& a);
 
+// Argument checks of the scored router (see moe_route_scored).
+int check_route_cfg(const char* who, const moe_route_cfg* c, const void* logits, int logit_type, long long ld, int T,
+                    int E, int k);
+
+// FP16 to E4M3 with block scales (see moe_quantize_fp8); arguments checked by the caller.
+int launch_quantize_fp8(const __half* x, int rows, int cols, int block_rows, uint8_t* q, float* scales,
+                        cudaStream_t st);
+
 // Slot-table updates of one residency step, passed to the publish kernel by
 // value (so no host buffer has to outlive the launch).
 constexpr int kMaxSlotUpdates = 128;

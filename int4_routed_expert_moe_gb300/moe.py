@@ -47,6 +47,16 @@ class moe_block_layout(ctypes.Structure):
         (n, ctypes.c_uint32) for n in ("gu_q_gate", "gu_q_up", "gu_sz", "d_q", "d_sz")]
 
 
+MOE_SCORE_SOFTMAX, MOE_SCORE_SIGMOID = 0, 1
+MOE_GROUP_MAX, MOE_GROUP_TOP2 = 0, 1
+MOE_F32, MOE_F16 = 0, 1
+
+
+class moe_route_cfg(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("score", "n_groups", "top_groups", "group_rank", "renorm")] + [
+        ("scale", ctypes.c_float)]
+
+
 MOE_POLICY_DECAY, MOE_POLICY_LRU, MOE_POLICY_PINNED = 0, 1, 2
 
 
@@ -86,6 +96,7 @@ _P = ctypes.c_void_p
 _I = ctypes.c_int
 _SZ = ctypes.c_size_t
 _SHAPE = ctypes.POINTER(moe_expert_shape)
+_CFG = ctypes.POINTER(moe_route_cfg)
 
 _SIGS = {
     "moe_status_string": (ctypes.c_char_p, [_I]),
@@ -96,17 +107,25 @@ _SIGS = {
     "moe_pack_expert": (_I, [_SHAPE] + [_P] * 10),
     "moe_unpack_expert": (_I, [_SHAPE] + [_P] * 10),
     "moe_route": (_I, [_P, _I, _I, _I, _I, _P, _P, _P, _P]),
+    "moe_route_scored": (_I, [_CFG, _P, _I, ctypes.c_longlong, _I, _I, _I, _P, _P, _P, _P, _P]),
     "moe_token_sort": (_I, [_P, _I, _I, _I, _P, _P, _P, _P]),
     "moe_forward_workspace_bytes": (_SZ, [_SHAPE, _I, _I, _I, _I]),
     "moe_expert_forward": (_I, [_SHAPE, _P, _I, _P, _P, _I, _I, _P, _P, _I, _P, _P, _P, _SZ, _I, _P]),
     "moe_expert_forward_zero_copy": (_I, [_SHAPE, _P, _I, _P, _P, _I, _I, _P, _P, _I, _P, _P, _P, _P, _SZ, _P]),
     "moe_layer_forward": (_I, [_SHAPE, _P, _P, _I, _I, _I, _I, _P, _P, _P, _P, _I, _P, _P, _P, _SZ, _I, _P]),
+    "moe_layer_forward_scored": (_I, [_SHAPE, _P, _CFG, _P, _I, ctypes.c_longlong, _I, _I, _I, _P, _P, _P, _P, _P, _I,
+                                      _P, _P, _P, _SZ, _I, _P]),
     "moe_layer_forward_noalloc": (_I, [_SHAPE, _P, _P, _I, _I, _I, _I, _P, _P, _P, _P, _I, _P, _P, _P]),
     "moe_layer_forward_noalloc_flags": (_I, [ctypes.POINTER(ctypes.c_int32), _P]),
     "moe_workspace_clear_flags": (_I, [_P, _P]),
     "moe_workspace_flags": (_I, [_P, ctypes.POINTER(ctypes.c_int32), _P]),
     "moe_shared_workspace_bytes": (_SZ, [_I, _I, _I]),
     "moe_shared_forward": (_I, [_P, _I, _I, _I, _P, _P, _P, _P, _P, _SZ, _P]),
+    "moe_quantize_fp8": (_I, [_P, _I, _I, _I, _P, _P, _P]),
+    "moe_matmul_fp8_workspace_bytes": (_SZ, [_I, _I, _I]),
+    "moe_matmul_fp8": (_I, [_P, _P, _I, _P, _P, _I, _I, _P, _P, _SZ, _P]),
+    "moe_shared_fp8_workspace_bytes": (_SZ, [_I, _I, _I]),
+    "moe_shared_forward_fp8": (_I, [_P, _I, _I, _I, _P, _P, _P, _P, _P, _P, _P, _P, _SZ, _P]),
     "moe_residency_create": (_I, [ctypes.POINTER(moe_residency_cfg), _P, _P, _P, _P, _P,
                                   ctypes.POINTER(_P)]),
     "moe_residency_prepare": (_I, [_P, _I, _P, _I]),
@@ -252,6 +271,42 @@ def moe_route(logits: torch.Tensor, k: int, renorm: bool, ids: torch.Tensor,
                           _stream(stream)), "moe_route")
 
 
+_SCORES = {"softmax": MOE_SCORE_SOFTMAX, "sigmoid": MOE_SCORE_SIGMOID}
+_RANKS = {"max": MOE_GROUP_MAX, "top2": MOE_GROUP_TOP2}
+_LOGIT_TYPES = {torch.float32: MOE_F32, torch.float16: MOE_F16}
+
+
+def moe_route_config(score: str = "softmax", n_groups: int = 1, top_groups: int = 1, group_rank: str = "max",
+                     renorm: bool = True, scale: float = 1.0) -> moe_route_cfg:
+    """A scored router's settings (made once, passed to every call)."""
+    return moe_route_cfg(_SCORES[score], int(n_groups), int(top_groups), _RANKS[group_rank], int(bool(renorm)),
+                         float(scale))
+
+
+def _logits(logits) -> tuple:
+    """(pointer, type, row stride) of a router's logits: rows may be strided."""
+    if not isinstance(logits, torch.Tensor) or not logits.is_cuda:
+        raise TypeError("logits must be a CUDA tensor")
+    if logits.dtype not in _LOGIT_TYPES:
+        raise TypeError(f"logits must be float32 or float16, got {logits.dtype}")
+    if logits.dim() != 2 or (logits.shape[1] > 1 and logits.stride(1) != 1):
+        raise ValueError("logits must be [T][E] with contiguous rows")
+    ld = logits.stride(0) if logits.shape[0] > 1 else logits.shape[1]
+    return logits.data_ptr(), _LOGIT_TYPES[logits.dtype], ld
+
+
+def moe_route_scored(cfg: moe_route_cfg, logits: torch.Tensor, k: int, bias: torch.Tensor | None,
+                     ids: torch.Tensor, weights: torch.Tensor, bad_tokens: torch.Tensor | None = None,
+                     stream=None) -> None:
+    ptr, kind, ld = _logits(logits)
+    T, E = logits.shape
+    _check(_lib.moe_route_scored(cfg, ptr, kind, ld, T, E, k, _dev(bias, torch.float32, "bias", E, nullable=True),
+                                 _dev(ids, torch.int32, "ids", T * k),
+                                 _dev(weights, torch.float32, "weights", T * k),
+                                 _dev(bad_tokens, torch.int32, "bad_tokens", 1, nullable=True),
+                                 _stream(stream)), "moe_route_scored")
+
+
 def moe_token_sort(ids: torch.Tensor, E: int, offsets: torch.Tensor, pair_tok: torch.Tensor,
                    pair_j: torch.Tensor, stream=None) -> None:
     T, k = ids.shape
@@ -324,6 +379,27 @@ def moe_layer_forward(shape, x: torch.Tensor, logits: torch.Tensor, k: int, reno
         _dev(workspace, torch.uint8, "workspace"), workspace.numel(), path, _stream(stream)), "moe_layer_forward")
 
 
+def moe_layer_forward_scored(shape, x: torch.Tensor, cfg: moe_route_cfg, logits: torch.Tensor, k: int,
+                             bias: torch.Tensor | None, ids: torch.Tensor, weights: torch.Tensor,
+                             pool: torch.Tensor, slot_of: torch.Tensor, n_slots: int,
+                             y_shared: torch.Tensor | None, y: torch.Tensor, workspace: torch.Tensor,
+                             path: int = MOE_PATH_AUTO, stream=None) -> None:
+    """moe_route_scored, then moe_expert_forward on its ids and weights."""
+    H, I, g = shape
+    ptr, kind, ld = _logits(logits)
+    T, E = logits.shape
+    s = _shape(shape)
+    bb = moe_expert_block_bytes(shape)
+    _check(_lib.moe_layer_forward_scored(
+        ctypes.byref(s), _dev(x, torch.float16, "x", T * H), cfg, ptr, kind, ld, T, E, k,
+        _dev(bias, torch.float32, "bias", E, nullable=True), _dev(ids, torch.int32, "ids", T * k),
+        _dev(weights, torch.float32, "weights", T * k), _dev(pool, torch.uint8, "pool", n_slots * bb),
+        _dev(slot_of, torch.int32, "slot_of", E), n_slots,
+        _dev(y_shared, torch.float16, "y_shared", T * H, nullable=True), _dev(y, torch.float16, "y", T * H),
+        _dev(workspace, torch.uint8, "workspace"), workspace.numel(), path, _stream(stream)),
+        "moe_layer_forward_scored")
+
+
 def moe_layer_forward_noalloc(shape, x: torch.Tensor, logits: torch.Tensor, k: int, renorm: bool,
                               ids: torch.Tensor, weights: torch.Tensor, pool: torch.Tensor,
                               slot_of: torch.Tensor, n_slots: int, y_shared: torch.Tensor | None,
@@ -373,6 +449,60 @@ def moe_shared_forward(x: torch.Tensor, wg: torch.Tensor, wu: torch.Tensor, wd: 
         _dev(wu, torch.float16, "wu", Is * H), _dev(wd, torch.float16, "wd", H * Is),
         _dev(y, torch.float16, "y", T * H), _dev(workspace, torch.uint8, "workspace"),
         workspace.numel(), _stream(stream)), "moe_shared_forward")
+
+
+# ---- FP8 non-routed path -----------------------------------------------------
+_FP8 = torch.float8_e4m3fn
+
+
+def _nb(n: int) -> int:
+    return (n + 127) // 128
+
+
+def moe_quantize_fp8(x: torch.Tensor, q: torch.Tensor, scales: torch.Tensor, block_rows: int = 1,
+                     stream=None) -> None:
+    """x (fp16 [rows][cols]) to float8_e4m3fn codes q and scales
+    [ceil(rows / block_rows)][ceil(cols / 128)]; block_rows 1 (activations) or 128 (weights)."""
+    rows, cols = x.shape
+    _check(_lib.moe_quantize_fp8(_dev(x, torch.float16, "x"), rows, cols, block_rows, _dev(q, _FP8, "q", rows * cols),
+                                 _dev(scales, torch.float32, "scales", -(-rows // max(1, block_rows)) * _nb(cols)),
+                                 _stream(stream)), "moe_quantize_fp8")
+
+
+def moe_matmul_fp8_workspace_bytes(T: int, N: int, K: int) -> int:
+    return _lib.moe_matmul_fp8_workspace_bytes(T, N, K)
+
+
+def moe_matmul_fp8(xq: torch.Tensor, xs: torch.Tensor, wq: torch.Tensor, ws: torch.Tensor, y: torch.Tensor,
+                   workspace: torch.Tensor, stream=None) -> None:
+    """y [T][N] = x W^T from the codes xq [T][K], wq [N][K] and their scales."""
+    T, K = xq.shape
+    N = wq.shape[0]
+    if wq.shape[1] != K:
+        raise ValueError(f"xq has {K} columns, wq {wq.shape[1]}")
+    nb = _nb(K)
+    _check(_lib.moe_matmul_fp8(
+        _dev(xq, _FP8, "xq"), _dev(xs, torch.float32, "xs", T * nb), T, _dev(wq, _FP8, "wq"),
+        _dev(ws, torch.float32, "ws", _nb(N) * nb), N, K, _dev(y, torch.float16, "y", T * N),
+        _dev(workspace, torch.uint8, "workspace"), workspace.numel(), _stream(stream)), "moe_matmul_fp8")
+
+
+def moe_shared_fp8_workspace_bytes(T: int, H: int, Is: int) -> int:
+    return _lib.moe_shared_fp8_workspace_bytes(T, H, Is)
+
+
+def moe_shared_forward_fp8(x: torch.Tensor, wg: torch.Tensor, sg: torch.Tensor, wu: torch.Tensor, su: torch.Tensor,
+                           wd: torch.Tensor, sd: torch.Tensor, y: torch.Tensor, workspace: torch.Tensor,
+                           stream=None) -> None:
+    """moe_shared_forward with float8_e4m3fn weights and their 128 x 128 block scales."""
+    T, H = x.shape
+    Is = wg.shape[0]
+    ns = _nb(H) * _nb(Is)
+    _check(_lib.moe_shared_forward_fp8(
+        _dev(x, torch.float16, "x"), T, H, Is, _dev(wg, _FP8, "wg", Is * H), _dev(sg, torch.float32, "sg", ns),
+        _dev(wu, _FP8, "wu", Is * H), _dev(su, torch.float32, "su", ns), _dev(wd, _FP8, "wd", H * Is),
+        _dev(sd, torch.float32, "sd", ns), _dev(y, torch.float16, "y", T * H),
+        _dev(workspace, torch.uint8, "workspace"), workspace.numel(), _stream(stream)), "moe_shared_forward_fp8")
 
 
 # ---- residency manager -----------------------------------------------------

@@ -1,0 +1,206 @@
+"""Scored router against the FP64 oracle (needs a GB300).
+
+Ids are compared exactly, except for tokens whose order hinges on two computed
+values closer than 1e-6 (FP32 scores and sums round at 6e-8 relative; either
+order is right there): there the weights alone are compared. Weights: FP32
+exponentials, one division and the renormalising sum, 1e-6 relative each at
+most, so rtol 4e-6."""
+import itertools
+
+import numpy as np
+import pytest
+import torch
+
+from oracle import fp8_oracle as f8
+from tests._lib import binding
+
+pytestmark = pytest.mark.gpu
+
+moe = binding() if torch.cuda.is_available() else None
+
+MARGIN, RTOL = 1e-6, 4e-6
+
+
+def _run(l, k, bias=None, stream=None, **cfg):
+    dev = torch.device("cuda")
+    T = l.shape[0]
+    lt = l if isinstance(l, torch.Tensor) else torch.from_numpy(l).to(dev)
+    ids = torch.full((T, k), -7, dtype=torch.int32, device=dev)
+    w = torch.full((T, k), 7.0, dtype=torch.float32, device=dev)
+    bad = torch.zeros(1, dtype=torch.int32, device=dev)
+    b = None if bias is None else torch.from_numpy(np.asarray(bias, np.float32)).to(dev)
+    moe.moe_route_scored(moe.moe_route_config(**cfg), lt, k, b, ids, w, bad, stream)
+    torch.cuda.synchronize()
+    return ids.cpu().numpy(), w.cpu().numpy(), int(bad.item())
+
+
+def _check(l, k, bias=None, **cfg):
+    got = _run(l, k, bias, **cfg)
+    ref = f8.route_scored(l, k, bias=bias, **cfg)
+    clear = f8.closest_call(l, k, bias=bias, **cfg) > MARGIN
+    assert clear.mean() > 0.9
+    assert np.array_equal(got[0][clear], ref[0][clear])
+    assert np.allclose(got[1], ref[1], rtol=RTOL, atol=1e-12)
+    assert got[2] == ref[2]
+    return got
+
+
+def _bias(rng, E):
+    return rng.permutation(np.linspace(-0.1, 0.1, E)).astype(np.float32)
+
+
+@pytest.mark.parametrize("score,rank,biased,renorm", list(itertools.product(
+    ["softmax", "sigmoid"], ["max", "top2"], [False, True], [False, True])))
+@pytest.mark.parametrize("T,E,G,tg,k", [(1, 256, 8, 4, 8), (37, 60, 6, 3, 4), (5, 8, 8, 3, 3), (9, 96, 1, 1, 32),
+                                        (3, 1024, 32, 5, 16)])
+def test_matches_oracle(T, E, G, tg, k, score, rank, biased, renorm):
+    rng = np.random.default_rng(E + T)
+    l = (1.5 * rng.normal(size=(T, E))).astype(np.float32)
+    _check(l, k, _bias(rng, E) if biased else None, score=score, n_groups=G, top_groups=tg, group_rank=rank,
+           renorm=renorm, scale=2.5)
+
+
+@pytest.mark.parametrize("E,G,k", [(1, 1, 1), (2, 2, 1), (33, 1, 7), (513, 1, 10), (1020, 17, 12), (1023, 31, 6),
+                                   (999, 9, 9), (31, 31, 4)])
+def test_odd_expert_counts(E, G, k):
+    rng = np.random.default_rng(E)
+    l = rng.normal(size=(11, E)).astype(np.float32)
+    _check(l, k, _bias(rng, E), score="sigmoid", n_groups=G, top_groups=max(1, G // 2), group_rank="top2")
+
+
+@pytest.mark.parametrize("T", [4099, 8192])
+def test_many_tokens(T):
+    rng = np.random.default_rng(T)
+    l = rng.normal(size=(T, 64)).astype(np.float32)
+    _check(l, 6, _bias(rng, 64), score="sigmoid", n_groups=4, top_groups=2, group_rank="top2", scale=1.5)
+
+
+def test_equals_moe_route_without_bias_and_groups():
+    l = np.random.default_rng(5).normal(size=(300, 64)).astype(np.float32)
+    l[:, 40:] = l[:, :24]  # exact ties
+    dev = torch.device("cuda")
+    for renorm in (False, True):
+        ids = torch.empty((300, 8), dtype=torch.int32, device=dev)
+        w = torch.empty((300, 8), dtype=torch.float32, device=dev)
+        moe.moe_route(torch.from_numpy(l).to(dev), 8, renorm, ids, w)
+        got = _run(l, 8, renorm=renorm)
+        assert np.array_equal(got[0], ids.cpu().numpy())
+        assert np.allclose(got[1], w.cpu().numpy(), rtol=RTOL)
+
+
+def test_ties_go_to_the_lowest_index():
+    l = np.zeros((3, 48), np.float32)
+    l[1, ::2] = -0.0
+    l[2, 40:] = 1.0
+    for score in ("softmax", "sigmoid"):
+        got = _run(l, 5, score=score, n_groups=6, top_groups=2, group_rank="top2")
+        assert got[0].tolist() == [[0, 1, 2, 3, 4], [0, 1, 2, 3, 4], [40, 41, 42, 43, 44]]
+
+
+def test_saturated_scores_are_ordered_by_logit():
+    # 1 / (1 + exp(-40)) rounds to 1 in FP32: the logits still order the experts.
+    l = (40.0 + np.random.default_rng(2).permutation(64)[None]).astype(np.float32)
+    got = _run(l, 4, score="sigmoid")
+    assert got[0].tolist() == [np.argsort(-l[0])[:4].tolist()] and np.allclose(got[1], 0.25)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("biased", [False, True])
+@pytest.mark.parametrize("G,rank", [(1, "max"), (4, "max"), (4, "top2")])
+def test_masks_and_bad_tokens(score, biased, G, rank):
+    rng = np.random.default_rng(7)
+    l = rng.normal(size=(40, 32)).astype(np.float32)
+    l[rng.random(l.shape) < 0.6] = -np.inf
+    l[3] = -np.inf                      # none left
+    l[4, 5], l[5, 31] = np.nan, np.inf
+    l[6] = -np.inf
+    l[6, 17] = 0.5                      # one left
+    l[7] = np.finfo(np.float32).min     # the type's lowest value is a logit like any other
+    l[8, 8:] = np.finfo(np.float32).min
+    bias = _bias(rng, 32) if biased else None
+    cfg = dict(score=score, n_groups=G, top_groups=max(1, G // 2), group_rank=rank)
+    got = _run(l, 6, bias, **cfg)
+    with np.errstate(over="ignore", invalid="ignore"):
+        ref = f8.route_scored(l, 6, bias=bias, **cfg)
+        gap = f8.closest_call(l, 6, bias=bias, **cfg)
+    clear = gap > MARGIN
+    assert np.array_equal(got[0][clear], ref[0][clear]) and clear.sum() > 30
+    assert np.allclose(got[1], ref[1], rtol=RTOL, atol=1e-12) and got[2] == ref[2] == 3
+    assert got[0][6].tolist() == [17] + [-1] * 5
+
+
+def test_bias_masks_and_bad_bias():
+    l = np.random.default_rng(8).normal(size=(9, 16)).astype(np.float32)
+    bias = np.zeros(16, np.float32)
+    bias[3:] = -np.inf
+    got = _check(l, 5, bias, score="sigmoid")
+    assert (got[0][:, 3:] == -1).all() and (got[0][:, :3] >= 0).all()
+    for v in (np.nan, np.inf):
+        bias[5] = v
+        got = _run(l, 5, bias, score="sigmoid")
+        assert (got[0] == -1).all() and not got[1].any() and got[2] == 9
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.float16])
+@pytest.mark.parametrize("E,pad", [(64, 0), (64, 64), (60, 5), (256, 1)])
+def test_types_and_row_strides(dtype, E, pad):
+    rng = np.random.default_rng(E + pad)
+    full = torch.from_numpy(rng.normal(size=(50, E + pad)).astype(np.float32)).to(dtype).cuda()
+    view = full[:, pad // 2:pad // 2 + E]
+    bias = _bias(rng, E)
+    cfg = dict(score="sigmoid", n_groups=4, top_groups=2, group_rank="top2", renorm=True, scale=2.5)
+    got = _run(view, 6, bias, **cfg)
+    l = view.float().cpu().numpy()
+    ref = f8.route_scored(l, 6, bias=bias, **cfg)
+    clear = f8.closest_call(l, 6, bias=bias, **cfg) > MARGIN
+    assert np.array_equal(got[0][clear], ref[0][clear])
+    assert np.allclose(got[1], ref[1], rtol=RTOL)
+
+
+def test_rows_beyond_32_bit_offsets():
+    # Row 40 starts 2.4e9 elements into the buffer (FP16, 4.8 GB).
+    ld, T, E = 60_000_000, 41, 16
+    buf = torch.zeros(ld * (T - 1) + E, dtype=torch.float16, device="cuda")
+    view = torch.as_strided(buf, (T, E), (ld, 1))
+    vals = np.random.default_rng(3).normal(size=(T, E)).astype(np.float16)
+    view.copy_(torch.from_numpy(vals).cuda())
+    got = _run(view, 4, score="sigmoid")
+    ref = f8.route_scored(vals, 4, score="sigmoid")
+    assert np.array_equal(got[0], ref[0]) and np.allclose(got[1], ref[1], rtol=RTOL)
+
+
+def test_other_stream_and_repeatability():
+    l = np.random.default_rng(4).normal(size=(500, 128)).astype(np.float32)
+    lt = torch.from_numpy(l).cuda()
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    a = _run(lt, 8, score="softmax", n_groups=8, top_groups=3, group_rank="top2")
+    b = _run(lt, 8, stream=s, score="softmax", n_groups=8, top_groups=3, group_rank="top2")
+    assert np.array_equal(a[0], b[0]) and np.array_equal(a[1], b[1])
+
+
+def test_refusals():
+    dev = torch.device("cuda")
+    l = torch.zeros((4, 16), device=dev)
+    ids = torch.empty((4, 4), dtype=torch.int32, device=dev)
+    w = torch.empty((4, 4), device=dev)
+    for cfg, k in ((dict(n_groups=3), 2), (dict(n_groups=4, top_groups=5), 2), (dict(n_groups=8, top_groups=1), 3),
+                   (dict(n_groups=0), 2), (dict(scale=float("nan")), 2), (dict(), 0), (dict(), 17)):
+        with pytest.raises((moe.MoeError, ValueError)):
+            moe.moe_route_scored(moe.moe_route_config(**cfg), l, k, None, ids, w)
+    cfg = moe.moe_route_config()
+    with pytest.raises(TypeError):
+        moe.moe_route_scored(cfg, l.double(), 2, None, ids, w)
+    with pytest.raises(ValueError):
+        moe.moe_route_scored(cfg, l.t(), 2, None, ids, w)
+    with pytest.raises(ValueError):
+        moe.moe_route_scored(cfg, l, 8, None, ids, w)
+    with pytest.raises(ValueError):
+        moe.moe_route_scored(cfg, l, 4, torch.zeros(8, device=dev), ids, w)
+
+
+def test_empty_batch():
+    dev = torch.device("cuda")
+    moe.moe_route_scored(moe.moe_route_config(), torch.empty((0, 16), device=dev), 4, None,
+                         torch.empty((0, 4), dtype=torch.int32, device=dev), torch.empty((0, 4), device=dev))
+    torch.cuda.synchronize()
