@@ -2,118 +2,551 @@
 //   y[t][n] = sum_b xs[t][b] ws[n/128][b] sum_{c in block b} xq[t][c] wq[n][c]
 // with E4M3 codes, one scale per 1 x 128 block of x and per 128 x 128 block of
 // W, FP32 sums.
-#include <cuda_fp8.h>
+//
+// Tensor-core kernel: 128 tokens (the MMA's M) by NT rows of W (its N); both
+// operands come by TMA in the 128-byte-swizzled K-major layout, one scale
+// block (128 codes, 128 bytes) per pipeline step. The scales change every
+// step, so a step's four MMAs (K = 32 each) start a fresh FP32 accumulator in
+// tensor memory, and promotion warps read it back and add it, times its
+// scale, to sums in registers. A token is a lane of tensor memory, hence one
+// thread; the weight scale is the same for 128 columns: the scale of a step
+// is one number per thread, and promotion one packed FMA per two sums.
+#include <algorithm>
+#include <mutex>
 
 #include "common.h"
 #include "device.cuh"
 #include "fp8.cuh"
 #include "kernels.h"
+#include "tc.cuh"
 
 namespace moe {
 namespace {
 
-constexpr int kTile = 64, kStep = 32;
+constexpr int BM = 128;           // tokens per tile
+constexpr int BK = fp8::kBlock;   // codes per step: one scale block, one swizzle row
+constexpr uint32_t kABytes = BM * BK;
+constexpr int kMaxSplits = 8;     // portable cluster size
 
-__device__ __forceinline__ float decode1(uint8_t c) {
-  __nv_fp8_e4m3 v;
-  v.__x = c;
-  return (float)v;
+// Geometry by tile width. Warp 0 issues TMA, warp 1 owns tensor memory and
+// issues the MMAs, the others promote, at most 64 columns each.
+template <int NT>
+struct Geo {
+  static constexpr int cols = NT < 64 ? NT : 64;  // columns per promotion warp
+  static constexpr int promo = 4 * (NT / cols);
+  static constexpr int threads = 64 + 32 * promo;
+  static constexpr uint32_t stage = kABytes + (uint32_t)NT * BK;
+  static constexpr int stages = NT == 256 ? 4 : NT == 128 ? 6 : 8;
+  static constexpr int bufs = NT == 256 ? 2 : NT == 128 ? 4 : 8;  // accumulators in tensor memory
+  static constexpr uint32_t tmem_cols = (uint32_t)bufs * NT;
+  static constexpr uint32_t off_ctrl = (uint32_t)stages * stage;
+  static constexpr size_t smem = (size_t)off_ctrl + 4096 + 1024;  // control block, alignment
+  static constexpr int red_pitch = NT + 4;                        // floats per row of a partial tile
+  static_assert((size_t)BM * red_pitch * 4 <= off_ctrl, "partial tile fits the stage area");
+  static_assert(tmem_cols <= 512 && (tmem_cols & (tmem_cols - 1)) == 0, "tensor memory budget");
+};
+
+struct GemmArgs {
+  int T, N, K;        // N: rows of W (output columns; Is for gate/up)
+  int nb;             // scale blocks along K
+  int mt, tiles;      // token tiles, tiles in all
+  int splits;         // blocks of a cluster share one tile's K steps
+  uint32_t a_bytes;   // bytes of the token tile's box
+  const float *xs, *ws, *ws2;
+  __half* y;          // product
+  uint8_t* hq;        // gate/up: h codes [T][N] and scales [T][nbh]
+  float* hs;
+  int nbh;
+  int32_t* flags;
+};
+
+struct Bars {
+  uint64_t *full, *empty, *acc_full, *acc_empty;
+  uint32_t* tmem_slot;
+  int* abort;
+  float* amax;  // [4][BM], gate/up
+};
+template <int NT>
+__device__ __forceinline__ Bars bars_at(uint8_t* p) {
+  using G = Geo<NT>;
+  Bars b;
+  uint64_t* q = reinterpret_cast<uint64_t*>(p);
+  b.full = q; q += G::stages;
+  b.empty = q; q += G::stages;
+  b.acc_full = q; q += G::bufs;
+  b.acc_empty = q; q += G::bufs;
+  b.tmem_slot = reinterpret_cast<uint32_t*>(q);
+  b.abort = reinterpret_cast<int*>(b.tmem_slot + 1);
+  b.amax = reinterpret_cast<float*>(p + 1024);
+  return b;
+}
+__device__ __forceinline__ void abort_block(const Bars& b, int32_t* flags) {
+  atomicOr(flags, 4);
+  *reinterpret_cast<volatile int*>(b.abort) = 1;
+}
+__device__ __forceinline__ bool is_aborted(const Bars& b) { return *reinterpret_cast<volatile int*>(b.abort) != 0; }
+
+// sum (two FP32 lanes) += d * s (both lanes).
+__device__ __forceinline__ void fma2(uint64_t& sum, uint32_t d0, uint32_t d1, uint64_t s2) {
+  uint64_t d;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "r"(d0), "r"(d1));
+  asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(sum) : "l"(d), "l"(s2));
+}
+__device__ __forceinline__ uint64_t pack2(float a, float b) {
+  uint64_t d;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(a), "f"(b));
+  return d;
+}
+__device__ __forceinline__ float2 unpack2(uint64_t v) {
+  float2 f;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(f.x), "=f"(f.y) : "l"(v));
+  return f;
+}
+__device__ __forceinline__ uint32_t half2_bits(float a, float b) {
+  const half2 h = __floats2half2_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-// 64 tokens x 64 rows of W per block of 256 threads, 4 x 4 sums per thread;
-// the sums of a 128-element block are scaled as they join the total.
-template <bool F32OUT>
-__global__ void __launch_bounds__(256) fp8_matmul_kernel(const uint8_t* __restrict__ xq, const float* __restrict__ xs,
-                                                         int T, const uint8_t* __restrict__ wq,
-                                                         const float* __restrict__ ws, int N, int K, void* y) {
-  __shared__ float sx[kTile][kStep + 1], sw[kTile][kStep + 1];
-  const int n0 = blockIdx.x * kTile, t0 = blockIdx.y * kTile;
-  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-  const int nb = (K + fp8::kBlock - 1) / fp8::kBlock;
-  float total[4][4] = {};
-  for (int b = 0; b < nb; ++b) {
-    float acc[4][4] = {};
-    for (int k0 = b * fp8::kBlock; k0 < min(K, (b + 1) * fp8::kBlock); k0 += kStep) {
-      __syncthreads();
-      for (int i = threadIdx.x; i < kTile * kStep; i += 256) {
-        const int r = i / kStep, c = i % kStep;
-        const bool kc = k0 + c < K;
-        sx[r][c] = kc && t0 + r < T ? decode1(xq[(size_t)(t0 + r) * K + k0 + c]) : 0.0f;
-        sw[r][c] = kc && n0 + r < N ? decode1(wq[(size_t)(n0 + r) * K + k0 + c]) : 0.0f;
-      }
-      __syncthreads();
-#pragma unroll 8
-      for (int c = 0; c < kStep; ++c) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-          for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(sx[ty * 4 + i][c], sw[tx * 4 + j][c], acc[i][j]);
-      }
-    }
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int t = t0 + ty * 4 + i, n = n0 + tx * 4 + j;
-        if (t < T && n < N)
-          total[i][j] = fmaf(xs[(size_t)t * nb + b] * ws[(size_t)(n / fp8::kBlock) * nb + b], acc[i][j], total[i][j]);
-      }
-  }
-  for (int i = 0; i < 4; ++i)
-    for (int j = 0; j < 4; ++j) {
-      const int t = t0 + ty * 4 + i, n = n0 + tx * 4 + j;
-      if (t < T && n < N) {
-        if (F32OUT) static_cast<float*>(y)[(size_t)t * N + n] = total[i][j];
-        else static_cast<__half*>(y)[(size_t)t * N + n] = __float2half_rn(total[i][j]);
-      }
-    }
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// 16 bytes of another block's shared memory, at this block's address `a`.
+__device__ __forceinline__ float4 ld_cluster(uint32_t a, uint32_t rank) {
+  uint32_t ra;
+  float4 v;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(ra) : "r"(a), "r"(rank));
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(ra)
+               : "memory");
+  return v;
+}
+// Named barrier over the promotion warps; true for all if q is true for any.
+template <int THREADS>
+__device__ __forceinline__ bool promo_any(bool q) {
+  uint32_t r;
+  asm volatile(
+      "{\n .reg .pred p, q;\n setp.ne.u32 q, %1, 0;\n barrier.cta.red.or.pred p, 1, %2, q;\n selp.u32 %0, 1, 0, p;\n}\n"
+      : "=r"(r) : "r"((uint32_t)q), "n"(THREADS) : "memory");
+  return r != 0;
 }
 
-// h = silu(gate) * up, quantised in 1 x 128 blocks: a warp per block.
-__global__ void __launch_bounds__(256) swiglu_quantize_kernel(const float* __restrict__ gate,
-                                                              const float* __restrict__ up, unsigned units, int cols,
-                                                              int cblocks, uint8_t* __restrict__ q,
-                                                              float* __restrict__ scales) {
-  const unsigned u = (blockIdx.x * 256u + threadIdx.x) >> 5;
-  const int lane = threadIdx.x & 31;
-  if (u >= units) return;
-  const unsigned r = u / (unsigned)cblocks;
-  const int c0 = (int)(u - r * (unsigned)cblocks) * 128 + lane * 4;
-  float h[4] = {};
+// h = silu(gate) * up of N values in place of gate, and their largest
+// magnitude (infinite if one of them is not finite).
+template <int N>
+__device__ __forceinline__ float swiglu(float (&gt)[N], const float (&up)[N]) {
   float m = 0.0f;
   bool bad = false;
-  if (c0 < cols) {
-    for (int j = 0; j < 4; ++j) {
-      const size_t i = (size_t)r * cols + c0 + j;
-      h[j] = silu_f(gate[i]) * up[i];
-      bad |= !(fabsf(h[j]) < INFINITY);
-      m = fmaxf(m, fabsf(h[j]));
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    gt[i] = silu_f(gt[i]) * up[i];
+    bad |= !(fabsf(gt[i]) < INFINITY);
+    m = fmaxf(m, fabsf(gt[i]));
+  }
+  return bad ? INFINITY : m;
+}
+
+// GATEUP: the tile is 128 rows of W_g and the same 128 of W_u; the epilogue
+// forms h = silu(gate) * up of one 128-column block and quantises it.
+template <int NT, bool GATEUP>
+__global__ void __launch_bounds__(Geo<NT>::threads, 1)
+    fp8_gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_w,
+                    const __grid_constant__ CUtensorMap map_w2, const GemmArgs a) {
+  using G = Geo<NT>;
+  static_assert(!GATEUP || NT == 256, "gate/up tile");
+  extern __shared__ uint8_t smraw[];
+  uint8_t* sm = tc::align1024(smraw);
+  const Bars b = bars_at<NT>(sm + G::off_ctrl);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    tc::tma_prefetch_desc(&map_x);
+    tc::tma_prefetch_desc(&map_w);
+    if (GATEUP) tc::tma_prefetch_desc(&map_w2);
+    for (int s = 0; s < G::stages; ++s) {
+      tc::bar_init(&b.full[s], 1);
+      tc::bar_init(&b.empty[s], 1);
+    }
+    for (int s = 0; s < G::bufs; ++s) {
+      tc::bar_init(&b.acc_full[s], 1);
+      tc::bar_init(&b.acc_empty[s], G::promo);
+    }
+    *b.abort = 0;
+    tc::bar_init_fence();
+  }
+  if (warp == 1) tc::tmem_alloc(b.tmem_slot, G::tmem_cols);
+  tc::tc_fence_before();
+  __syncthreads();
+  tc::tc_fence_after();
+  const uint32_t tmem = *b.tmem_slot;
+  griddep_wait();
+  griddep_launch_dependents();
+
+  const int S = a.splits;
+  const int rank = S > 1 ? (int)cluster_rank() : 0;
+  const int kb0 = a.nb * rank / S, kb1 = a.nb * (rank + 1) / S;
+  const int first = (int)blockIdx.x / S, stride = (int)gridDim.x / S;
+  constexpr int kN = GATEUP ? 128 : NT;  // output columns per tile
+
+  if (warp == 0) {
+    int g = 0;
+    bool ok = true;
+    for (int tile = first; tile < a.tiles && ok; tile += stride) {
+      const int m0 = (tile % a.mt) * BM, n0 = (tile / a.mt) * kN;
+      for (int kb = kb0; kb < kb1; ++kb, ++g) {
+        const int s = g % G::stages;
+        if (g >= G::stages && !tc::bar_wait_warp(&b.empty[s], ((g / G::stages) - 1) & 1)) {
+          if (lane == 0) abort_block(b, a.flags);
+          ok = false;
+          break;
+        }
+        if (__any_sync(0xffffffffu, is_aborted(b))) {
+          ok = false;
+          break;
+        }
+        if (tc::elect_one()) {
+          uint8_t* st = sm + (size_t)s * G::stage;
+          tc::bar_expect_tx(&b.full[s], a.a_bytes + NT * BK);
+          tc::tma_load_2d(st, &map_x, kb * BK, m0, &b.full[s]);
+          tc::tma_load_2d(st + kABytes, &map_w, kb * BK, n0, &b.full[s]);
+          if (GATEUP) tc::tma_load_2d(st + kABytes + 128 * BK, &map_w2, kb * BK, n0, &b.full[s]);
+        }
+        __syncwarp();
+      }
+    }
+    if (!ok && lane == 0)  // loads still in flight land before the block leaves (bounded)
+      for (int i = g > G::stages ? g - G::stages : 0; i < g; ++i)
+        tc::bar_wait(&b.full[i % G::stages], (i / G::stages) & 1);
+  } else if (warp == 1) {
+    constexpr uint32_t idesc = tc::idesc_f16(BM, NT);
+    int g = 0;
+    bool ok = true;
+    for (int tile = first; tile < a.tiles && ok; tile += stride) {
+      for (int kb = kb0; kb < kb1; ++kb, ++g) {
+        const int s = g % G::stages, u = g % G::bufs;
+        if ((g >= G::bufs && !tc::bar_wait_warp(&b.acc_empty[u], ((g / G::bufs) - 1) & 1)) ||
+            !tc::bar_wait_warp(&b.full[s], (g / G::stages) & 1)) {
+          if (lane == 0) abort_block(b, a.flags);
+          ok = false;
+          break;
+        }
+        tc::tc_fence_after();
+        const uint32_t base = tc::smem_addr(sm + (size_t)s * G::stage);
+        const uint64_t ad = tc::sw128_desc(base), bd = tc::sw128_desc(base + kABytes);
+        if (tc::elect_one()) {
+#pragma unroll
+          for (int kk = 0; kk < BK / 32; ++kk)
+            tc::mma_f8(tmem + (uint32_t)(u * NT), ad + 2 * kk, bd + 2 * kk, idesc, kk > 0);
+          tc::mma_commit(&b.empty[s]);
+          tc::mma_commit(&b.acc_full[u]);
+        }
+        __syncwarp();
+      }
+    }
+  } else {
+    // Promotion warp: lane quarter q4, columns [c0, c0 + cols) (gate/up: 32
+    // gate columns and the same 32 of up).
+    const int q4 = warp & 3, j4 = (warp - 2) >> 2;
+    const uint32_t tl = tmem + ((uint32_t)(32 * q4) << 16);
+    const uint32_t ca = GATEUP ? 32 * j4 : G::cols * j4, cb = GATEUP ? 128 + 32 * j4 : ca + 32;
+    constexpr int kPairs = G::cols / 2;
+    int g = 0;
+    bool ok = true;
+    for (int tile = first; tile < a.tiles; tile += stride) {
+      const int m0 = (tile % a.mt) * BM, n0 = (tile / a.mt) * kN;
+      const int r = 32 * q4 + lane, row = m0 + r;
+      // Scales: one per token and step, one (gate/up: two) per weight block and step.
+      const bool live = row < a.T;
+      const float* px = a.xs + (size_t)(live ? row : 0) * a.nb;
+      const int wb = (GATEUP ? n0 : n0 + (int)ca) / 128;
+      const bool wlive = wb * 128 < a.N;
+      const float* pw = a.ws + (size_t)(wlive ? wb : 0) * a.nb;
+      const float* pw2 = GATEUP ? a.ws2 + (size_t)wb * a.nb : pw;
+      uint64_t sum[kPairs];
+#pragma unroll
+      for (int i = 0; i < kPairs; ++i) sum[i] = 0;
+      float x0 = live ? px[kb0] : 0.0f, w0 = wlive ? pw[kb0] : 0.0f, u0 = GATEUP ? pw2[kb0] : 0.0f;
+      for (int kb = kb0; kb < kb1; ++kb, ++g) {
+        const int u = g % G::bufs;
+        const float sa = x0 * w0, sb = GATEUP ? x0 * u0 : sa;
+        if (kb + 1 < kb1) {  // the next step's scales load while this one is waited for
+          x0 = live ? px[kb + 1] : 0.0f;
+          w0 = wlive ? pw[kb + 1] : 0.0f;
+          if (GATEUP) u0 = pw2[kb + 1];
+        }
+        if (!tc::bar_wait_warp(&b.acc_full[u], (g / G::bufs) & 1)) {
+          if (lane == 0) abort_block(b, a.flags);
+          ok = false;
+          break;
+        }
+        tc::tc_fence_after();
+        const uint32_t buf = tl + (uint32_t)(u * NT);
+        const uint64_t sa2 = pack2(sa, sa), sb2 = GATEUP ? pack2(sb, sb) : sa2;
+        uint32_t d[32];
+        tc::tmem_ld32(buf + ca, d);
+        tc::tmem_ld32_wait(d);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) fma2(sum[i], d[2 * i], d[2 * i + 1], sa2);
+        if (G::cols == 64) {
+          tc::tmem_ld32(buf + cb, d);
+          tc::tmem_ld32_wait(d);
+        }
+        tc::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) tc::bar_arrive(&b.acc_empty[u]);
+        if (G::cols == 64) {
+#pragma unroll
+          for (int i = 0; i < 16; ++i) fma2(sum[(16 + i) % kPairs], d[2 * i], d[2 * i + 1], sb2);
+        }
+      }
+      if (S > 1) {  // partial tile to shared memory (every stage has been consumed)
+        if (live && ok) {
+          float* red = reinterpret_cast<float*>(sm) + (size_t)r * G::red_pitch;
+#pragma unroll
+          for (int i = 0; i < kPairs; i += 2) {
+            const float2 p = unpack2(sum[i]), q = unpack2(sum[i + 1]);
+            *reinterpret_cast<float4*>(red + (i < 16 ? ca + 2 * i : cb + 2 * (i - 16))) =
+                make_float4(p.x, p.y, q.x, q.y);
+          }
+        }
+        break;
+      }
+      if (!GATEUP) {
+        if (!ok) break;
+        if (live) {
+          __half* out = a.y + (size_t)row * a.N + n0 + ca;
+          const int left = a.N - (n0 + (int)ca);
+          if (a.N % 8 == 0) {
+#pragma unroll
+            for (int i = 0; i < kPairs; i += 4) {
+              uint32_t h[4];
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const float2 p = unpack2(sum[i + e]);
+                h[e] = half2_bits(p.x, p.y);
+              }
+              if (2 * i < left) *reinterpret_cast<uint4*>(out + 2 * i) = make_uint4(h[0], h[1], h[2], h[3]);
+            }
+          } else {
+#pragma unroll
+            for (int i = 0; i < kPairs; ++i) {
+              const float2 p = unpack2(sum[i]);
+              if (2 * i < left) out[2 * i] = __float2half_rn(p.x);
+              if (2 * i + 1 < left) out[2 * i + 1] = __float2half_rn(p.y);
+            }
+          }
+        }
+      } else {
+        // h of 32 columns per thread; the block's amax over its four warps.
+        float h[32], up[32];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const float2 p = unpack2(sum[i]), q = unpack2(sum[(16 + i) % kPairs]);
+          h[2 * i] = p.x; h[2 * i + 1] = p.y;
+          up[2 * i] = q.x; up[2 * i + 1] = q.y;
+        }
+        float m = swiglu(h, up);
+        b.amax[j4 * BM + r] = m;
+        asm volatile("barrier.sync 1, %0;" ::"n"(32 * G::promo) : "memory");
+#pragma unroll
+        for (int w = 0; w < 4; ++w) m = fmaxf(m, b.amax[w * BM + r]);
+        // Maxima read before the next tile's; one verdict for all the warps.
+        if (promo_any<32 * G::promo>(!ok || is_aborted(b))) break;
+        const fp8::BlockScale bs = fp8::block_scale(m);
+        if (live) {
+          uint8_t* out = a.hq + (size_t)row * a.N + n0 + ca;
+#pragma unroll
+          for (int i = 0; i < 32; i += 16) {
+            uint32_t c[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              c[e] = fp8::encode4(h[i + 4 * e] * bs.inv, h[i + 4 * e + 1] * bs.inv, h[i + 4 * e + 2] * bs.inv,
+                                  h[i + 4 * e + 3] * bs.inv);
+            if (n0 + (int)ca + i < a.N) *reinterpret_cast<uint4*>(out + i) = make_uint4(c[0], c[1], c[2], c[3]);
+          }
+          if (j4 == 0) a.hs[(size_t)row * a.nbh + n0 / 128] = bs.scale;
+        }
+      }
     }
   }
-  if (bad) m = INFINITY;
+  if (S > 1) {
+    // The cluster's partial tiles, added in rank order (the same order every
+    // time), each block finishing its share of the tile.
+    __syncwarp();
+    cluster_sync();
+    const int m0 = (first % a.mt) * BM, n0 = (first / a.mt) * kN;
+    const int rows = min(BM, a.T - m0);
+    const uint32_t red = tc::smem_addr(sm);
+    if (!GATEUP) {
+      constexpr int kQ = NT / 4;  // 4-column pieces per row
+      for (int i = rank * G::threads + (int)threadIdx.x; i < rows * kQ; i += S * G::threads) {
+        const int r = i / kQ, c = (i % kQ) * 4;
+        float4 t = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        for (int p = 0; p < S; ++p) {
+          const float4 v = ld_cluster(red + (uint32_t)(r * G::red_pitch + c) * 4, (uint32_t)p);
+          t.x += v.x; t.y += v.y; t.z += v.z; t.w += v.w;
+        }
+        __half* out = a.y + (size_t)(m0 + r) * a.N + n0 + c;
+        const int left = a.N - (n0 + c);
+        if (a.N % 4 == 0) {
+          if (left > 0) *reinterpret_cast<uint2*>(out) = make_uint2(half2_bits(t.x, t.y), half2_bits(t.z, t.w));
+        } else {
+          const float v[4] = {t.x, t.y, t.z, t.w};
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-  const fp8::BlockScale b = fp8::block_scale(m);
-  if (c0 < cols)
-    *reinterpret_cast<uint32_t*>(q + (size_t)r * cols + c0) =
-        fp8::encode4(h[0] * b.inv, h[1] * b.inv, h[2] * b.inv, h[3] * b.inv);
-  if (lane == 0) scales[u] = b.scale;
+          for (int e = 0; e < 4; ++e)
+            if (e < left) out[e] = __float2half_rn(v[e]);
+        }
+      }
+    } else {
+      constexpr int kWarps = G::threads / 32;
+      for (int r = rank * kWarps + warp; r < rows; r += S * kWarps) {
+        float h[4] = {}, up[4] = {};
+        for (int p = 0; p < S; ++p) {
+          const float4 v = ld_cluster(red + (uint32_t)(r * G::red_pitch + 4 * lane) * 4, (uint32_t)p);
+          const float4 w = ld_cluster(red + (uint32_t)(r * G::red_pitch + 128 + 4 * lane) * 4, (uint32_t)p);
+          h[0] += v.x; h[1] += v.y; h[2] += v.z; h[3] += v.w;
+          up[0] += w.x; up[1] += w.y; up[2] += w.z; up[3] += w.w;
+        }
+        float m = swiglu(h, up);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+        const fp8::BlockScale bs = fp8::block_scale(m);
+        if (n0 + 4 * lane < a.N)
+          *reinterpret_cast<uint32_t*>(a.hq + (size_t)(m0 + r) * a.N + n0 + 4 * lane) =
+              fp8::encode4(h[0] * bs.inv, h[1] * bs.inv, h[2] * bs.inv, h[3] * bs.inv);
+        if (lane == 0) a.hs[(size_t)(m0 + r) * a.nbh + n0 / 128] = bs.scale;
+      }
+    }
+    __syncwarp();
+    cluster_sync();  // nobody leaves while its partial tile is read
+  }
+  tc::gemm_teardown(tmem, G::tmem_cols);
 }
 
 inline size_t round256(size_t b) { return (b + 255) / 256 * 256; }
 inline int blocks128(int n) { return (n + 127) / 128; }
 
-int launch_matmul(const uint8_t* xq, const float* xs, int T, const uint8_t* wq, const float* ws, int N, int K, void* y,
-                  bool f32, cudaStream_t st) {
-  const dim3 grid((N + kTile - 1) / kTile, (T + kTile - 1) / kTile);
-  if (f32) fp8_matmul_kernel<true><<<grid, 256, 0, st>>>(xq, xs, T, wq, ws, N, K, y);
-  else fp8_matmul_kernel<false><<<grid, 256, 0, st>>>(xq, xs, T, wq, ws, N, K, y);
-  return check_launch("fp8 matmul");
+int code_map(CUtensorMap* m, const void* base, int K, int rows, int box_rows) {
+  const uint64_t dims[2] = {(uint64_t)K, (uint64_t)rows};
+  const uint64_t str[1] = {(uint64_t)K};
+  const uint32_t box[2] = {BK, (uint32_t)box_rows};
+  return encode_tensor_map(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, base, dims, str, box, CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
-// Workspace of the FFN after the header: xq, xs, hq, hs, gate, up.
+// Tile width and cluster split of a product.
+struct Plan {
+  int nt, splits;
+};
+Plan plan_of(int T, int N, int nb, int sms, bool gateup) {
+  const int mt = (T + BM - 1) / BM;
+  Plan p = {256, 1};
+  if (gateup) {
+    const int tiles = mt * blocks128(N);
+    while (p.splits < kMaxSplits && p.splits * 2 <= nb && tiles * p.splits * 2 <= sms) p.splits *= 2;
+    return p;
+  }
+  // The widest tile that still fills the SMs, then split K while they are not.
+  while (p.nt > 32 && mt * ((N + p.nt - 1) / p.nt) < sms / 2) p.nt /= 2;
+  const int tiles = mt * ((N + p.nt - 1) / p.nt);
+  while (p.splits < kMaxSplits && p.splits * 4 <= nb && tiles * p.splits * 2 <= sms) p.splits *= 2;
+  return p;
+}
+
+struct Operand {
+  const uint8_t* q;
+  const float* s;
+};
+
+template <int NT, bool GATEUP>
+int launch_gemm(GemmArgs a, const Operand& x, const Operand& w, const Operand* w2, int splits, int sms, int dev,
+                cudaStream_t st) {
+  using G = Geo<NT>;
+  {
+    static std::mutex mu;
+    static bool set[kMaxDevices] = {};
+    std::lock_guard<std::mutex> lock(mu);
+    if (!set[dev]) {
+      MOE_CUDA_TRY(cudaFuncSetAttribute(fp8_gemm_kernel<NT, GATEUP>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                        (int)G::smem));
+      set[dev] = true;
+    }
+  }
+  int box = 8;  // rows of the token box: the batch's, rounded up
+  while (box < BM && box < a.T) box *= 2;
+  const int kn = GATEUP ? 128 : NT;
+  a.a_bytes = (uint32_t)box * BK;
+  a.xs = x.s;
+  a.ws = w.s;
+  a.ws2 = w2 ? w2->s : nullptr;
+  a.nb = blocks128(a.K);
+  a.mt = (a.T + BM - 1) / BM;
+  a.tiles = a.mt * ((a.N + kn - 1) / kn);
+  a.splits = splits;
+  CUtensorMap mx, mw, mw2;
+  int rc;
+  if ((rc = code_map(&mx, x.q, a.K, a.T, box)) != MOE_OK) return rc;
+  if ((rc = code_map(&mw, w.q, a.K, a.N, kn)) != MOE_OK) return rc;
+  mw2 = mw;
+  if (w2 && (rc = code_map(&mw2, w2->q, a.K, a.N, kn)) != MOE_OK) return rc;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(splits > 1 ? a.tiles * splits : std::min(a.tiles, sms)));
+  cfg.blockDim = dim3(G::threads);
+  cfg.dynamicSmemBytes = G::smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (splits > 1) {
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = (unsigned)splits;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.numAttrs = 2;
+  }
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, fp8_gemm_kernel<NT, GATEUP>, mx, mw, mw2, a);
+  if (e != cudaSuccess) return fail(MOE_ERR_CUDA, "fp8 product launch: %s", cudaGetErrorString(e));
+  return MOE_OK;
+}
+
+int product(const Operand& x, const Operand& w, int T, int N, int K, __half* y, int32_t* flags, cudaStream_t st) {
+  int dev = 0, sms = 0;
+  const int rc = current_device_sms(&dev, &sms);
+  if (rc != MOE_OK) return rc;
+  GemmArgs a = {};
+  a.T = T; a.N = N; a.K = K;
+  a.y = y;
+  a.flags = flags;
+  const Plan p = plan_of(T, N, blocks128(K), sms, false);
+  switch (p.nt) {
+    case 256: return launch_gemm<256, false>(a, x, w, nullptr, p.splits, sms, dev, st);
+    case 128: return launch_gemm<128, false>(a, x, w, nullptr, p.splits, sms, dev, st);
+    case 64: return launch_gemm<64, false>(a, x, w, nullptr, p.splits, sms, dev, st);
+    default: return launch_gemm<32, false>(a, x, w, nullptr, p.splits, sms, dev, st);
+  }
+}
+
+int gate_up(const Operand& x, const Operand& wg, const Operand& wu, int T, int Is, int H, uint8_t* hq, float* hs,
+            int32_t* flags, cudaStream_t st) {
+  int dev = 0, sms = 0;
+  const int rc = current_device_sms(&dev, &sms);
+  if (rc != MOE_OK) return rc;
+  GemmArgs a = {};
+  a.T = T; a.N = Is; a.K = H;
+  a.hq = hq; a.hs = hs;
+  a.nbh = blocks128(Is);
+  a.flags = flags;
+  const Plan p = plan_of(T, Is, blocks128(H), sms, true);
+  return launch_gemm<256, true>(a, x, wg, &wu, p.splits, sms, dev, st);
+}
+
+// Workspace of the FFN after the header: x and h as codes and scales.
 struct FfnWs {
-  size_t xq, xs, hq, hs, gate, up, total;
+  size_t xq, xs, hq, hs, total;
 };
 FfnWs ffn_ws(int T, int H, int Is) {
   FfnWs w;
@@ -122,8 +555,6 @@ FfnWs ffn_ws(int T, int H, int Is) {
   w.xs = o; o += round256((size_t)T * blocks128(H) * 4);
   w.hq = o; o += round256((size_t)T * Is);
   w.hs = o; o += round256((size_t)T * blocks128(Is) * 4);
-  w.gate = o; o += round256((size_t)T * Is * 4);
-  w.up = o; o += round256((size_t)T * Is * 4);
   w.total = o;
   return w;
 }
@@ -154,8 +585,8 @@ int moe_matmul_fp8(const void* xq, const float* xs, int T, const void* wq, const
   const size_t need = moe_matmul_fp8_workspace_bytes(T, N, K);
   if (workspace_bytes < need)
     return moe::fail(MOE_ERR_CAPACITY, "moe_matmul_fp8: workspace %zu < %zu bytes", workspace_bytes, need);
-  return moe::launch_matmul(static_cast<const uint8_t*>(xq), xs, T, static_cast<const uint8_t*>(wq), ws, N, K, y,
-                            false, static_cast<cudaStream_t>(stream));
+  return moe::product({static_cast<const uint8_t*>(xq), xs}, {static_cast<const uint8_t*>(wq), ws}, T, N, K,
+                      static_cast<__half*>(y), static_cast<int32_t*>(workspace), static_cast<cudaStream_t>(stream));
 }
 
 size_t moe_shared_fp8_workspace_bytes(int T, int H, int Is) {
@@ -187,18 +618,16 @@ int moe_shared_forward_fp8(const void* x, int T, int H, int Is, const void* wg, 
     return moe::fail(MOE_ERR_CAPACITY, "moe_shared_forward_fp8: workspace %zu < %zu bytes", workspace_bytes, need);
   const moe::FfnWs o = moe::ffn_ws(T, H, Is);
   uint8_t* w8 = static_cast<uint8_t*>(workspace);
+  int32_t* flags = reinterpret_cast<int32_t*>(w8);
   uint8_t *xq = w8 + o.xq, *hq = w8 + o.hq;
   float *xs = reinterpret_cast<float*>(w8 + o.xs), *hs = reinterpret_cast<float*>(w8 + o.hs);
-  float *gate = reinterpret_cast<float*>(w8 + o.gate), *up = reinterpret_cast<float*>(w8 + o.up);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const moe::Operand g = {static_cast<const uint8_t*>(wg), sg}, u = {static_cast<const uint8_t*>(wu), su},
+                     d = {static_cast<const uint8_t*>(wd), sd};
   int rc = moe::launch_quantize_fp8(static_cast<const __half*>(x), T, H, 1, xq, xs, st);
   if (rc != MOE_OK) return rc;
-  if ((rc = moe::launch_matmul(xq, xs, T, static_cast<const uint8_t*>(wg), sg, Is, H, gate, true, st))) return rc;
-  if ((rc = moe::launch_matmul(xq, xs, T, static_cast<const uint8_t*>(wu), su, Is, H, up, true, st))) return rc;
-  const unsigned units = (unsigned)T * (unsigned)moe::blocks128(Is);
-  moe::swiglu_quantize_kernel<<<(units + 7) / 8, 256, 0, st>>>(gate, up, units, Is, moe::blocks128(Is), hq, hs);
-  if ((rc = moe::check_launch("swiglu quantize"))) return rc;
-  return moe::launch_matmul(hq, hs, T, static_cast<const uint8_t*>(wd), sd, H, Is, y, false, st);
+  if ((rc = moe::gate_up({xq, xs}, g, u, T, Is, H, hq, hs, flags, st)) != MOE_OK) return rc;
+  return moe::product({hq, hs}, d, T, H, Is, static_cast<__half*>(y), flags, st);
 }
 
 }  // extern "C"
