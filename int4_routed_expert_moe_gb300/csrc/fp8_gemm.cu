@@ -427,6 +427,334 @@ __global__ void __launch_bounds__(Geo<NT>::threads, 1)
   tc::gemm_teardown(tmem, G::tmem_cols);
 }
 
+// ---- SM pairs: 256 tokens by 256 rows of W ----------------------------------
+// Two blocks of a cluster run one tile with cta_group::2 MMAs: each holds its
+// 128 tokens (A) and half of the weight rows (B), and each accumulates its
+// tokens against all 256 rows. Against a block on its own with a 128 x 256
+// tile, a step's shared-memory traffic (TMA writes and MMA reads) falls from
+// 96 KB to 64 KB per SM in the 512 cycles its MMAs take.
+// Warps: 0 TMA, 1 tensor memory and (in the leading block) MMA issue, 2-3
+// scales, 4-19 promotion (a lane quarter, 64 columns each).
+struct Pair {
+  static constexpr int promo = 16, threads = 640;
+  static constexpr int stages = 4, bufs = 2, slots = 8;
+  static constexpr uint32_t stage = kABytes + 128 * BK;  // per block: 128 tokens, 128 rows of W
+  static constexpr uint32_t off_out = stages * stage;    // [promo][32 rows][64 columns] FP16
+  static constexpr uint32_t off_scale = off_out + promo * 4096;
+  static constexpr uint32_t off_ctrl = off_scale + slots * 2 * BM * 4;
+  static constexpr size_t smem = (size_t)off_ctrl + 4096 + 1024;
+};
+struct PairBars {
+  uint64_t *full, *empty, *acc_full, *acc_empty, *sc_full, *sc_empty;
+  uint32_t* tmem_slot;
+  int* abort;
+  float* amax;
+};
+__device__ __forceinline__ PairBars pair_bars(uint8_t* p) {
+  PairBars b;
+  uint64_t* q = reinterpret_cast<uint64_t*>(p);
+  b.full = q; q += Pair::stages;
+  b.empty = q; q += Pair::stages;
+  b.acc_full = q; q += Pair::bufs;
+  b.acc_empty = q; q += Pair::bufs;
+  b.sc_full = q; q += Pair::slots;
+  b.sc_empty = q; q += Pair::slots;
+  b.tmem_slot = reinterpret_cast<uint32_t*>(q);
+  b.abort = reinterpret_cast<int*>(b.tmem_slot + 1);
+  b.amax = reinterpret_cast<float*>(p + 1024);
+  return b;
+}
+__device__ __forceinline__ void pair_abort(const PairBars& b, int32_t* flags) {
+  atomicOr(flags, 4);
+  *reinterpret_cast<volatile int*>(b.abort) = 1;
+}
+
+template <bool GATEUP>
+__global__ void __launch_bounds__(Pair::threads, 1)
+    fp8_pair_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_w,
+                    const __grid_constant__ CUtensorMap map_w2, const __grid_constant__ CUtensorMap map_y,
+                    const GemmArgs a) {
+  using G = Pair;
+  extern __shared__ uint8_t smraw[];
+  uint8_t* sm = tc::align1024(smraw);
+  const PairBars b = pair_bars(sm + G::off_ctrl);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = (int)cluster_rank();
+  if (threadIdx.x == 0) {
+    tc::tma_prefetch_desc(&map_x);
+    tc::tma_prefetch_desc(rank && GATEUP ? &map_w2 : &map_w);
+    if (!GATEUP) tc::tma_prefetch_desc(&map_y);
+    for (int s = 0; s < G::stages; ++s) {
+      tc::bar_init(&b.full[s], 1);
+      tc::bar_init(&b.empty[s], 1);
+    }
+    for (int s = 0; s < G::bufs; ++s) {
+      tc::bar_init(&b.acc_full[s], 1);
+      tc::bar_init(&b.acc_empty[s], 2 * G::promo);
+    }
+    for (int s = 0; s < G::slots; ++s) {
+      tc::bar_init(&b.sc_full[s], 2);
+      tc::bar_init(&b.sc_empty[s], G::promo);
+    }
+    *reinterpret_cast<volatile int*>(b.abort) = 0;
+    tc::bar_init_fence();
+  }
+  if (warp == 1) tc::tmem_alloc2(b.tmem_slot, 512);
+  tc::tc_fence_before();
+  __syncthreads();
+  cluster_sync();
+  tc::tc_fence_after();
+  const uint32_t tmem = *b.tmem_slot;
+  griddep_wait();
+  griddep_launch_dependents();
+
+  const int nb = a.nb;
+  const int first = (int)blockIdx.x / 2, stride = (int)gridDim.x / 2;
+  constexpr int kN = GATEUP ? 128 : 256;  // output columns per tile
+
+  if (warp == 0) {
+    // Both blocks' loads complete on the leading block's barrier.
+    const CUtensorMap* mw = GATEUP && rank ? &map_w2 : &map_w;
+    int g = 0;
+    bool ok = true;
+    for (int tile = first; tile < a.tiles && ok; tile += stride) {
+      const int m0 = (tile % a.mt) * 256 + rank * BM, n0 = (tile / a.mt) * kN + (GATEUP ? 0 : rank * 128);
+      for (int kb = 0; kb < nb; ++kb, ++g) {
+        const int s = g % G::stages;
+        if (g >= G::stages && !tc::bar_wait_warp(&b.empty[s], ((g / G::stages) - 1) & 1)) {
+          if (lane == 0) pair_abort(b, a.flags);
+          ok = false;
+          break;
+        }
+        if (tc::elect_one()) {
+          uint8_t* st = sm + (size_t)s * G::stage;
+          const uint32_t full = tc::map_rank(tc::smem_addr(&b.full[s]), 0);
+          if (rank == 0) tc::bar_expect_tx(&b.full[s], 2 * G::stage);
+          tc::tma_load_2d_pair(st, &map_x, kb * BK, m0, full);
+          tc::tma_load_2d_pair(st + kABytes, mw, kb * BK, n0, full);
+        }
+        __syncwarp();
+      }
+    }
+    // After a wait that ran out, the loads still in flight land before the
+    // block leaves: 2 ms, since no barrier of this block counts them.
+    if (!ok) {
+      const uint64_t t0 = tc::global_ns();
+      for (int i = 0; i < 1000000 && tc::global_ns() - t0 < 2000000ull; ++i) {
+      }
+    }
+  } else if (warp == 1) {
+    if (rank == 0) {
+      constexpr uint32_t idesc = tc::idesc_f16(256, 256);
+      int g = 0;
+      bool ok = true;
+      for (int tile = first; tile < a.tiles && ok; tile += stride) {
+        for (int kb = 0; kb < nb; ++kb, ++g) {
+          const int s = g % G::stages, u = g % G::bufs;
+          if ((g >= G::bufs && !tc::bar_wait_warp(&b.acc_empty[u], ((g / G::bufs) - 1) & 1)) ||
+              !tc::bar_wait_warp(&b.full[s], (g / G::stages) & 1)) {
+            if (lane == 0) pair_abort(b, a.flags);
+            ok = false;
+            break;
+          }
+          tc::tc_fence_after();
+          const uint32_t base = tc::smem_addr(sm + (size_t)s * G::stage);
+          const uint64_t ad = tc::sw128_desc(base), bd = tc::sw128_desc(base + kABytes);
+          if (tc::elect_one()) {
+#pragma unroll
+            for (int kk = 0; kk < BK / 32; ++kk)
+              tc::mma_f8_pair(tmem + (uint32_t)(u * 256), ad + 2 * kk, bd + 2 * kk, idesc, kk > 0);
+            tc::mma_commit_pair(&b.empty[s]);
+            tc::mma_commit_pair(&b.acc_full[u]);
+          }
+          __syncwarp();
+        }
+      }
+    }
+  } else if (warp < 4) {
+    // Scales: the products xs * ws of a step, [2 weight blocks][128 tokens],
+    // four steps of two tokens per lane loaded at a time, one group ahead.
+    const int r0 = (warp - 2) * 64 + lane;
+    const bool vec = (nb & 3) == 0 && (reinterpret_cast<uintptr_t>(a.xs) & 15) == 0;
+    float* sc = reinterpret_cast<float*>(sm + G::off_scale);
+    int g = 0;
+    bool ok = true;
+    for (int tile = first; tile < a.tiles && ok; tile += stride) {
+      const int m0 = (tile % a.mt) * 256 + rank * BM, n0 = (tile / a.mt) * kN;
+      const int wb = n0 / 128;
+      const float* pw0 = a.ws + (size_t)wb * nb;
+      const float* pw1 = GATEUP ? a.ws2 + (size_t)wb * nb : (n0 + 128 < a.N ? pw0 + nb : nullptr);
+      const float* px[2];
+      bool live[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        live[i] = m0 + r0 + 32 * i < a.T;
+        px[i] = a.xs + (size_t)(live[i] ? m0 + r0 + 32 * i : 0) * nb;
+      }
+      float x[2][4], w0[4], w1[4];
+      auto load = [&](int kb) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          if (vec && live[i]) {
+            const float4 v = *reinterpret_cast<const float4*>(px[i] + kb);
+            x[i][0] = v.x; x[i][1] = v.y; x[i][2] = v.z; x[i][3] = v.w;
+          } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) x[i][e] = live[i] && kb + e < nb ? px[i][kb + e] : 0.0f;
+          }
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          w0[e] = kb + e < nb ? pw0[kb + e] : 0.0f;
+          w1[e] = pw1 && kb + e < nb ? pw1[kb + e] : 0.0f;
+        }
+      };
+      load(0);
+      for (int kb = 0; kb < nb && ok; kb += 4) {
+        float p[4][2][2];
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            p[e][0][i] = x[i][e] * w0[e];
+            p[e][1][i] = x[i][e] * w1[e];
+          }
+        if (kb + 4 < nb) load(kb + 4);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          if (kb + e >= nb) break;
+          const int s = g % G::slots;
+          if (g >= G::slots && !tc::bar_wait_warp(&b.sc_empty[s], ((g / G::slots) - 1) & 1)) {
+            if (lane == 0) pair_abort(b, a.flags);
+            ok = false;
+            break;
+          }
+          float* d = sc + s * 2 * BM + r0;
+          d[0] = p[e][0][0];
+          d[32] = p[e][0][1];
+          d[BM] = p[e][1][0];
+          d[BM + 32] = p[e][1][1];
+          __syncwarp();
+          if (lane == 0) tc::bar_arrive(&b.sc_full[s]);
+          ++g;
+        }
+      }
+    }
+  } else {
+    const int q4 = warp & 3, j4 = (warp - 4) >> 2;
+    const uint32_t tl = tmem + ((uint32_t)(32 * q4) << 16);
+    const uint32_t ca = GATEUP ? 32 * j4 : 64 * j4, cb = GATEUP ? 128 + 32 * j4 : ca + 32;
+    const float* sca = reinterpret_cast<const float*>(sm + G::off_scale) + (GATEUP ? 0 : (j4 >> 1) * BM) + 32 * q4 + lane;
+    const uint32_t acc_empty0 = tc::map_rank(tc::smem_addr(&b.acc_empty[0]), 0);
+    uint8_t* out = sm + G::off_out + (warp - 4) * 4096;
+    int g = 0;
+    bool ok = true;
+    for (int tile = first; tile < a.tiles; tile += stride) {
+      const int m0 = (tile % a.mt) * 256 + rank * BM, n0 = (tile / a.mt) * kN;
+      const int r = 32 * q4 + lane, row = m0 + r;
+      uint64_t sum[32];
+#pragma unroll
+      for (int i = 0; i < 32; ++i) sum[i] = 0;
+      for (int kb = 0; kb < nb; ++kb, ++g) {
+        const int u = g % G::bufs, s = g % G::slots;
+        if (!tc::bar_wait_warp(&b.sc_full[s], (g / G::slots) & 1)) {
+          ok = false;
+          break;
+        }
+        const float sa = sca[s * 2 * BM], sb = GATEUP ? sca[s * 2 * BM + BM] : sa;
+        if (!tc::bar_wait_warp(&b.acc_full[u], (g / G::bufs) & 1)) {
+          ok = false;
+          break;
+        }
+        tc::tc_fence_after();
+        const uint32_t buf = tl + (uint32_t)(u * 256);
+        uint32_t d[32];
+        tc::tmem_ld32(buf + ca, d);
+        if (lane == 0) tc::bar_arrive(&b.sc_empty[s]);
+        tc::tmem_ld32_wait(d);
+        const uint64_t sa2 = pack2(sa, sa);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) fma2(sum[i], d[2 * i], d[2 * i + 1], sa2);
+        tc::tmem_ld32(buf + cb, d);
+        tc::tmem_ld32_wait(d);
+        tc::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) tc::bar_arrive_cluster(acc_empty0 + 8 * u);
+        const uint64_t sb2 = GATEUP ? pack2(sb, sb) : sa2;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) fma2(sum[16 + i], d[2 * i], d[2 * i + 1], sb2);
+      }
+      if (!ok && lane == 0) pair_abort(b, a.flags);
+      if (!GATEUP) {
+        if (!ok) break;
+        if (a.N % 8 == 0) {
+          // Rows of 64 FP16 columns in the 128-byte swizzle, stored by TMA.
+          if (lane == 0) tc::tma_store_wait_read();
+          __syncwarp();
+#pragma unroll
+          for (int c = 0; c < 8; ++c) {
+            uint32_t h[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const float2 p = unpack2(sum[4 * c + e]);
+              h[e] = half2_bits(p.x, p.y);
+            }
+            *reinterpret_cast<uint4*>(out + tc::sw128_offset(lane, c)) = make_uint4(h[0], h[1], h[2], h[3]);
+          }
+          tc::fence_async_smem();
+          __syncwarp();
+          const int y0 = m0 + 32 * q4, x0 = n0 + (int)ca;
+          if (lane == 0 && y0 < a.T && x0 < a.N) tc::tma_store_2d(&map_y, x0, y0, out);
+        } else if (row < a.T) {
+          __half* o = a.y + (size_t)row * a.N + n0 + ca;
+          const int left = a.N - (n0 + (int)ca);
+#pragma unroll
+          for (int i = 0; i < 32; ++i) {
+            const float2 p = unpack2(sum[i]);
+            if (2 * i < left) o[2 * i] = __float2half_rn(p.x);
+            if (2 * i + 1 < left) o[2 * i + 1] = __float2half_rn(p.y);
+          }
+        }
+      } else {
+        float h[32], up[32];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const float2 p = unpack2(sum[i]), q = unpack2(sum[16 + i]);
+          h[2 * i] = p.x; h[2 * i + 1] = p.y;
+          up[2 * i] = q.x; up[2 * i + 1] = q.y;
+        }
+        float m = swiglu(h, up);
+        b.amax[j4 * BM + r] = m;
+        asm volatile("barrier.sync 1, %0;" ::"n"(32 * G::promo) : "memory");
+#pragma unroll
+        for (int w = 0; w < 4; ++w) m = fmaxf(m, b.amax[w * BM + r]);
+        // Maxima read before the next tile's; one verdict for all the warps.
+        if (promo_any<32 * G::promo>(!ok)) break;
+        const fp8::BlockScale bs = fp8::block_scale(m);
+        if (row < a.T) {
+          uint8_t* o = a.hq + (size_t)row * a.N + n0 + ca;
+#pragma unroll
+          for (int i = 0; i < 32; i += 16) {
+            uint32_t c[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              c[e] = fp8::encode4(h[i + 4 * e] * bs.inv, h[i + 4 * e + 1] * bs.inv, h[i + 4 * e + 2] * bs.inv,
+                                  h[i + 4 * e + 3] * bs.inv);
+            if (n0 + (int)ca + i < a.N) *reinterpret_cast<uint4*>(o + i) = make_uint4(c[0], c[1], c[2], c[3]);
+          }
+          if (j4 == 0) a.hs[(size_t)row * a.nbh + n0 / 128] = bs.scale;
+        }
+      }
+    }
+    if (!GATEUP && lane == 0) tc::tma_store_wait_all();
+  }
+  tc::tc_fence_before();
+  __syncwarp();
+  cluster_sync();  // neither block leaves while the other's MMAs, loads or arrivals can reach it
+  tc::tc_fence_after();
+  if (warp == 1) tc::tmem_dealloc2(tmem, 512);
+}
+
 inline size_t round256(size_t b) { return (b + 255) / 256 * 256; }
 inline int blocks128(int n) { return (n + 127) / 128; }
 
@@ -513,6 +841,59 @@ int launch_gemm(GemmArgs a, const Operand& x, const Operand& w, const Operand* w
   return MOE_OK;
 }
 
+// The pair kernel: y or (hq, hs).
+template <bool GATEUP>
+int launch_pair(GemmArgs a, const Operand& x, const Operand& w, const Operand* w2, int sms, int dev, cudaStream_t st) {
+  {
+    static std::mutex mu;
+    static bool set[kMaxDevices] = {};
+    std::lock_guard<std::mutex> lock(mu);
+    if (!set[dev]) {
+      MOE_CUDA_TRY(cudaFuncSetAttribute(fp8_pair_kernel<GATEUP>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                        (int)Pair::smem));
+      set[dev] = true;
+    }
+  }
+  const int kn = GATEUP ? 128 : 256;
+  a.xs = x.s;
+  a.ws = w.s;
+  a.ws2 = w2 ? w2->s : nullptr;
+  a.nb = blocks128(a.K);
+  a.mt = (a.T + 255) / 256;
+  a.tiles = a.mt * ((a.N + kn - 1) / kn);
+  CUtensorMap mx, mw, mw2, my;
+  int rc;
+  if ((rc = code_map(&mx, x.q, a.K, a.T, BM)) != MOE_OK) return rc;
+  if ((rc = code_map(&mw, w.q, a.K, a.N, 128)) != MOE_OK) return rc;
+  mw2 = mw;
+  if (w2 && (rc = code_map(&mw2, w2->q, a.K, a.N, 128)) != MOE_OK) return rc;
+  my = mx;
+  if (!GATEUP && a.N % 8 == 0) {
+    const uint64_t dims[2] = {(uint64_t)a.N, (uint64_t)a.T};
+    const uint64_t str[1] = {(uint64_t)a.N * 2};
+    const uint32_t box[2] = {64, 32};
+    if ((rc = encode_tensor_map(&my, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, a.y, dims, str, box,
+                                CU_TENSOR_MAP_SWIZZLE_128B)) != MOE_OK)
+      return rc;
+  }
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(2 * std::min(a.tiles, sms / 2)));
+  cfg.blockDim = dim3(Pair::threads);
+  cfg.dynamicSmemBytes = Pair::smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = 2;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, fp8_pair_kernel<GATEUP>, mx, mw, mw2, my, a);
+  if (e != cudaSuccess) return fail(MOE_ERR_CUDA, "fp8 product launch: %s", cudaGetErrorString(e));
+  return MOE_OK;
+}
+
 int product(const Operand& x, const Operand& w, int T, int N, int K, __half* y, int32_t* flags, cudaStream_t st) {
   int dev = 0, sms = 0;
   const int rc = current_device_sms(&dev, &sms);
@@ -521,6 +902,7 @@ int product(const Operand& x, const Operand& w, int T, int N, int K, __half* y, 
   a.T = T; a.N = N; a.K = K;
   a.y = y;
   a.flags = flags;
+  if (T > BM && ((T + 255) / 256) * ((N + 255) / 256) >= sms / 4) return launch_pair<false>(a, x, w, nullptr, sms, dev, st);
   const Plan p = plan_of(T, N, blocks128(K), sms, false);
   switch (p.nt) {
     case 256: return launch_gemm<256, false>(a, x, w, nullptr, p.splits, sms, dev, st);
@@ -540,6 +922,7 @@ int gate_up(const Operand& x, const Operand& wg, const Operand& wu, int T, int I
   a.hq = hq; a.hs = hs;
   a.nbh = blocks128(Is);
   a.flags = flags;
+  if (T > BM && ((T + 255) / 256) * blocks128(Is) >= sms / 4) return launch_pair<true>(a, x, wg, &wu, sms, dev, st);
   const Plan p = plan_of(T, Is, blocks128(H), sms, true);
   return launch_gemm<256, true>(a, x, wg, &wu, p.splits, sms, dev, st);
 }
