@@ -434,13 +434,13 @@ __global__ void __launch_bounds__(Geo<NT>::threads, 1)
 // tile, a step's shared-memory traffic (TMA writes and MMA reads) falls from
 // 96 KB to 64 KB per SM in the 512 cycles its MMAs take.
 // Warps: 0 TMA, 1 tensor memory and (in the leading block) MMA issue, 2-3
-// scales, 4-19 promotion (a lane quarter, 64 columns each).
+// scales, 4-11 promotion (a lane quarter, 128 columns each).
 struct Pair {
-  static constexpr int promo = 16, threads = 640;
+  static constexpr int promo = 8, threads = 384;
   static constexpr int stages = 4, bufs = 2, slots = 8;
   static constexpr uint32_t stage = kABytes + 128 * BK;  // per block: 128 tokens, 128 rows of W
-  static constexpr uint32_t off_out = stages * stage;    // [promo][32 rows][64 columns] FP16
-  static constexpr uint32_t off_scale = off_out + promo * 4096;
+  static constexpr uint32_t off_out = stages * stage;    // [promo][2][32 rows][64 columns] FP16
+  static constexpr uint32_t off_scale = off_out + promo * 8192;
   static constexpr uint32_t off_ctrl = off_scale + slots * 2 * BM * 4;
   static constexpr size_t smem = (size_t)off_ctrl + 4096 + 1024;
 };
@@ -512,149 +512,27 @@ __global__ void __launch_bounds__(Pair::threads, 1)
   const int first = (int)blockIdx.x / 2, stride = (int)gridDim.x / 2;
   constexpr int kN = GATEUP ? 128 : 256;  // output columns per tile
 
-  if (warp == 0) {
-    // Both blocks' loads complete on the leading block's barrier.
-    const CUtensorMap* mw = GATEUP && rank ? &map_w2 : &map_w;
-    int g = 0;
-    bool ok = true;
-    for (int tile = first; tile < a.tiles && ok; tile += stride) {
-      const int m0 = (tile % a.mt) * 256 + rank * BM, n0 = (tile / a.mt) * kN + (GATEUP ? 0 : rank * 128);
-      for (int kb = 0; kb < nb; ++kb, ++g) {
-        const int s = g % G::stages;
-        if (g >= G::stages && !tc::bar_wait_warp(&b.empty[s], ((g / G::stages) - 1) & 1)) {
-          if (lane == 0) pair_abort(b, a.flags);
-          ok = false;
-          break;
-        }
-        if (tc::elect_one()) {
-          uint8_t* st = sm + (size_t)s * G::stage;
-          const uint32_t full = tc::map_rank(tc::smem_addr(&b.full[s]), 0);
-          if (rank == 0) tc::bar_expect_tx(&b.full[s], 2 * G::stage);
-          tc::tma_load_2d_pair(st, &map_x, kb * BK, m0, full);
-          tc::tma_load_2d_pair(st + kABytes, mw, kb * BK, n0, full);
-        }
-        __syncwarp();
-      }
-    }
-    // After a wait that ran out, the loads still in flight land before the
-    // block leaves: 2 ms, since no barrier of this block counts them.
-    if (!ok) {
-      const uint64_t t0 = tc::global_ns();
-      for (int i = 0; i < 1000000 && tc::global_ns() - t0 < 2000000ull; ++i) {
-      }
-    }
-  } else if (warp == 1) {
-    if (rank == 0) {
-      constexpr uint32_t idesc = tc::idesc_f16(256, 256);
-      int g = 0;
-      bool ok = true;
-      for (int tile = first; tile < a.tiles && ok; tile += stride) {
-        for (int kb = 0; kb < nb; ++kb, ++g) {
-          const int s = g % G::stages, u = g % G::bufs;
-          if ((g >= G::bufs && !tc::bar_wait_warp(&b.acc_empty[u], ((g / G::bufs) - 1) & 1)) ||
-              !tc::bar_wait_warp(&b.full[s], (g / G::stages) & 1)) {
-            if (lane == 0) pair_abort(b, a.flags);
-            ok = false;
-            break;
-          }
-          tc::tc_fence_after();
-          const uint32_t base = tc::smem_addr(sm + (size_t)s * G::stage);
-          const uint64_t ad = tc::sw128_desc(base), bd = tc::sw128_desc(base + kABytes);
-          if (tc::elect_one()) {
-#pragma unroll
-            for (int kk = 0; kk < BK / 32; ++kk)
-              tc::mma_f8_pair(tmem + (uint32_t)(u * 256), ad + 2 * kk, bd + 2 * kk, idesc, kk > 0);
-            tc::mma_commit_pair(&b.empty[s]);
-            tc::mma_commit_pair(&b.acc_full[u]);
-          }
-          __syncwarp();
-        }
-      }
-    }
-  } else if (warp < 4) {
-    // Scales: the products xs * ws of a step, [2 weight blocks][128 tokens],
-    // four steps of two tokens per lane loaded at a time, one group ahead.
-    const int r0 = (warp - 2) * 64 + lane;
-    const bool vec = (nb & 3) == 0 && (reinterpret_cast<uintptr_t>(a.xs) & 15) == 0;
-    float* sc = reinterpret_cast<float*>(sm + G::off_scale);
-    int g = 0;
-    bool ok = true;
-    for (int tile = first; tile < a.tiles && ok; tile += stride) {
-      const int m0 = (tile % a.mt) * 256 + rank * BM, n0 = (tile / a.mt) * kN;
-      const int wb = n0 / 128;
-      const float* pw0 = a.ws + (size_t)wb * nb;
-      const float* pw1 = GATEUP ? a.ws2 + (size_t)wb * nb : (n0 + 128 < a.N ? pw0 + nb : nullptr);
-      const float* px[2];
-      bool live[2];
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        live[i] = m0 + r0 + 32 * i < a.T;
-        px[i] = a.xs + (size_t)(live[i] ? m0 + r0 + 32 * i : 0) * nb;
-      }
-      float x[2][4], w0[4], w1[4];
-      auto load = [&](int kb) {
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          if (vec && live[i]) {
-            const float4 v = *reinterpret_cast<const float4*>(px[i] + kb);
-            x[i][0] = v.x; x[i][1] = v.y; x[i][2] = v.z; x[i][3] = v.w;
-          } else {
-#pragma unroll
-            for (int e = 0; e < 4; ++e) x[i][e] = live[i] && kb + e < nb ? px[i][kb + e] : 0.0f;
-          }
-        }
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          w0[e] = kb + e < nb ? pw0[kb + e] : 0.0f;
-          w1[e] = pw1 && kb + e < nb ? pw1[kb + e] : 0.0f;
-        }
-      };
-      load(0);
-      for (int kb = 0; kb < nb && ok; kb += 4) {
-        float p[4][2][2];
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            p[e][0][i] = x[i][e] * w0[e];
-            p[e][1][i] = x[i][e] * w1[e];
-          }
-        if (kb + 4 < nb) load(kb + 4);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          if (kb + e >= nb) break;
-          const int s = g % G::slots;
-          if (g >= G::slots && !tc::bar_wait_warp(&b.sc_empty[s], ((g / G::slots) - 1) & 1)) {
-            if (lane == 0) pair_abort(b, a.flags);
-            ok = false;
-            break;
-          }
-          float* d = sc + s * 2 * BM + r0;
-          d[0] = p[e][0][0];
-          d[32] = p[e][0][1];
-          d[BM] = p[e][1][0];
-          d[BM + 32] = p[e][1][1];
-          __syncwarp();
-          if (lane == 0) tc::bar_arrive(&b.sc_full[s]);
-          ++g;
-        }
-      }
-    }
-  } else {
-    const int q4 = warp & 3, j4 = (warp - 4) >> 2;
+  // 384 x 168 registers at launch = 128 x 104 + 256 x 200.
+  if (warp >= 4) {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
+    // Lane quarter q4; 128 columns from 128 j2 (gate/up: 64 of each from
+    // 64 j2), taken from tensor memory 32 at a time, the next 32 on their way
+    // while the FMAs of the last run.
+    const int q4 = warp & 3, j2 = (warp - 4) >> 2;
     const uint32_t tl = tmem + ((uint32_t)(32 * q4) << 16);
-    const uint32_t ca = GATEUP ? 32 * j4 : 64 * j4, cb = GATEUP ? 128 + 32 * j4 : ca + 32;
-    const float* sca = reinterpret_cast<const float*>(sm + G::off_scale) + (GATEUP ? 0 : (j4 >> 1) * BM) + 32 * q4 + lane;
+    const uint32_t c0 = GATEUP ? 64 * j2 : 128 * j2;
+    auto col = [&](int c) { return GATEUP && c >= 2 ? 128 + c0 + 32 * (c - 2) : c0 + 32 * c; };
+    const float* sca = reinterpret_cast<const float*>(sm + G::off_scale) + (GATEUP ? 0 : j2 * BM) + 32 * q4 + lane;
     const uint32_t acc_empty0 = tc::map_rank(tc::smem_addr(&b.acc_empty[0]), 0);
-    uint8_t* out = sm + G::off_out + (warp - 4) * 4096;
+    uint8_t* out = sm + G::off_out + (warp - 4) * 8192;
     int g = 0;
     bool ok = true;
     for (int tile = first; tile < a.tiles; tile += stride) {
       const int m0 = (tile % a.mt) * 256 + rank * BM, n0 = (tile / a.mt) * kN;
       const int r = 32 * q4 + lane, row = m0 + r;
-      uint64_t sum[32];
+      uint64_t sum[64];
 #pragma unroll
-      for (int i = 0; i < 32; ++i) sum[i] = 0;
+      for (int i = 0; i < 64; ++i) sum[i] = 0;
       for (int kb = 0; kb < nb; ++kb, ++g) {
         const int u = g % G::bufs, s = g % G::slots;
         if (!tc::bar_wait_warp(&b.sc_full[s], (g / G::slots) & 1)) {
@@ -668,21 +546,24 @@ __global__ void __launch_bounds__(Pair::threads, 1)
         }
         tc::tc_fence_after();
         const uint32_t buf = tl + (uint32_t)(u * 256);
-        uint32_t d[32];
-        tc::tmem_ld32(buf + ca, d);
+        uint32_t d[2][32];
+        tc::tmem_ld32(buf + col(0), d[0]);
+        const uint64_t sa2 = pack2(sa, sa), sb2 = GATEUP ? pack2(sb, sb) : sa2;
         if (lane == 0) tc::bar_arrive(&b.sc_empty[s]);
-        tc::tmem_ld32_wait(d);
-        const uint64_t sa2 = pack2(sa, sa);
 #pragma unroll
-        for (int i = 0; i < 16; ++i) fma2(sum[i], d[2 * i], d[2 * i + 1], sa2);
-        tc::tmem_ld32(buf + cb, d);
-        tc::tmem_ld32_wait(d);
-        tc::tc_fence_before();
-        __syncwarp();
-        if (lane == 0) tc::bar_arrive_cluster(acc_empty0 + 8 * u);
-        const uint64_t sb2 = GATEUP ? pack2(sb, sb) : sa2;
+        for (int c = 0; c < 4; ++c) {
+          tc::tmem_ld32_wait(d[c & 1]);
+          if (c < 3) {
+            tc::tmem_ld32(buf + col(c + 1), d[(c + 1) & 1]);
+          } else {
+            tc::tc_fence_before();
+            __syncwarp();
+            if (lane == 0) tc::bar_arrive_cluster(acc_empty0 + 8 * u);
+          }
 #pragma unroll
-        for (int i = 0; i < 16; ++i) fma2(sum[16 + i], d[2 * i], d[2 * i + 1], sb2);
+          for (int i = 0; i < 16; ++i)
+            fma2(sum[16 * c + i], d[c & 1][2 * i], d[c & 1][2 * i + 1], c < 2 ? sa2 : sb2);
+        }
       }
       if (!ok && lane == 0) pair_abort(b, a.flags);
       if (!GATEUP) {
@@ -692,61 +573,197 @@ __global__ void __launch_bounds__(Pair::threads, 1)
           if (lane == 0) tc::tma_store_wait_read();
           __syncwarp();
 #pragma unroll
-          for (int c = 0; c < 8; ++c) {
+          for (int c = 0; c < 16; ++c) {
             uint32_t h[4];
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
               const float2 p = unpack2(sum[4 * c + e]);
               h[e] = half2_bits(p.x, p.y);
             }
-            *reinterpret_cast<uint4*>(out + tc::sw128_offset(lane, c)) = make_uint4(h[0], h[1], h[2], h[3]);
+            *reinterpret_cast<uint4*>(out + (c >> 3) * 4096 + tc::sw128_offset(lane, c & 7)) =
+                make_uint4(h[0], h[1], h[2], h[3]);
           }
           tc::fence_async_smem();
           __syncwarp();
-          const int y0 = m0 + 32 * q4, x0 = n0 + (int)ca;
-          if (lane == 0 && y0 < a.T && x0 < a.N) tc::tma_store_2d(&map_y, x0, y0, out);
+          const int y0 = m0 + 32 * q4, x0 = n0 + (int)c0;
+          if (lane == 0 && y0 < a.T && x0 < a.N) {
+            tc::tma_store_2d(&map_y, x0, y0, out);
+            if (x0 + 64 < a.N) tc::tma_store_2d(&map_y, x0 + 64, y0, out + 4096);
+          }
         } else if (row < a.T) {
-          __half* o = a.y + (size_t)row * a.N + n0 + ca;
-          const int left = a.N - (n0 + (int)ca);
+          __half* o = a.y + (size_t)row * a.N + n0 + c0;
+          const int left = a.N - (n0 + (int)c0);
 #pragma unroll
-          for (int i = 0; i < 32; ++i) {
+          for (int i = 0; i < 64; ++i) {
             const float2 p = unpack2(sum[i]);
             if (2 * i < left) o[2 * i] = __float2half_rn(p.x);
             if (2 * i + 1 < left) o[2 * i + 1] = __float2half_rn(p.y);
           }
         }
       } else {
-        float h[32], up[32];
+        float h[64], up[64];
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const float2 p = unpack2(sum[i]), q = unpack2(sum[16 + i]);
+        for (int i = 0; i < 32; ++i) {
+          const float2 p = unpack2(sum[i]), q = unpack2(sum[32 + i]);
           h[2 * i] = p.x; h[2 * i + 1] = p.y;
           up[2 * i] = q.x; up[2 * i + 1] = q.y;
         }
         float m = swiglu(h, up);
-        b.amax[j4 * BM + r] = m;
+        b.amax[j2 * BM + r] = m;
         asm volatile("barrier.sync 1, %0;" ::"n"(32 * G::promo) : "memory");
-#pragma unroll
-        for (int w = 0; w < 4; ++w) m = fmaxf(m, b.amax[w * BM + r]);
+        m = fmaxf(m, b.amax[(j2 ^ 1) * BM + r]);
         // Maxima read before the next tile's; one verdict for all the warps.
         if (promo_any<32 * G::promo>(!ok)) break;
         const fp8::BlockScale bs = fp8::block_scale(m);
         if (row < a.T) {
-          uint8_t* o = a.hq + (size_t)row * a.N + n0 + ca;
+          uint8_t* o = a.hq + (size_t)row * a.N + n0 + c0;
+          if (n0 + (int)c0 < a.N) {  // Is is a multiple of 64
 #pragma unroll
-          for (int i = 0; i < 32; i += 16) {
-            uint32_t c[4];
+            for (int i = 0; i < 64; i += 16) {
+              uint32_t c[4];
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-              c[e] = fp8::encode4(h[i + 4 * e] * bs.inv, h[i + 4 * e + 1] * bs.inv, h[i + 4 * e + 2] * bs.inv,
-                                  h[i + 4 * e + 3] * bs.inv);
-            if (n0 + (int)ca + i < a.N) *reinterpret_cast<uint4*>(o + i) = make_uint4(c[0], c[1], c[2], c[3]);
+              for (int e = 0; e < 4; ++e)
+                c[e] = fp8::encode4(h[i + 4 * e] * bs.inv, h[i + 4 * e + 1] * bs.inv, h[i + 4 * e + 2] * bs.inv,
+                                    h[i + 4 * e + 3] * bs.inv);
+              *reinterpret_cast<uint4*>(o + i) = make_uint4(c[0], c[1], c[2], c[3]);
+            }
           }
-          if (j4 == 0) a.hs[(size_t)row * a.nbh + n0 / 128] = bs.scale;
+          if (j2 == 0) a.hs[(size_t)row * a.nbh + n0 / 128] = bs.scale;
         }
       }
     }
     if (!GATEUP && lane == 0) tc::tma_store_wait_all();
+  } else {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
+    if (warp == 0) {
+      // Both blocks' loads complete on the leading block's barrier.
+      const CUtensorMap* mw = GATEUP && rank ? &map_w2 : &map_w;
+      int g = 0;
+      bool ok = true;
+      for (int tile = first; tile < a.tiles && ok; tile += stride) {
+        const int m0 = (tile % a.mt) * 256 + rank * BM, n0 = (tile / a.mt) * kN + (GATEUP ? 0 : rank * 128);
+        for (int kb = 0; kb < nb; ++kb, ++g) {
+          const int s = g % G::stages;
+          if (g >= G::stages && !tc::bar_wait_warp(&b.empty[s], ((g / G::stages) - 1) & 1)) {
+            if (lane == 0) pair_abort(b, a.flags);
+            ok = false;
+            break;
+          }
+          if (tc::elect_one()) {
+            uint8_t* st = sm + (size_t)s * G::stage;
+            const uint32_t full = tc::map_rank(tc::smem_addr(&b.full[s]), 0);
+            if (rank == 0) tc::bar_expect_tx(&b.full[s], 2 * G::stage);
+            tc::tma_load_2d_pair(st, &map_x, kb * BK, m0, full);
+            tc::tma_load_2d_pair(st + kABytes, mw, kb * BK, n0, full);
+          }
+          __syncwarp();
+        }
+      }
+      // After a wait that ran out, the loads still in flight land before the
+      // block leaves: 2 ms, since no barrier of this block counts them.
+      if (!ok) {
+        const uint64_t t0 = tc::global_ns();
+        for (int i = 0; i < 1000000 && tc::global_ns() - t0 < 2000000ull; ++i) {
+        }
+      }
+    } else if (warp == 1) {
+      if (rank == 0) {
+        constexpr uint32_t idesc = tc::idesc_f16(256, 256);
+        int g = 0;
+        bool ok = true;
+        for (int tile = first; tile < a.tiles && ok; tile += stride) {
+          for (int kb = 0; kb < nb; ++kb, ++g) {
+            const int s = g % G::stages, u = g % G::bufs;
+            if ((g >= G::bufs && !tc::bar_wait_warp(&b.acc_empty[u], ((g / G::bufs) - 1) & 1)) ||
+                !tc::bar_wait_warp(&b.full[s], (g / G::stages) & 1)) {
+              if (lane == 0) pair_abort(b, a.flags);
+              ok = false;
+              break;
+            }
+            tc::tc_fence_after();
+            const uint32_t base = tc::smem_addr(sm + (size_t)s * G::stage);
+            const uint64_t ad = tc::sw128_desc(base), bd = tc::sw128_desc(base + kABytes);
+            if (tc::elect_one()) {
+#pragma unroll
+              for (int kk = 0; kk < BK / 32; ++kk)
+                tc::mma_f8_pair(tmem + (uint32_t)(u * 256), ad + 2 * kk, bd + 2 * kk, idesc, kk > 0);
+              tc::mma_commit_pair(&b.empty[s]);
+              tc::mma_commit_pair(&b.acc_full[u]);
+            }
+            __syncwarp();
+          }
+        }
+      }
+    } else if (warp < 4) {
+      // Scales: the products xs * ws of a step, [2 weight blocks][128 tokens],
+      // four steps of two tokens per lane loaded at a time, one group ahead.
+      const int r0 = (warp - 2) * 64 + lane;
+      const bool vec = (nb & 3) == 0 && (reinterpret_cast<uintptr_t>(a.xs) & 15) == 0;
+      float* sc = reinterpret_cast<float*>(sm + G::off_scale);
+      int g = 0;
+      bool ok = true;
+      for (int tile = first; tile < a.tiles && ok; tile += stride) {
+        const int m0 = (tile % a.mt) * 256 + rank * BM, n0 = (tile / a.mt) * kN;
+        const int wb = n0 / 128;
+        const float* pw0 = a.ws + (size_t)wb * nb;
+        const float* pw1 = GATEUP ? a.ws2 + (size_t)wb * nb : (n0 + 128 < a.N ? pw0 + nb : nullptr);
+        const float* px[2];
+        bool live[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          live[i] = m0 + r0 + 32 * i < a.T;
+          px[i] = a.xs + (size_t)(live[i] ? m0 + r0 + 32 * i : 0) * nb;
+        }
+        float x[2][4], w0[4], w1[4];
+        auto load = [&](int kb) {
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            if (vec && live[i]) {
+              const float4 v = *reinterpret_cast<const float4*>(px[i] + kb);
+              x[i][0] = v.x; x[i][1] = v.y; x[i][2] = v.z; x[i][3] = v.w;
+            } else {
+#pragma unroll
+              for (int e = 0; e < 4; ++e) x[i][e] = live[i] && kb + e < nb ? px[i][kb + e] : 0.0f;
+            }
+          }
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            w0[e] = kb + e < nb ? pw0[kb + e] : 0.0f;
+            w1[e] = pw1 && kb + e < nb ? pw1[kb + e] : 0.0f;
+          }
+        };
+        load(0);
+        for (int kb = 0; kb < nb && ok; kb += 4) {
+          float p[4][2][2];
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              p[e][0][i] = x[i][e] * w0[e];
+              p[e][1][i] = x[i][e] * w1[e];
+            }
+          if (kb + 4 < nb) load(kb + 4);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            if (kb + e >= nb) break;
+            const int s = g % G::slots;
+            if (g >= G::slots && !tc::bar_wait_warp(&b.sc_empty[s], ((g / G::slots) - 1) & 1)) {
+              if (lane == 0) pair_abort(b, a.flags);
+              ok = false;
+              break;
+            }
+            float* d = sc + s * 2 * BM + r0;
+            d[0] = p[e][0][0];
+            d[32] = p[e][0][1];
+            d[BM] = p[e][1][0];
+            d[BM + 32] = p[e][1][1];
+            __syncwarp();
+            if (lane == 0) tc::bar_arrive(&b.sc_full[s]);
+            ++g;
+          }
+        }
+      }
+    }
   }
   tc::tc_fence_before();
   __syncwarp();
