@@ -8,6 +8,7 @@
 //   groups of E/G experts ranked by max v or by the sum of their two largest
 //   scores, the best top_groups kept; top-k of the kept experts by
 //   (v desc, index asc); w_j = s_{id_j} [/ (sum_j s_{id_j} + 1e-20)] * scale.
+#include <algorithm>
 #include <climits>
 
 #include "common.h"
@@ -24,6 +25,7 @@ struct ScoredArgs {
   int G, per;       // groups, experts per group
   int lg_shift;     // log2 of the lanes that hold one group
   int chunk;        // experts per lane
+  int vec;          // rows can be read 16 bytes at a time
   int top_g, rank_top2, sigmoid, renorm;
   float scale;
   const float* bias;
@@ -32,13 +34,19 @@ struct ScoredArgs {
   int32_t* bad;
 };
 
+// The value of an order_key (of a finite value).
+__device__ __forceinline__ float key_value(uint32_t k) {
+  return __uint_as_float((k & 0x80000000u) ? (k & 0x7fffffffu) : ~k);
+}
+
 template <bool HALF>
 __device__ __forceinline__ float load_logit(const void* row, int e) {
   if (HALF) return __half2float(static_cast<const __half*>(row)[e]);
   return static_cast<const float*>(row)[e];
 }
 
-__device__ __forceinline__ float sigmoid_f(float v) { return 1.0f / (1.0f + expf(-v)); }
+// Relative error about 2^-21; 0 below -87 (where exp(-v) overflows) or so.
+__device__ __forceinline__ float sigmoid_f(float v) { return __fdividef(1.0f, 1.0f + expf(-v)); }
 
 __device__ __forceinline__ float warp_max(float v) {
 #pragma unroll
@@ -46,119 +54,214 @@ __device__ __forceinline__ float warp_max(float v) {
   return v;
 }
 
-// One warp per token. The lanes are split evenly over the groups (rounded up
-// to a power of two), and a lane holds `chunk` consecutive experts of its
-// group, so a group's two best are a butterfly over its own lanes.
+// N consecutive values at p, 16 bytes at a time (p 16-byte aligned).
+template <int N, bool HALF>
+__device__ __forceinline__ void load_vec(const void* p, float (&v)[N]) {
+  if (HALF) {
+#pragma unroll
+    for (int i = 0; i < N; i += 8) {
+      const uint4 w = static_cast<const uint4*>(p)[i / 8];
+      const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (i + j < N) v[i + j] = __half2float(__ushort_as_half((unsigned short)(u[j / 2] >> (16 * (j & 1)))));
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; i += 4) {
+      const float4 w = static_cast<const float4*>(p)[i / 4];
+      const float u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (i + j < N) v[i + j] = u[j];
+    }
+  }
+}
+
+constexpr int kWarpsPerBlock = 4;
+
+// One warp per token (looping over tokens when there are many). The lanes are
+// split evenly over the groups (rounded up to a power of two), and a lane
+// holds `chunk` consecutive experts of its group, so a group's two best are a
+// butterfly over its own lanes.
+//
+// Top-k: the k-th largest of the lanes' maxima (k rounds of one warp
+// reduction) is a bound that at least k candidates reach; the candidates that
+// reach it are usually few more than k. They are compacted to shared memory,
+// and each lane ranks one of them by (v desc, index asc) against the others.
+// Where more than 32 reach the bound, k rounds of argmax instead.
 template <int PER, bool HALF>
-__global__ void __launch_bounds__(128) route_scored_kernel(const ScoredArgs a) {
-  griddep_wait();
-  griddep_launch_dependents();
+__global__ void __launch_bounds__(32 * kWarpsPerBlock) route_scored_kernel(const ScoredArgs a) {
+  constexpr bool kBiasRegs = PER <= 16;  // a lane's biases stay in registers over its tokens
+  __shared__ float2 cand_all[kWarpsPerBlock][32];
   const unsigned full = 0xffffffffu;
-  const int lane = threadIdx.x & 31;
-  const int t = (blockIdx.x * blockDim.x + threadIdx.x) >> 5;
-  if (t >= a.T) return;
-  const size_t esz = HALF ? 2 : 4;
-  const uint8_t* row = static_cast<const uint8_t*>(a.logits) + (size_t)t * a.ld * esz;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  float2* cand = cand_all[warp];
   const int grp = lane >> a.lg_shift, sub = lane & ((1 << a.lg_shift) - 1);
   const int first = grp * a.per + sub * a.chunk;
   const int n = grp < a.G ? max(0, min(a.chunk, a.per - sub * a.chunk)) : 0;
-
-  float v[PER];  // logits, then what orders the experts (-inf: not to be chosen)
-  bool bad = false;
-  float mx = -INFINITY;
-#pragma unroll
-  for (int j = 0; j < PER; ++j) {
-    v[j] = j < n ? load_logit<HALF>(row, first + j) : -INFINITY;
-    bad |= isnan(v[j]) || v[j] == INFINITY;
-    mx = fmaxf(mx, v[j]);
-  }
-  float m = 0.0f, sum = 1.0f;
-  if (!a.sigmoid) {
-    m = warp_max(mx);
-    float s = 0.0f;
-#pragma unroll
-    for (int j = 0; j < PER; ++j) s += v[j] > -INFINITY ? expf(v[j] - m) : 0.0f;
-    sum = warp_sum(s);
-  }
-  auto score = [&](float l) { return a.sigmoid ? sigmoid_f(l) : expf(l - m) / sum; };
-  float g1 = -INFINITY, g2 = -INFINITY;  // the lane's two best for the group's value
-  bool live = false;
-#pragma unroll
-  for (int j = 0; j < PER; ++j) {
-    if (j < n) {
-      float o = v[j], r = o;
-      if (a.bias) {
-        const float b = a.bias[first + j];
-        bad |= isnan(b) || b == INFINITY;
-        o = o > -INFINITY && b > -INFINITY ? score(o) + b : -INFINITY;
-        r = o;
-      } else if (a.rank_top2) {
-        r = o > -INFINITY ? score(o) : -INFINITY;
-      }
-      v[j] = o;
-      live |= o > -INFINITY;
-      g2 = fmaxf(g2, fminf(g1, r));
-      g1 = fmaxf(g1, r);
-    }
-  }
-  if (__any_sync(full, bad) || !__any_sync(full, live)) {
-    if (lane < a.k) {
-      a.ids[(size_t)t * a.k + lane] = -1;
-      a.weights[(size_t)t * a.k + lane] = 0.0f;
-    }
-    if (lane == 0 && a.bad) atomicAdd(a.bad, 1);
-    return;
-  }
-  bool kept = grp < a.G;
-  if (a.top_g < a.G) {
-    for (int o = 1; o < (1 << a.lg_shift); o <<= 1) {
-      const float h1 = __shfl_xor_sync(full, g1, o), h2 = __shfl_xor_sync(full, g2, o);
-      g2 = fmaxf(fminf(g1, h1), fmaxf(g2, h2));
-      g1 = fmaxf(g1, h1);
-    }
-    const float gv = a.rank_top2 && g2 > -INFINITY ? g1 + g2 : g1;
-    int before = 0;
-    for (int h = 0; h < a.G; ++h) before += ranks_before(__shfl_sync(full, gv, h << a.lg_shift), h, gv, grp);
-    kept = kept && before < a.top_g;
-  }
-
-  // Top-k: each lane offers its best expert not yet picked; a round takes the
-  // largest order key of the warp and the lowest index that has it.
-  float bv = -INFINITY;
-  int bi = INT_MAX;
-  auto best_after = [&](float lv, int li) {  // the lane's best that ranks after (lv, li)
-    bv = -INFINITY;
-    bi = INT_MAX;
+  griddep_wait();
+  griddep_launch_dependents();
+  float bias[kBiasRegs ? PER : 1];
+  bool bad_bias = false;
+  if (a.bias) {
 #pragma unroll
     for (int j = 0; j < PER; ++j)
-      if (v[j] > -INFINITY && ranks_before(lv, li, v[j], first + j) && ranks_before(v[j], first + j, bv, bi)) {
-        bv = v[j];
-        bi = first + j;
+      if (j < n) {
+        const float b = a.bias[first + j];
+        bad_bias |= isnan(b) || b == INFINITY;
+        if (kBiasRegs) bias[j] = b;
       }
-  };
-  if (kept) best_after(INFINITY, -1);
-  int my_i = -1;
-  for (int r = 0; r < a.k; ++r) {
-    const uint32_t key = bi != INT_MAX ? order_key(bv) : 0u;
-    const uint32_t kmax = __reduce_max_sync(full, key);
-    if (kmax == 0u) break;  // no expert left: the other picks stay -1
-    const int win = (int)__reduce_min_sync(full, key == kmax ? (uint32_t)bi : 0xffffffffu);
-    if (lane == r) my_i = win;
-    if (bi == win) best_after(bv, win);
   }
-  const float s = my_i >= 0 ? score(load_logit<HALF>(row, my_i)) : 0.0f;
-  const float total = warp_sum(s);
-  if (lane < a.k) {
-    a.ids[(size_t)t * a.k + lane] = my_i;
-    a.weights[(size_t)t * a.k + lane] = (a.renorm ? s / (total + 1e-20f) : s) * a.scale;
+  for (int t = blockIdx.x * kWarpsPerBlock + warp; t < a.T; t += gridDim.x * kWarpsPerBlock) {
+    const uint8_t* row = static_cast<const uint8_t*>(a.logits) + (size_t)t * a.ld * (HALF ? 2 : 4);
+    float v[PER];  // logits, then what orders the experts (-inf: not to be chosen)
+    if (a.vec && n == PER) {
+      load_vec<PER, HALF>(row + (size_t)first * (HALF ? 2 : 4), v);
+    } else {
+#pragma unroll
+      for (int j = 0; j < PER; ++j) v[j] = j < n ? load_logit<HALF>(row, first + j) : -INFINITY;
+    }
+    bool bad = bad_bias;
+    float mx = -INFINITY;
+#pragma unroll
+    for (int j = 0; j < PER; ++j) {
+      bad |= !(v[j] < INFINITY);  // NaN or +inf
+      mx = fmaxf(mx, v[j]);
+    }
+    float m = 0.0f, inv = 1.0f;
+    if (!a.sigmoid) {
+      m = warp_max(mx);
+      float s = 0.0f;
+#pragma unroll
+      for (int j = 0; j < PER; ++j) s += v[j] > -INFINITY ? expf(v[j] - m) : 0.0f;
+      inv = 1.0f / warp_sum(s);
+    }
+    auto score = [&](float l) { return a.sigmoid ? sigmoid_f(l) : expf(l - m) * inv; };
+    float g1 = mx, g2 = -INFINITY;  // the lane's two best for the group's value
+    float top = mx;                 // the lane's best in the order
+    if (a.bias || a.rank_top2) {
+      g1 = top = -INFINITY;
+#pragma unroll
+      for (int j = 0; j < PER; ++j) {
+        float o = v[j], r = o;
+        if (a.bias) {
+          const float b = kBiasRegs ? bias[kBiasRegs ? j : 0] : (j < n ? a.bias[first + j] : 0.0f);
+          r = o = j < n && o > -INFINITY && b > -INFINITY ? score(o) + b : -INFINITY;
+          v[j] = o;
+        } else {
+          r = o > -INFINITY ? score(o) : -INFINITY;
+        }
+        top = fmaxf(top, o);
+        g2 = fmaxf(g2, fminf(g1, r));
+        g1 = fmaxf(g1, r);
+      }
+    }
+    if (__any_sync(full, bad) || !__any_sync(full, top > -INFINITY)) {
+      if (lane < a.k) {
+        a.ids[(size_t)t * a.k + lane] = -1;
+        a.weights[(size_t)t * a.k + lane] = 0.0f;
+      }
+      if (lane == 0 && a.bad) atomicAdd(a.bad, 1);
+      continue;
+    }
+    bool kept = grp < a.G;
+    if (a.top_g < a.G) {
+      for (int o = 1; o < (1 << a.lg_shift); o <<= 1) {
+        const float h1 = __shfl_xor_sync(full, g1, o), h2 = __shfl_xor_sync(full, g2, o);
+        g2 = fmaxf(fminf(g1, h1), fmaxf(g2, h2));
+        g1 = fmaxf(g1, h1);
+      }
+      const float gv = a.rank_top2 && g2 > -INFINITY ? g1 + g2 : g1;
+      int before = 0;
+#pragma unroll 4
+      for (int h = 0; h < a.G; ++h) {
+        const float o = __shfl_sync(full, gv, h << a.lg_shift);
+        before += o > gv || (o == gv && h < grp);
+      }
+      kept = kept && before < a.top_g;
+    }
+
+    const uint32_t key0 = kept && top > -INFINITY ? order_key(top) : 0u;  // a real key is above 0
+    uint32_t key = key0, bound = 0u;
+    for (int r = 0; r < a.k; ++r) {
+      bound = __reduce_max_sync(full, key);
+      if (key == bound) key = 0u;
+    }
+    int count = 0;
+    if (bound == 0u) {  // fewer than k lanes hold a candidate: all of them
+#pragma unroll
+      for (int j = 0; j < PER; ++j) {
+        const bool on = kept && v[j] > -INFINITY;
+        const unsigned ball = __ballot_sync(full, on);
+        const int pos = count + __popc(ball & ((1u << lane) - 1u));
+        if (on && pos < 32) cand[pos] = make_float2(v[j], __int_as_float(first + j));
+        count += __popc(ball);
+      }
+    } else {
+      const float lim = kept ? key_value(bound) : INFINITY;
+#pragma unroll
+      for (int j = 0; j < PER; ++j) {
+        const bool on = v[j] >= lim;
+        const unsigned ball = __ballot_sync(full, on);
+        const int pos = count + __popc(ball & ((1u << lane) - 1u));
+        if (on && pos < 32) cand[pos] = make_float2(v[j], __int_as_float(first + j));
+        count += __popc(ball);
+      }
+    }
+    int my_i = -1, my_r = 32;  // this lane's pick and its rank
+    if (count <= 32) {
+      __syncwarp();
+      const float2 me = cand[lane < count ? lane : 0];
+      if (lane < count) {
+        my_i = __float_as_int(me.y);
+        my_r = 0;
+        for (int c = 0; c < count; ++c) {
+          const float2 o = cand[c];
+          my_r += ranks_before(o.x, __float_as_int(o.y), me.x, my_i);
+        }
+      } else if (lane < a.k) {
+        my_r = lane;  // no expert left for this pick
+      }
+      __syncwarp();
+    } else {
+      float bv = -INFINITY;
+      int bi = INT_MAX;
+      auto best_after = [&](float lv, int li) {  // the lane's best that ranks after (lv, li)
+        bv = -INFINITY;
+        bi = INT_MAX;
+#pragma unroll
+        for (int j = 0; j < PER; ++j)
+          if (v[j] > -INFINITY && ranks_before(lv, li, v[j], first + j) && ranks_before(v[j], first + j, bv, bi)) {
+            bv = v[j];
+            bi = first + j;
+          }
+      };
+      if (kept) best_after(INFINITY, -1);
+      for (int r = 0; r < a.k; ++r) {  // more than 32 candidates, k <= 32: every round finds one
+        const uint32_t bk = bi != INT_MAX ? order_key(bv) : 0u;
+        const uint32_t kmax = __reduce_max_sync(full, bk);
+        const int win = (int)__reduce_min_sync(full, bk == kmax ? (uint32_t)bi : 0xffffffffu);
+        if (lane == r) my_i = win;
+        if (bi == win) best_after(bv, win);
+      }
+      my_r = lane;
+    }
+    const bool picked = my_r < a.k && my_i >= 0;
+    float s = picked ? score(load_logit<HALF>(row, my_i)) : 0.0f;
+    if (a.renorm) s = s / (warp_sum(s) + 1e-20f);
+    if (my_r < a.k) {
+      a.ids[(size_t)t * a.k + my_r] = my_i;
+      a.weights[(size_t)t * a.k + my_r] = s * a.scale;
+    }
   }
 }
 
 template <int PER, bool HALF>
-cudaError_t launch_scored(const ScoredArgs& a, cudaStream_t st) {
+cudaError_t launch_scored(const ScoredArgs& a, int sms, cudaStream_t st) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)((a.T + 3) / 4));
-  cfg.blockDim = dim3(128);
+  cfg.gridDim = dim3((unsigned)std::min((a.T + kWarpsPerBlock - 1) / kWarpsPerBlock, sms * 12));
+  cfg.blockDim = dim3(32 * kWarpsPerBlock);
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -169,13 +272,13 @@ cudaError_t launch_scored(const ScoredArgs& a, cudaStream_t st) {
 }
 
 template <bool HALF>
-cudaError_t launch_scored(const ScoredArgs& a, cudaStream_t st) {
-  if (a.chunk <= 2) return launch_scored<2, HALF>(a, st);
-  if (a.chunk <= 4) return launch_scored<4, HALF>(a, st);
-  if (a.chunk <= 8) return launch_scored<8, HALF>(a, st);
-  if (a.chunk <= 16) return launch_scored<16, HALF>(a, st);
-  if (a.chunk <= 32) return launch_scored<32, HALF>(a, st);
-  return launch_scored<64, HALF>(a, st);
+cudaError_t launch_scored(const ScoredArgs& a, int sms, cudaStream_t st) {
+  if (a.chunk <= 2) return launch_scored<2, HALF>(a, sms, st);
+  if (a.chunk <= 4) return launch_scored<4, HALF>(a, sms, st);
+  if (a.chunk <= 8) return launch_scored<8, HALF>(a, sms, st);
+  if (a.chunk <= 16) return launch_scored<16, HALF>(a, sms, st);
+  if (a.chunk <= 32) return launch_scored<32, HALF>(a, sms, st);
+  return launch_scored<64, HALF>(a, sms, st);
 }
 
 }  // namespace
@@ -211,7 +314,7 @@ extern "C" int moe_route_scored(const moe_route_cfg* cfg, const void* logits, in
                                 void* stream) {
   moe::NvtxRange nvtx_range("moe_route_scored");
   moe::clear_error();
-  const int rc = moe::check_route_cfg("moe_route_scored", cfg, logits, logit_type, ld, T, E, k);
+  int rc = moe::check_route_cfg("moe_route_scored", cfg, logits, logit_type, ld, T, E, k);
   if (rc != MOE_OK) return rc;
   if (T == 0) return MOE_OK;
   if (!logits || !ids || !weights) return moe::fail(MOE_ERR_ARG, "moe_route_scored: NULL pointer");
@@ -225,6 +328,10 @@ extern "C" int moe_route_scored(const moe_route_cfg* cfg, const void* logits, in
   while ((32 >> shift) < a.G) --shift;
   a.lg_shift = shift;
   a.chunk = (a.per + (1 << shift) - 1) >> shift;
+  // 16-byte loads where every lane's run of experts starts on 16 bytes.
+  const int esz = logit_type == MOE_F16 ? 2 : 4;
+  a.vec = reinterpret_cast<uintptr_t>(logits) % 16 == 0 && ld * esz % 16 == 0 && a.chunk * esz % 16 == 0 &&
+          a.per * esz % 16 == 0;
   a.top_g = cfg->top_groups;
   a.rank_top2 = cfg->group_rank == MOE_GROUP_TOP2 && a.per > 1;
   a.sigmoid = cfg->score == MOE_SCORE_SIGMOID;
@@ -235,7 +342,10 @@ extern "C" int moe_route_scored(const moe_route_cfg* cfg, const void* logits, in
   a.weights = weights;
   a.bad = bad_tokens;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const cudaError_t e = logit_type == MOE_F16 ? moe::launch_scored<true>(a, st) : moe::launch_scored<false>(a, st);
+  int dev = 0, sms = 0;
+  if ((rc = moe::current_device_sms(&dev, &sms)) != MOE_OK) return rc;
+  const cudaError_t e = logit_type == MOE_F16 ? moe::launch_scored<true>(a, sms, st)
+                                             : moe::launch_scored<false>(a, sms, st);
   if (e != cudaSuccess) return moe::fail(MOE_ERR_CUDA, "moe_route_scored launch: %s", cudaGetErrorString(e));
   return MOE_OK;
 }
