@@ -27,6 +27,10 @@ constexpr int BM = 128;           // tokens per tile
 constexpr int BK = fp8::kBlock;   // codes per step: one scale block, one swizzle row
 constexpr uint32_t kABytes = BM * BK;
 constexpr int kMaxSplits = 8;     // portable cluster size
+// Scales of up to 32 steps in shared memory: the tokens' [step][token] (odd
+// pitch: written by step, read by token), the two weight blocks' [2][step].
+constexpr int kChunk = 32, kScalePitch = BM + 1;
+constexpr uint32_t kScaleBytes = (kChunk * kScalePitch + 2 * kChunk) * 4;
 
 // Geometry by tile width. Warp 0 issues TMA, warp 1 owns tensor memory and
 // issues the MMAs, the others promote, at most 64 columns each.
@@ -39,10 +43,11 @@ struct Geo {
   static constexpr int stages = NT == 256 ? 4 : NT == 128 ? 6 : 8;
   static constexpr int bufs = NT == 256 ? 2 : NT == 128 ? 4 : 8;  // accumulators in tensor memory
   static constexpr uint32_t tmem_cols = (uint32_t)bufs * NT;
-  static constexpr uint32_t off_ctrl = (uint32_t)stages * stage;
+  static constexpr uint32_t off_scale = (uint32_t)stages * stage;
+  static constexpr uint32_t off_ctrl = off_scale + kScaleBytes;
   static constexpr size_t smem = (size_t)off_ctrl + 4096 + 1024;  // control block, alignment
   static constexpr int red_pitch = NT + 4;                        // floats per row of a partial tile
-  static_assert((size_t)BM * red_pitch * 4 <= off_ctrl, "partial tile fits the stage area");
+  static_assert((size_t)BM * red_pitch * 4 <= off_scale, "partial tile fits the stage area");
   static_assert(tmem_cols <= 512 && (tmem_cols & (tmem_cols - 1)) == 0, "tensor memory budget");
 };
 
@@ -144,7 +149,7 @@ __device__ __forceinline__ float swiglu(float (&gt)[N], const float (&up)[N]) {
   bool bad = false;
 #pragma unroll
   for (int i = 0; i < N; ++i) {
-    gt[i] = silu_f(gt[i]) * up[i];
+    gt[i] = silu_fast(gt[i]) * up[i];
     bad |= !(fabsf(gt[i]) < INFINITY);
     m = fmaxf(m, fabsf(gt[i]));
   }
@@ -254,55 +259,63 @@ __global__ void __launch_bounds__(Geo<NT>::threads, 1)
     const uint32_t tl = tmem + ((uint32_t)(32 * q4) << 16);
     const uint32_t ca = GATEUP ? 32 * j4 : G::cols * j4, cb = GATEUP ? 128 + 32 * j4 : ca + 32;
     constexpr int kPairs = G::cols / 2;
+    float* sx = reinterpret_cast<float*>(sm + G::off_scale);
+    float* sw = sx + kChunk * kScalePitch;
+    const int blk = GATEUP ? 0 : (int)ca / 128;
     int g = 0;
     bool ok = true;
     for (int tile = first; tile < a.tiles; tile += stride) {
       const int m0 = (tile % a.mt) * BM, n0 = (tile / a.mt) * kN;
       const int r = 32 * q4 + lane, row = m0 + r;
-      // Scales: one per token and step, one (gate/up: two) per weight block and step.
       const bool live = row < a.T;
-      const float* px = a.xs + (size_t)(live ? row : 0) * a.nb;
-      const int wb = (GATEUP ? n0 : n0 + (int)ca) / 128;
-      const bool wlive = wb * 128 < a.N;
-      const float* pw = a.ws + (size_t)(wlive ? wb : 0) * a.nb;
-      const float* pw2 = GATEUP ? a.ws2 + (size_t)wb * a.nb : pw;
       uint64_t sum[kPairs];
 #pragma unroll
       for (int i = 0; i < kPairs; ++i) sum[i] = 0;
-      float x0 = live ? px[kb0] : 0.0f, w0 = wlive ? pw[kb0] : 0.0f, u0 = GATEUP ? pw2[kb0] : 0.0f;
-      for (int kb = kb0; kb < kb1; ++kb, ++g) {
-        const int u = g % G::bufs;
-        const float sa = x0 * w0, sb = GATEUP ? x0 * u0 : sa;
-        if (kb + 1 < kb1) {  // the next step's scales load while this one is waited for
-          x0 = live ? px[kb + 1] : 0.0f;
-          w0 = wlive ? pw[kb + 1] : 0.0f;
-          if (GATEUP) u0 = pw2[kb + 1];
+      bool stop = false;
+      for (int kc = kb0; kc < kb1; kc += kChunk) {
+        // The chunk's scales, all loads in flight at once. One verdict for all
+        // the warps, and the last chunk's scales have been read.
+        const int steps = min(kChunk, kb1 - kc);
+        if ((stop = promo_any<32 * G::promo>(!ok))) break;
+        const int tid = (int)threadIdx.x - 64, e = tid & 31, rows = min(BM, a.T - m0);
+        if (e < steps) {
+#pragma unroll 8
+          for (int i = tid >> 5; i < rows; i += G::promo)
+            sx[e * kScalePitch + i] = a.xs[(size_t)(m0 + i) * a.nb + kc + e];
+          if (tid < 64) {  // warp i: weight block i of the tile
+            const int wb = n0 / 128 + (GATEUP ? 0 : tid >> 5);
+            const float* pw = GATEUP && tid >= 32 ? a.ws2 : a.ws;
+            sw[tid] = wb * 128 < a.N ? pw[(size_t)wb * a.nb + kc + e] : 0.0f;
+          }
         }
-        if (!tc::bar_wait_warp(&b.acc_full[u], (g / G::bufs) & 1)) {
-          if (lane == 0) abort_block(b, a.flags);
-          ok = false;
-          break;
-        }
-        tc::tc_fence_after();
-        const uint32_t buf = tl + (uint32_t)(u * NT);
-        const uint64_t sa2 = pack2(sa, sa), sb2 = GATEUP ? pack2(sb, sb) : sa2;
-        uint32_t d[32];
-        tc::tmem_ld32(buf + ca, d);
-        tc::tmem_ld32_wait(d);
+        asm volatile("barrier.sync 1, %0;" ::"n"(32 * G::promo) : "memory");
+        for (int st = 0; st < steps; ++st, ++g) {
+          const int u = g % G::bufs;
+          const float x = sx[st * kScalePitch + r];
+          const float sa = x * sw[blk * kChunk + st], sb = GATEUP ? x * sw[kChunk + st] : sa;
+          if (!tc::bar_wait_warp(&b.acc_full[u], (g / G::bufs) & 1)) {
+            if (lane == 0) abort_block(b, a.flags);
+            ok = false;
+            break;
+          }
+          tc::tc_fence_after();
+          const uint32_t buf = tl + (uint32_t)(u * NT);
+          const uint64_t sa2 = pack2(sa, sa), sb2 = GATEUP ? pack2(sb, sb) : sa2;
+          uint32_t d[16];
 #pragma unroll
-        for (int i = 0; i < 16; ++i) fma2(sum[i], d[2 * i], d[2 * i + 1], sa2);
-        if (G::cols == 64) {
-          tc::tmem_ld32(buf + cb, d);
-          tc::tmem_ld32_wait(d);
-        }
-        tc::tc_fence_before();
-        __syncwarp();
-        if (lane == 0) tc::bar_arrive(&b.acc_empty[u]);
-        if (G::cols == 64) {
+          for (int c = 0; c < G::cols / 16; ++c) {
+            tc::tmem_ld16u(buf + (c < 2 ? ca + 16 * c : cb + 16 * (c - 2)), d);
+            if (c == G::cols / 16 - 1) {
+              tc::tc_fence_before();
+              __syncwarp();
+              if (lane == 0) tc::bar_arrive(&b.acc_empty[u]);
+            }
 #pragma unroll
-          for (int i = 0; i < 16; ++i) fma2(sum[(16 + i) % kPairs], d[2 * i], d[2 * i + 1], sb2);
+            for (int i = 0; i < 8; ++i) fma2(sum[8 * c + i], d[2 * i], d[2 * i + 1], c < 2 ? sa2 : sb2);
+          }
         }
       }
+      if (stop) break;
       if (S > 1) {  // partial tile to shared memory (every stage has been consumed)
         if (live && ok) {
           float* red = reinterpret_cast<float*>(sm) + (size_t)r * G::red_pitch;
@@ -316,8 +329,7 @@ __global__ void __launch_bounds__(Geo<NT>::threads, 1)
         break;
       }
       if (!GATEUP) {
-        if (!ok) break;
-        if (live) {
+        if (live && ok) {
           __half* out = a.y + (size_t)row * a.N + n0 + ca;
           const int left = a.N - (n0 + (int)ca);
           if (a.N % 8 == 0) {
