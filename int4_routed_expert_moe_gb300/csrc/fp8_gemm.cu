@@ -17,6 +17,7 @@
 #include "common.h"
 #include "device.cuh"
 #include "fp8.cuh"
+#include "fp8_gemv.h"
 #include "kernels.h"
 #include "tc.cuh"
 
@@ -924,6 +925,7 @@ int launch_pair(GemmArgs a, const Operand& x, const Operand& w, const Operand* w
 }
 
 int product(const Operand& x, const Operand& w, int T, int N, int K, __half* y, int32_t* flags, cudaStream_t st) {
+  if (T <= kGemvMaxTokens) return fp8_gemv(x.q, x.s, T, w.q, w.s, N, K, y, st);
   int dev = 0, sms = 0;
   const int rc = current_device_sms(&dev, &sms);
   if (rc != MOE_OK) return rc;
@@ -1036,6 +1038,9 @@ int moe_shared_forward_fp8(const void* x, int T, int H, int Is, const void* wg, 
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const moe::Operand g = {static_cast<const uint8_t*>(wg), sg}, u = {static_cast<const uint8_t*>(wu), su},
                      d = {static_cast<const uint8_t*>(wd), sd};
+  if (T <= moe::kGemvMaxTokens)
+    return moe::fp8_gemv_ffn(static_cast<const __half*>(x), T, H, Is, g.q, sg, u.q, su, d.q, sd, xq, xs, hq,
+                             hs, static_cast<__half*>(y), st);
   int rc = moe::launch_quantize_fp8(static_cast<const __half*>(x), T, H, 1, xq, xs, st);
   if (rc != MOE_OK) return rc;
   if ((rc = moe::gate_up({xq, xs}, g, u, T, Is, H, hq, hs, flags, st)) != MOE_OK) return rc;

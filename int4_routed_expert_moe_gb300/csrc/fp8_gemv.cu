@@ -1,0 +1,288 @@
+// Block-scaled FP8 product for a few tokens: the weights are read once and
+// that is the cost (N K bytes against 2 T N K operations), so the kernel is a
+// weight stream. A block owns 16 rows of W, its warps take the 128-column
+// scale blocks in turn, and a warp's share of a block goes straight from
+// global memory to registers in 16-byte pieces.
+//
+// The dot products run on m16n8k32 MMAs (16 rows by 8 tokens): the order of
+// the reduction index inside a scale block is free as long as both operands
+// agree, so lane (g, q) loads 16-byte pieces q and q + 4 of rows g and g + 8
+// and of token g, and word i of each piece is an operand of MMA i. Staging W
+// through shared memory for tcgen05 costs about 2000 cycles before the first
+// MMA and some 600 per scale block here (barriers, copies and MMAs issued one
+// by one); this form starts with the loads.
+//
+// FFN form: the gate/up launch runs clusters of eight blocks, which together
+// own the 128 columns of one scale block of h; they exchange their tokens'
+// largest magnitudes through distributed shared memory and store h as codes.
+// A small x is quantised by every block for itself, a larger one by a launch
+// of its own.
+#include <algorithm>
+
+#include "common.h"
+#include "device.cuh"
+#include "fp8.cuh"
+#include "fp8_gemv.h"
+#include "kernels.h"
+
+namespace moe {
+namespace {
+
+constexpr int kWarps = 8;
+
+__device__ __forceinline__ void mma_m16n8k32(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                             uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k32.row.col.f32.e4m3.e4m3.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%0, %1, %2, %3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ uint32_t word(const uint4& v, int i) { return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w; }
+
+struct GemvArgs {
+  int T, N, K, nb;
+  const uint8_t* xq;  // codes [T][K] and scales [T][nb], or
+  const float* xs;
+  const __half* xf;   // FP16 activations [T][K]
+  const uint8_t *w, *w2;
+  const float *ws, *ws2;
+  __half* y;          // [T][N]
+  uint8_t* hq;        // gate/up: h codes [T][N] and scales [T][nbh]
+  float* hs;
+  int nbh;
+};
+
+// A scale block's weights of one matrix: pieces q and q + 4 of rows g, g + 8.
+struct WFrag {
+  uint4 lo[2], hi[2];  // [piece] of row g / row g + 8
+};
+__device__ __forceinline__ void load_w(WFrag& f, const uint8_t* lo, const uint8_t* hi, int k, int K) {
+#pragma unroll
+  for (int p = 0; p < 2; ++p) {
+    const bool on = k + 64 * p < K;
+    f.lo[p] = on && lo ? ld_stream_v4(lo + k + 64 * p) : make_uint4(0, 0, 0, 0);
+    f.hi[p] = on && hi ? ld_stream_v4(hi + k + 64 * p) : make_uint4(0, 0, 0, 0);
+  }
+}
+
+// Quantises x [T][K] into shared memory: unit u = t * nb + kb holds the codes
+// of one scale block, eight lanes of sixteen values.
+__device__ __forceinline__ void quantize_x(const GemvArgs& a, uint8_t (*codes)[fp8::kBlock], float* scales) {
+  const int sub = threadIdx.x & 7, units = a.T * a.nb;
+  for (int u0 = 0; u0 < units; u0 += 4 * kWarps) {
+    const int u = u0 + (int)(threadIdx.x >> 3), t = u / a.nb, c = (u - t * a.nb) * fp8::kBlock + 16 * sub;
+    uint4 in[2] = {};
+    if (u < units && c < a.K) {
+      const uint4* p = reinterpret_cast<const uint4*>(a.xf + (size_t)t * a.K + c);
+      in[0] = p[0];
+      in[1] = p[1];
+    }
+    uint32_t m = fp8::amax_bits(in[0], fp8::amax_bits(in[1], 0u));
+    m = max(m & 0xffffu, m >> 16);
+#pragma unroll
+    for (int o = 1; o < 8; o <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+    const fp8::BlockScale b = fp8::block_scale(m);
+    if (u < units) {
+      *reinterpret_cast<uint4*>(&codes[u][16 * sub]) = fp8::encode16(in, b.inv);
+      if (sub == 0) scales[u] = b.scale;
+    }
+  }
+  __syncthreads();
+}
+
+constexpr int kUnits = 128;  // scale blocks of x a block quantises for itself
+constexpr int kCluster = 8;  // blocks of 16 columns per scale block of h
+
+__device__ __forceinline__ void st_cluster(float* p, uint32_t rank, float v) {
+  uint32_t ra;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(ra)
+               : "r"(static_cast<uint32_t>(__cvta_generic_to_shared(p))), "r"(rank));
+  asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(ra), "f"(v) : "memory");
+}
+
+// NB: tiles of 8 tokens. GATEUP: gate and up rows, h out; else one matrix, y
+// out. XF: x comes as FP16. EARLY: the launch before this one is of the same
+// call and starts it only after everything before the call has finished, so
+// the weights may be read before that launch's results are waited for.
+template <int NB, bool GATEUP, bool XF, bool EARLY>
+__global__ void __launch_bounds__(32 * kWarps) fp8_gemv_kernel(const GemvArgs a) {
+  constexpr int NP = GATEUP ? 2 : 1;  // projections
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
+  if (GATEUP) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+  const int n0 = blockIdx.x * 16;
+  const bool on_lo = n0 + g < a.N, on_hi = n0 + g + 8 < a.N;
+  const int wb = min(n0, a.N - 1) / fp8::kBlock;
+  const uint8_t *lo[NP], *hi[NP];
+  const float* ws[NP];
+#pragma unroll
+  for (int p = 0; p < NP; ++p) {
+    const uint8_t* w = p ? a.w2 : a.w;
+    lo[p] = on_lo ? w + (size_t)(n0 + g) * a.K : nullptr;
+    hi[p] = on_hi ? w + (size_t)(n0 + g + 8) * a.K : nullptr;
+    ws[p] = (p ? a.ws2 : a.ws) + (size_t)wb * a.nb;
+  }
+  __shared__ __align__(16) uint8_t xcodes[XF ? kUnits : 1][fp8::kBlock];
+  __shared__ float xscales[XF ? kUnits : 1];
+  WFrag wf[NP];
+  if (!EARLY) griddep_wait();
+#pragma unroll
+  for (int p = 0; p < NP; ++p) load_w(wf[p], lo[p], hi[p], warp * fp8::kBlock + 16 * q, a.K);
+  if (EARLY) griddep_wait();
+  griddep_launch_dependents();
+  if (XF) quantize_x(a, xcodes, xscales);
+
+  float tot[NP][NB][4] = {};
+  for (int kb = warp; kb < a.nb; kb += kWarps) {
+    const int k = kb * fp8::kBlock + 16 * q;
+    uint4 x[NB][2];
+    float s0[NB], s1[NB];  // scales of tokens 2q and 2q + 1 of each tile
+#pragma unroll
+    for (int i = 0; i < NB; ++i) {
+      const int t = 8 * i + g, ta = 8 * i + 2 * q;
+#pragma unroll
+      for (int p = 0; p < 2; ++p) {
+        x[i][p] = make_uint4(0, 0, 0, 0);
+        if (XF) {
+          if (t < a.T) x[i][p] = *reinterpret_cast<const uint4*>(&xcodes[t * a.nb + kb][16 * q + 64 * p]);
+        } else if (t < a.T && k + 64 * p < a.K) {
+          x[i][p] = *reinterpret_cast<const uint4*>(a.xq + (size_t)t * a.K + k + 64 * p);
+        }
+      }
+      s0[i] = ta < a.T ? (XF ? xscales[ta * a.nb + kb] : a.xs[(size_t)ta * a.nb + kb]) : 0.0f;
+      s1[i] = ta + 1 < a.T ? (XF ? xscales[(ta + 1) * a.nb + kb] : a.xs[(size_t)(ta + 1) * a.nb + kb]) : 0.0f;
+    }
+    float sw[NP];
+#pragma unroll
+    for (int p = 0; p < NP; ++p) sw[p] = ws[p][kb];
+    WFrag cur[NP];
+#pragma unroll
+    for (int p = 0; p < NP; ++p) {
+      cur[p] = wf[p];
+      load_w(wf[p], lo[p], hi[p], k + kWarps * fp8::kBlock, a.K);  // the next block's, past K: nothing
+    }
+#pragma unroll
+    for (int p = 0; p < NP; ++p)
+#pragma unroll
+      for (int i = 0; i < NB; ++i) {
+        float c[4] = {};
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          mma_m16n8k32(c, word(cur[p].lo[0], j), word(cur[p].hi[0], j), word(cur[p].lo[1], j), word(cur[p].hi[1], j),
+                       word(x[i][0], j), word(x[i][1], j));
+        const float u0 = s0[i] * sw[p], u1 = s1[i] * sw[p];
+        tot[p][i][0] = fmaf(c[0], u0, tot[p][i][0]);
+        tot[p][i][1] = fmaf(c[1], u1, tot[p][i][1]);
+        tot[p][i][2] = fmaf(c[2], u0, tot[p][i][2]);
+        tot[p][i][3] = fmaf(c[3], u1, tot[p][i][3]);
+      }
+  }
+  // The warps' sums, added in warp order: thread (t, n) of 16 tokens.
+  __shared__ float red[kWarps][NP][8 * NB][17];
+#pragma unroll
+  for (int p = 0; p < NP; ++p)
+#pragma unroll
+    for (int i = 0; i < NB; ++i)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) red[warp][p][8 * i + 2 * q + (e & 1)][g + 8 * (e >> 1)] = tot[p][i][e];
+  __syncthreads();
+  static_assert(16 * 8 * NB <= 32 * kWarps, "a thread per (token, row)");
+  const int t = threadIdx.x >> 4, n = threadIdx.x & 15;
+  const bool on = t < min(8 * NB, a.T);
+  float v[NP] = {};
+  if (on) {
+#pragma unroll
+    for (int p = 0; p < NP; ++p)
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) v[p] += red[w][p][t][n];
+  }
+  if (!GATEUP) {
+    if (on && n0 + n < a.N) a.y[(size_t)t * a.N + n0 + n] = __float2half_rn(v[0]);
+    return;
+  }
+  // h, and its block's largest magnitude: 16 columns here, the cluster's 128.
+  const float h = silu_fast(v[0]) * v[NP - 1];
+  float m = fabsf(h) < INFINITY ? fabsf(h) : INFINITY;
+#pragma unroll
+  for (int o = 1; o < 16; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  __shared__ float amax[kCluster][8 * NB];
+  uint32_t rank;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");  // every block of the cluster has started
+  if (on && n < kCluster) st_cluster(&amax[rank][t], (uint32_t)n, m);
+  __syncwarp();
+  asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
+  if (!on) return;
+#pragma unroll
+  for (int r = 0; r < kCluster; ++r) m = fmaxf(m, amax[r][t]);
+  const fp8::BlockScale b = fp8::block_scale(m);
+  if (n0 + n < a.N) a.hq[(size_t)t * a.N + n0 + n] = (uint8_t)fp8::encode2(h * b.inv, 0.0f);
+  if (rank == 0 && n == 0) a.hs[(size_t)t * a.nbh + n0 / fp8::kBlock] = b.scale;
+}
+
+template <int NB, bool GATEUP, bool XF, bool EARLY>
+int launch(const GemvArgs& a, cudaStream_t st) {
+  cudaLaunchConfig_t cfg = {};
+  const int tiles = (a.N + 15) / 16;
+  cfg.gridDim = dim3((unsigned)(GATEUP ? (tiles + kCluster - 1) / kCluster * kCluster : tiles));
+  cfg.blockDim = dim3(32 * kWarps);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = kCluster;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = GATEUP ? 2 : 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, fp8_gemv_kernel<NB, GATEUP, XF, EARLY>, a);
+  if (e != cudaSuccess) return fail(MOE_ERR_CUDA, "fp8 gemv launch: %s", cudaGetErrorString(e));
+  return MOE_OK;
+}
+template <bool GATEUP, bool XF, bool EARLY>
+int launch(const GemvArgs& a, cudaStream_t st) {
+  return a.T <= 8 ? launch<1, GATEUP, XF, EARLY>(a, st) : launch<2, GATEUP, XF, EARLY>(a, st);
+}
+
+}  // namespace
+
+int fp8_gemv(const uint8_t* xq, const float* xs, int T, const uint8_t* wq, const float* ws, int N, int K, __half* y,
+             cudaStream_t st) {
+  GemvArgs a = {};
+  a.T = T; a.N = N; a.K = K;
+  a.nb = (K + fp8::kBlock - 1) / fp8::kBlock;
+  a.xq = xq; a.xs = xs;
+  a.w = wq; a.ws = ws;
+  a.y = y;
+  return launch<false, false, false>(a, st);
+}
+
+int fp8_gemv_ffn(const __half* x, int T, int H, int Is, const uint8_t* wg, const float* sg, const uint8_t* wu,
+                 const float* su, const uint8_t* wd, const float* sd, uint8_t* xq, float* xs, uint8_t* hq, float* hs,
+                 __half* y, cudaStream_t st) {
+  GemvArgs a = {};
+  a.T = T; a.N = Is; a.K = H;
+  a.nb = (H + fp8::kBlock - 1) / fp8::kBlock;
+  a.w = wg; a.ws = sg;
+  a.w2 = wu; a.ws2 = su;
+  a.hq = hq; a.hs = hs;
+  a.nbh = (Is + fp8::kBlock - 1) / fp8::kBlock;
+  int rc;
+  if (T * a.nb <= kUnits) {
+    a.xf = x;
+    rc = launch<true, true, false>(a, st);
+  } else {
+    if ((rc = launch_quantize_fp8(x, T, H, 1, xq, xs, st)) != MOE_OK) return rc;
+    a.xq = xq; a.xs = xs;
+    rc = launch<true, false, true>(a, st);
+  }
+  if (rc != MOE_OK) return rc;
+  a.N = H; a.K = Is;
+  a.nb = a.nbh;
+  a.xq = hq; a.xs = hs;
+  a.w = wd; a.ws = sd;
+  a.y = y;
+  return launch<false, false, true>(a, st);
+}
+
+}  // namespace moe

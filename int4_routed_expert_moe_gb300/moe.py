@@ -185,6 +185,11 @@ def _dev(t: torch.Tensor | None, dtype, name: str, numel: int | None = None, nul
         if nullable:
             return None
         raise ValueError(f"{name} is required")
+    try:  # the usual case in few steps; what is wrong is looked for below
+        if t.is_cuda and t.dtype is dtype and t.is_contiguous() and (numel is None or t.numel() >= numel):
+            return t.data_ptr()
+    except AttributeError:
+        pass
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
     if dtype is not None and t.dtype != dtype:
