@@ -106,7 +106,7 @@ __device__ __forceinline__ void st_cluster(float* p, uint32_t rank, float v) {
 // call and starts it only after everything before the call has finished, so
 // the weights may be read before that launch's results are waited for.
 template <int NB, bool GATEUP, bool XF, bool EARLY>
-__global__ void __launch_bounds__(32 * kWarps) fp8_gemv_kernel(const GemvArgs a) {
+__global__ void __launch_bounds__(32 * kWarps, 2) fp8_gemv_kernel(const GemvArgs a) {
   constexpr int NP = GATEUP ? 2 : 1;  // projections
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
   if (GATEUP) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
@@ -124,58 +124,72 @@ __global__ void __launch_bounds__(32 * kWarps) fp8_gemv_kernel(const GemvArgs a)
   }
   __shared__ __align__(16) uint8_t xcodes[XF ? kUnits : 1][fp8::kBlock];
   __shared__ float xscales[XF ? kUnits : 1];
-  WFrag wf[NP];
-  if (!EARLY) griddep_wait();
+  // A step is one scale block; a warp takes steps warp, warp + 8, ... with the
+  // loads of the next DEPTH on their way.
+  constexpr int DEPTH = NB == 1 ? 2 : 1;
+  WFrag wf[DEPTH][NP];
+  uint4 x[DEPTH][NB][2];
+  float s0[DEPTH][NB], s1[DEPTH][NB], sw[DEPTH][NP];  // scales of tokens 2q and 2q + 1 of each tile, of the rows
+  auto load_weights = [&](int d, int kb) {
 #pragma unroll
-  for (int p = 0; p < NP; ++p) load_w(wf[p], lo[p], hi[p], warp * fp8::kBlock + 16 * q, a.K);
-  if (EARLY) griddep_wait();
-  griddep_launch_dependents();
-  if (XF) quantize_x(a, xcodes, xscales);
-
-  float tot[NP][NB][4] = {};
-  for (int kb = warp; kb < a.nb; kb += kWarps) {
+    for (int p = 0; p < NP; ++p) {
+      load_w(wf[d][p], lo[p], hi[p], kb * fp8::kBlock + 16 * q, a.K);  // past K: nothing
+      sw[d][p] = kb < a.nb ? ws[p][kb] : 0.0f;
+    }
+  };
+  auto load_tokens = [&](int d, int kb) {
     const int k = kb * fp8::kBlock + 16 * q;
-    uint4 x[NB][2];
-    float s0[NB], s1[NB];  // scales of tokens 2q and 2q + 1 of each tile
+    const bool in = kb < a.nb;
 #pragma unroll
     for (int i = 0; i < NB; ++i) {
       const int t = 8 * i + g, ta = 8 * i + 2 * q;
 #pragma unroll
       for (int p = 0; p < 2; ++p) {
-        x[i][p] = make_uint4(0, 0, 0, 0);
+        x[d][i][p] = make_uint4(0, 0, 0, 0);
         if (XF) {
-          if (t < a.T) x[i][p] = *reinterpret_cast<const uint4*>(&xcodes[t * a.nb + kb][16 * q + 64 * p]);
+          if (in && t < a.T) x[d][i][p] = *reinterpret_cast<const uint4*>(&xcodes[t * a.nb + kb][16 * q + 64 * p]);
         } else if (t < a.T && k + 64 * p < a.K) {
-          x[i][p] = *reinterpret_cast<const uint4*>(a.xq + (size_t)t * a.K + k + 64 * p);
+          x[d][i][p] = *reinterpret_cast<const uint4*>(a.xq + (size_t)t * a.K + k + 64 * p);
         }
       }
-      s0[i] = ta < a.T ? (XF ? xscales[ta * a.nb + kb] : a.xs[(size_t)ta * a.nb + kb]) : 0.0f;
-      s1[i] = ta + 1 < a.T ? (XF ? xscales[(ta + 1) * a.nb + kb] : a.xs[(size_t)(ta + 1) * a.nb + kb]) : 0.0f;
+      s0[d][i] = in && ta < a.T ? (XF ? xscales[ta * a.nb + kb] : a.xs[(size_t)ta * a.nb + kb]) : 0.0f;
+      s1[d][i] = in && ta + 1 < a.T ? (XF ? xscales[(ta + 1) * a.nb + kb] : a.xs[(size_t)(ta + 1) * a.nb + kb]) : 0.0f;
     }
-    float sw[NP];
+  };
+  if (!EARLY) griddep_wait();
 #pragma unroll
-    for (int p = 0; p < NP; ++p) sw[p] = ws[p][kb];
-    WFrag cur[NP];
+  for (int d = 0; d < DEPTH; ++d) load_weights(d, warp + d * kWarps);
+  if (EARLY) griddep_wait();
+  griddep_launch_dependents();
+  if (XF) quantize_x(a, xcodes, xscales);
 #pragma unroll
-    for (int p = 0; p < NP; ++p) {
-      cur[p] = wf[p];
-      load_w(wf[p], lo[p], hi[p], k + kWarps * fp8::kBlock, a.K);  // the next block's, past K: nothing
+  for (int d = 0; d < DEPTH; ++d) load_tokens(d, warp + d * kWarps);
+
+  float tot[NP][NB][4] = {};
+  for (int kb0 = warp; kb0 < a.nb; kb0 += DEPTH * kWarps) {
+#pragma unroll
+    for (int d = 0; d < DEPTH; ++d) {
+      const int kb = kb0 + d * kWarps;
+      if (kb >= a.nb) break;
+#pragma unroll
+      for (int p = 0; p < NP; ++p)
+#pragma unroll
+        for (int i = 0; i < NB; ++i) {
+          const WFrag& w = wf[d][p];
+          float c[4] = {};
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            mma_m16n8k32(c, word(w.lo[0], j), word(w.hi[0], j), word(w.lo[1], j), word(w.hi[1], j),
+                         word(x[d][i][0], j), word(x[d][i][1], j));
+          const float u0 = s0[d][i] * sw[d][p], u1 = s1[d][i] * sw[d][p];
+          tot[p][i][0] = fmaf(c[0], u0, tot[p][i][0]);
+          tot[p][i][1] = fmaf(c[1], u1, tot[p][i][1]);
+          tot[p][i][2] = fmaf(c[2], u0, tot[p][i][2]);
+          tot[p][i][3] = fmaf(c[3], u1, tot[p][i][3]);
+        }
+      load_weights(d, kb + DEPTH * kWarps);
+      load_tokens(d, kb + DEPTH * kWarps);
     }
-#pragma unroll
-    for (int p = 0; p < NP; ++p)
-#pragma unroll
-      for (int i = 0; i < NB; ++i) {
-        float c[4] = {};
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-          mma_m16n8k32(c, word(cur[p].lo[0], j), word(cur[p].hi[0], j), word(cur[p].lo[1], j), word(cur[p].hi[1], j),
-                       word(x[i][0], j), word(x[i][1], j));
-        const float u0 = s0[i] * sw[p], u1 = s1[i] * sw[p];
-        tot[p][i][0] = fmaf(c[0], u0, tot[p][i][0]);
-        tot[p][i][1] = fmaf(c[1], u1, tot[p][i][1]);
-        tot[p][i][2] = fmaf(c[2], u0, tot[p][i][2]);
-        tot[p][i][3] = fmaf(c[3], u1, tot[p][i][3]);
-      }
   }
   // The warps' sums, added in warp order: thread (t, n) of 16 tokens.
   __shared__ float red[kWarps][NP][8 * NB][17];
