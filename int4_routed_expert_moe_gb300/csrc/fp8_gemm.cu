@@ -142,19 +142,23 @@ __device__ __forceinline__ bool promo_any(bool q) {
   return r != 0;
 }
 
+// The larger of the two, NaN if one is.
+__device__ __forceinline__ float fmax_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
 // h = silu(gate) * up of N values in place of gate, and their largest
-// magnitude (infinite if one of them is not finite).
+// magnitude (NaN or infinite if one of them is).
 template <int N>
 __device__ __forceinline__ float swiglu(float (&gt)[N], const float (&up)[N]) {
   float m = 0.0f;
-  bool bad = false;
 #pragma unroll
   for (int i = 0; i < N; ++i) {
     gt[i] = silu_fast(gt[i]) * up[i];
-    bad |= !(fabsf(gt[i]) < INFINITY);
-    m = fmaxf(m, fabsf(gt[i]));
+    m = fmax_nan(m, fabsf(gt[i]));
   }
-  return bad ? INFINITY : m;
+  return m;
 }
 
 // GATEUP: the tile is 128 rows of W_g and the same 128 of W_u; the epilogue
@@ -366,7 +370,7 @@ __global__ void __launch_bounds__(Geo<NT>::threads, 1)
         b.amax[j4 * BM + r] = m;
         asm volatile("barrier.sync 1, %0;" ::"n"(32 * G::promo) : "memory");
 #pragma unroll
-        for (int w = 0; w < 4; ++w) m = fmaxf(m, b.amax[w * BM + r]);
+        for (int w = 0; w < 4; ++w) m = fmax_nan(m, b.amax[w * BM + r]);
         // Maxima read before the next tile's; one verdict for all the warps.
         if (promo_any<32 * G::promo>(!ok || is_aborted(b))) break;
         const fp8::BlockScale bs = fp8::block_scale(m);
@@ -426,7 +430,7 @@ __global__ void __launch_bounds__(Geo<NT>::threads, 1)
         }
         float m = swiglu(h, up);
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+        for (int o = 16; o > 0; o >>= 1) m = fmax_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
         const fp8::BlockScale bs = fp8::block_scale(m);
         if (n0 + 4 * lane < a.N)
           *reinterpret_cast<uint32_t*>(a.hq + (size_t)(m0 + r) * a.N + n0 + 4 * lane) =
@@ -450,7 +454,7 @@ __global__ void __launch_bounds__(Geo<NT>::threads, 1)
 // scales, 4-11 promotion (a lane quarter, 128 columns each).
 struct Pair {
   static constexpr int promo = 8, threads = 384;
-  static constexpr int stages = 4, bufs = 2, slots = 8;
+  static constexpr int stages = 4, bufs = 2, groups = 2, slots = 4 * groups;  // scales: groups of four steps
   static constexpr uint32_t stage = kABytes + 128 * BK;  // per block: 128 tokens, 128 rows of W
   static constexpr uint32_t off_out = stages * stage;    // [promo][2][32 rows][64 columns] FP16
   static constexpr uint32_t off_scale = off_out + promo * 8192;
@@ -470,8 +474,8 @@ __device__ __forceinline__ PairBars pair_bars(uint8_t* p) {
   b.empty = q; q += Pair::stages;
   b.acc_full = q; q += Pair::bufs;
   b.acc_empty = q; q += Pair::bufs;
-  b.sc_full = q; q += Pair::slots;
-  b.sc_empty = q; q += Pair::slots;
+  b.sc_full = q; q += Pair::groups;
+  b.sc_empty = q; q += Pair::groups;
   b.tmem_slot = reinterpret_cast<uint32_t*>(q);
   b.abort = reinterpret_cast<int*>(b.tmem_slot + 1);
   b.amax = reinterpret_cast<float*>(p + 1024);
@@ -480,6 +484,29 @@ __device__ __forceinline__ PairBars pair_bars(uint8_t* p) {
 __device__ __forceinline__ void pair_abort(const PairBars& b, int32_t* flags) {
   atomicOr(flags, 4);
   *reinterpret_cast<volatile int*>(b.abort) = 1;
+}
+
+// A promotion warp's wait: no verdict to agree on. After a wait that ran out
+// (here or in another role of the block) the rest return at once, the warp
+// walks through its tiles without results, and every barrier is met.
+// (Shared-memory addresses, not pointers: the promotion loop is short of
+// registers.)
+__device__ __forceinline__ void pair_wait(uint32_t bar, uint32_t parity, uint32_t abort, int32_t* flags) {
+  if (!tc::bar_try_wait_at(bar, parity)) {
+    const uint64_t t0 = tc::global_ns();
+    for (;;) {
+      if (tc::bar_try_wait_at(bar, parity)) break;
+      uint32_t gone;
+      asm volatile("ld.volatile.shared::cta.u32 %0, [%1];" : "=r"(gone) : "r"(abort) : "memory");
+      if (gone) break;
+      if (tc::global_ns() - t0 > tc::kWaitNs) {
+        atomicOr(flags, 4);
+        asm volatile("st.volatile.shared::cta.u32 [%0], %1;" ::"r"(abort), "r"(1) : "memory");
+        break;
+      }
+    }
+  }
+  __syncwarp();
 }
 
 template <bool GATEUP>
@@ -496,7 +523,7 @@ __global__ void __launch_bounds__(Pair::threads, 1)
   if (threadIdx.x == 0) {
     tc::tma_prefetch_desc(&map_x);
     tc::tma_prefetch_desc(rank && GATEUP ? &map_w2 : &map_w);
-    if (!GATEUP) tc::tma_prefetch_desc(&map_y);
+    tc::tma_prefetch_desc(&map_y);
     for (int s = 0; s < G::stages; ++s) {
       tc::bar_init(&b.full[s], 1);
       tc::bar_init(&b.empty[s], 1);
@@ -505,7 +532,7 @@ __global__ void __launch_bounds__(Pair::threads, 1)
       tc::bar_init(&b.acc_full[s], 1);
       tc::bar_init(&b.acc_empty[s], 2 * G::promo);
     }
-    for (int s = 0; s < G::slots; ++s) {
+    for (int s = 0; s < G::groups; ++s) {
       tc::bar_init(&b.sc_full[s], 2);
       tc::bar_init(&b.sc_empty[s], G::promo);
     }
@@ -525,21 +552,22 @@ __global__ void __launch_bounds__(Pair::threads, 1)
   const int first = (int)blockIdx.x / 2, stride = (int)gridDim.x / 2;
   constexpr int kN = GATEUP ? 128 : 256;  // output columns per tile
 
-  // 384 x 168 registers at launch = 128 x 104 + 256 x 200.
+  // 384 x 168 registers at launch = 128 x 72 + 256 x 216.
   if (warp >= 4) {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
     // Lane quarter q4; 128 columns from 128 j2 (gate/up: 64 of each from
-    // 64 j2), taken from tensor memory 32 at a time, the next 32 on their way
-    // while the FMAs of the last run.
+    // 64 j2), taken from tensor memory 32 at a time (a load returns in some 35
+    // cycles; the other warp of the scheduler has FMAs to issue meanwhile).
     const int q4 = warp & 3, j2 = (warp - 4) >> 2;
     const uint32_t tl = tmem + ((uint32_t)(32 * q4) << 16);
     const uint32_t c0 = GATEUP ? 64 * j2 : 128 * j2;
     auto col = [&](int c) { return GATEUP && c >= 2 ? 128 + c0 + 32 * (c - 2) : c0 + 32 * c; };
     const float* sca = reinterpret_cast<const float*>(sm + G::off_scale) + (GATEUP ? 0 : j2 * BM) + 32 * q4 + lane;
+    const uint32_t acc_full = tc::smem_addr(b.acc_full), sc_full = tc::smem_addr(b.sc_full);
+    const uint32_t abort = tc::smem_addr(b.abort);
     const uint32_t acc_empty0 = tc::map_rank(tc::smem_addr(&b.acc_empty[0]), 0);
     uint8_t* out = sm + G::off_out + (warp - 4) * 8192;
-    int g = 0;
-    bool ok = true;
+    int g = 0, gg = 0;
     for (int tile = first; tile < a.tiles; tile += stride) {
       const int m0 = (tile % a.mt) * 256 + rank * BM, n0 = (tile / a.mt) * kN;
       const int r = 32 * q4 + lane, row = m0 + r;
@@ -547,40 +575,34 @@ __global__ void __launch_bounds__(Pair::threads, 1)
 #pragma unroll
       for (int i = 0; i < 64; ++i) sum[i] = 0;
       for (int kb = 0; kb < nb; ++kb, ++g) {
-        const int u = g % G::bufs, s = g % G::slots;
-        if (!tc::bar_wait_warp(&b.sc_full[s], (g / G::slots) & 1)) {
-          ok = false;
-          break;
-        }
-        const float sa = sca[s * 2 * BM], sb = GATEUP ? sca[s * 2 * BM + BM] : sa;
-        if (!tc::bar_wait_warp(&b.acc_full[u], (g / G::bufs) & 1)) {
-          ok = false;
-          break;
-        }
+        const int u = g % G::bufs, e = kb & 3;
+        if (e == 0) pair_wait(sc_full + 8 * (gg % G::groups), (gg / G::groups) & 1, abort, a.flags);
+        const float* sc = sca + ((gg % G::groups) * 4 + e) * 2 * BM;
+        const float sa = sc[0], sb = GATEUP ? sc[BM] : sa;
+        pair_wait(acc_full + 8 * u, (g / G::bufs) & 1, abort, a.flags);
         tc::tc_fence_after();
         const uint32_t buf = tl + (uint32_t)(u * 256);
-        uint32_t d[2][32];
-        tc::tmem_ld32(buf + col(0), d[0]);
         const uint64_t sa2 = pack2(sa, sa), sb2 = GATEUP ? pack2(sb, sb) : sa2;
-        if (lane == 0) tc::bar_arrive(&b.sc_empty[s]);
+        if (e == 3 || kb == nb - 1) {
+          if (lane == 0) tc::bar_arrive_at(sc_full + 8 * G::groups + 8 * (gg % G::groups));
+          ++gg;
+        }
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
-          tc::tmem_ld32_wait(d[c & 1]);
-          if (c < 3) {
-            tc::tmem_ld32(buf + col(c + 1), d[(c + 1) & 1]);
-          } else {
+          uint32_t d[32];
+          tc::tmem_ld32(buf + col(c), d);
+          tc::tmem_ld32_wait(d);
+          if (c == 3) {
             tc::tc_fence_before();
-            __syncwarp();
             if (lane == 0) tc::bar_arrive_cluster(acc_empty0 + 8 * u);
           }
 #pragma unroll
-          for (int i = 0; i < 16; ++i)
-            fma2(sum[16 * c + i], d[c & 1][2 * i], d[c & 1][2 * i + 1], c < 2 ? sa2 : sb2);
+          for (int i = 0; i < 16; ++i) fma2(sum[16 * c + i], d[2 * i], d[2 * i + 1], c < 2 ? sa2 : sb2);
         }
       }
-      if (!ok && lane == 0) pair_abort(b, a.flags);
+      const bool ok = *reinterpret_cast<volatile int*>(b.abort) == 0;
       if (!GATEUP) {
-        if (!ok) break;
+        if (!ok) continue;
         if (a.N % 8 == 0) {
           // Rows of 64 FP16 columns in the 128-byte swizzle, stored by TMA.
           if (lane == 0) tc::tma_store_wait_read();
@@ -622,32 +644,32 @@ __global__ void __launch_bounds__(Pair::threads, 1)
           up[2 * i] = q.x; up[2 * i + 1] = q.y;
         }
         float m = swiglu(h, up);
+        if (lane == 0) tc::tma_store_wait_read();
+        __syncwarp();
         b.amax[j2 * BM + r] = m;
         asm volatile("barrier.sync 1, %0;" ::"n"(32 * G::promo) : "memory");
-        m = fmaxf(m, b.amax[(j2 ^ 1) * BM + r]);
-        // Maxima read before the next tile's; one verdict for all the warps.
-        if (promo_any<32 * G::promo>(!ok)) break;
+        m = fmax_nan(m, b.amax[(j2 ^ 1) * BM + r]);
         const fp8::BlockScale bs = fp8::block_scale(m);
-        if (row < a.T) {
-          uint8_t* o = a.hq + (size_t)row * a.N + n0 + c0;
-          if (n0 + (int)c0 < a.N) {  // Is is a multiple of 64
 #pragma unroll
-            for (int i = 0; i < 64; i += 16) {
-              uint32_t c[4];
+        for (int i = 0; i < 64; i += 16) {
+          uint32_t c[4];
 #pragma unroll
-              for (int e = 0; e < 4; ++e)
-                c[e] = fp8::encode4(h[i + 4 * e] * bs.inv, h[i + 4 * e + 1] * bs.inv, h[i + 4 * e + 2] * bs.inv,
-                                    h[i + 4 * e + 3] * bs.inv);
-              *reinterpret_cast<uint4*>(o + i) = make_uint4(c[0], c[1], c[2], c[3]);
-            }
-          }
-          if (j2 == 0) a.hs[(size_t)row * a.nbh + n0 / 128] = bs.scale;
+          for (int e = 0; e < 4; ++e)
+            c[e] = fp8::encode4(h[i + 4 * e] * bs.inv, h[i + 4 * e + 1] * bs.inv, h[i + 4 * e + 2] * bs.inv,
+                                h[i + 4 * e + 3] * bs.inv);
+          *reinterpret_cast<uint4*>(out + 64 * lane + i) = make_uint4(c[0], c[1], c[2], c[3]);
         }
+        tc::fence_async_smem();
+        // The maxima have been read before the next tile's are written.
+        asm volatile("barrier.sync 1, %0;" ::"n"(32 * G::promo) : "memory");
+        const int y0 = m0 + 32 * q4, x0 = n0 + (int)c0;  // rows of 64 codes; Is is a multiple of 64
+        if (ok && lane == 0 && y0 < a.T && x0 < a.N) tc::tma_store_2d(&map_y, x0, y0, out);
+        if (ok && j2 == 0 && row < a.T) a.hs[(size_t)row * a.nbh + n0 / 128] = bs.scale;
       }
     }
-    if (!GATEUP && lane == 0) tc::tma_store_wait_all();
+    if (lane == 0) tc::tma_store_wait_all();
   } else {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
     if (warp == 0) {
       // Both blocks' loads complete on the leading block's barrier.
       const CUtensorMap* mw = GATEUP && rank ? &map_w2 : &map_w;
@@ -708,72 +730,51 @@ __global__ void __launch_bounds__(Pair::threads, 1)
         }
       }
     } else if (warp < 4) {
-      // Scales: the products xs * ws of a step, [2 weight blocks][128 tokens],
-      // four steps of two tokens per lane loaded at a time, one group ahead.
+      // Scales: the products xs * ws of a step, [2 weight blocks][128 tokens];
+      // a group of four steps at a time, two tokens per lane. Up to two groups
+      // ahead of the promotion, which hides the loads.
       const int r0 = (warp - 2) * 64 + lane;
       const bool vec = (nb & 3) == 0 && (reinterpret_cast<uintptr_t>(a.xs) & 15) == 0;
-      float* sc = reinterpret_cast<float*>(sm + G::off_scale);
+      float* sc = reinterpret_cast<float*>(sm + G::off_scale) + r0;
       int g = 0;
       bool ok = true;
       for (int tile = first; tile < a.tiles && ok; tile += stride) {
         const int m0 = (tile % a.mt) * 256 + rank * BM, n0 = (tile / a.mt) * kN;
-        const int wb = n0 / 128;
-        const float* pw0 = a.ws + (size_t)wb * nb;
-        const float* pw1 = GATEUP ? a.ws2 + (size_t)wb * nb : (n0 + 128 < a.N ? pw0 + nb : nullptr);
-        const float* px[2];
-        bool live[2];
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          live[i] = m0 + r0 + 32 * i < a.T;
-          px[i] = a.xs + (size_t)(live[i] ? m0 + r0 + 32 * i : 0) * nb;
-        }
-        float x[2][4], w0[4], w1[4];
-        auto load = [&](int kb) {
+        const float* pw0 = a.ws + (size_t)(n0 / 128) * nb;
+        const float* pw1 = GATEUP ? a.ws2 + (size_t)(n0 / 128) * nb : (n0 + 128 < a.N ? pw0 + nb : nullptr);
+        for (int kb = 0; kb < nb; kb += 4, ++g) {
+          float x[2][4], w[2][4];
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
-            if (vec && live[i]) {
-              const float4 v = *reinterpret_cast<const float4*>(px[i] + kb);
+            const bool live = m0 + r0 + 32 * i < a.T;
+            const float* px = a.xs + (size_t)(m0 + r0 + 32 * i) * nb + kb;
+            if (vec) {
+              const float4 v = live ? *reinterpret_cast<const float4*>(px) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
               x[i][0] = v.x; x[i][1] = v.y; x[i][2] = v.z; x[i][3] = v.w;
             } else {
 #pragma unroll
-              for (int e = 0; e < 4; ++e) x[i][e] = live[i] && kb + e < nb ? px[i][kb + e] : 0.0f;
+              for (int e = 0; e < 4; ++e) x[i][e] = live && kb + e < nb ? px[e] : 0.0f;
             }
           }
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            w0[e] = kb + e < nb ? pw0[kb + e] : 0.0f;
-            w1[e] = pw1 && kb + e < nb ? pw1[kb + e] : 0.0f;
+            w[0][e] = kb + e < nb ? pw0[kb + e] : 0.0f;
+            w[1][e] = pw1 && kb + e < nb ? pw1[kb + e] : 0.0f;
           }
-        };
-        load(0);
-        for (int kb = 0; kb < nb && ok; kb += 4) {
-          float p[4][2][2];
+          const int s = g % G::groups;
+          if (g >= G::groups && !tc::bar_wait_warp(&b.sc_empty[s], ((g / G::groups) - 1) & 1)) {
+            if (lane == 0) pair_abort(b, a.flags);
+            ok = false;
+            break;
+          }
 #pragma unroll
           for (int e = 0; e < 4; ++e)
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              p[e][0][i] = x[i][e] * w0[e];
-              p[e][1][i] = x[i][e] * w1[e];
-            }
-          if (kb + 4 < nb) load(kb + 4);
+            for (int j = 0; j < 2; ++j)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            if (kb + e >= nb) break;
-            const int s = g % G::slots;
-            if (g >= G::slots && !tc::bar_wait_warp(&b.sc_empty[s], ((g / G::slots) - 1) & 1)) {
-              if (lane == 0) pair_abort(b, a.flags);
-              ok = false;
-              break;
-            }
-            float* d = sc + s * 2 * BM + r0;
-            d[0] = p[e][0][0];
-            d[32] = p[e][0][1];
-            d[BM] = p[e][1][0];
-            d[BM + 32] = p[e][1][1];
-            __syncwarp();
-            if (lane == 0) tc::bar_arrive(&b.sc_full[s]);
-            ++g;
-          }
+              for (int i = 0; i < 2; ++i) sc[((4 * s + e) * 2 + j) * BM + 32 * i] = x[i][e] * w[j][e];
+          __syncwarp();
+          if (lane == 0) tc::bar_arrive(&b.sc_full[s]);
         }
       }
     }
@@ -898,8 +899,14 @@ int launch_pair(GemmArgs a, const Operand& x, const Operand& w, const Operand* w
   mw2 = mw;
   if (w2 && (rc = code_map(&mw2, w2->q, a.K, a.N, 128)) != MOE_OK) return rc;
   my = mx;
-  if (!GATEUP && a.N % 8 == 0) {
-    const uint64_t dims[2] = {(uint64_t)a.N, (uint64_t)a.T};
+  const uint64_t dims[2] = {(uint64_t)a.N, (uint64_t)a.T};
+  if (GATEUP) {
+    const uint64_t str[1] = {(uint64_t)a.N};
+    const uint32_t box[2] = {64, 32};
+    if ((rc = encode_tensor_map(&my, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, a.hq, dims, str, box,
+                                CU_TENSOR_MAP_SWIZZLE_NONE)) != MOE_OK)
+      return rc;
+  } else if (a.N % 8 == 0) {
     const uint64_t str[1] = {(uint64_t)a.N * 2};
     const uint32_t box[2] = {64, 32};
     if ((rc = encode_tensor_map(&my, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, a.y, dims, str, box,
