@@ -150,13 +150,33 @@ __device__ __forceinline__ float fmax_nan(float a, float b) {
 }
 // h = silu(gate) * up of N values in place of gate, and their largest
 // magnitude (NaN or infinite if one of them is).
+// The special-function unit's own 2^x and 1/x (relative errors about 2^-22).
+constexpr float kLog2e = 1.4426950408889634f;
+__device__ __forceinline__ float exp2_approx(float v) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+  return r;
+}
+__device__ __forceinline__ float rcp_approx(float v) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+  return r;
+}
+// silu(v) = v / (1 + exp(-v)); two values share one reciprocal, 1/a = b / (ab):
+// the special-function unit paces this epilogue (16 results per cycle and SM).
+// exp is capped at 2^60, so that ab stays finite: silu is then off by less
+// than 2^-53.
 template <int N>
 __device__ __forceinline__ float swiglu(float (&gt)[N], const float (&up)[N]) {
   float m = 0.0f;
 #pragma unroll
-  for (int i = 0; i < N; ++i) {
-    gt[i] = silu_fast(gt[i]) * up[i];
-    m = fmax_nan(m, fabsf(gt[i]));
+  for (int i = 0; i < N; i += 2) {
+    const float d0 = 1.0f + exp2_approx(fminf(gt[i] * -kLog2e, 60.0f));
+    const float d1 = 1.0f + exp2_approx(fminf(gt[i + 1] * -kLog2e, 60.0f));
+    const float r = rcp_approx(d0 * d1);
+    gt[i] = gt[i] * (r * d1) * up[i];
+    gt[i + 1] = gt[i + 1] * (r * d0) * up[i + 1];
+    m = fmax_nan(m, fmax_nan(fabsf(gt[i]), fabsf(gt[i + 1])));
   }
   return m;
 }
@@ -605,7 +625,7 @@ __global__ void __launch_bounds__(Pair::threads, 1)
         if (!ok) continue;
         if (a.N % 8 == 0) {
           // Rows of 64 FP16 columns in the 128-byte swizzle, stored by TMA.
-          if (lane == 0) tc::tma_store_wait_read();
+          if (lane < 2) tc::tma_store_wait_read();
           __syncwarp();
 #pragma unroll
           for (int c = 0; c < 16; ++c) {
@@ -621,10 +641,9 @@ __global__ void __launch_bounds__(Pair::threads, 1)
           tc::fence_async_smem();
           __syncwarp();
           const int y0 = m0 + 32 * q4, x0 = n0 + (int)c0;
-          if (lane == 0 && y0 < a.T && x0 < a.N) {
-            tc::tma_store_2d(&map_y, x0, y0, out);
-            if (x0 + 64 < a.N) tc::tma_store_2d(&map_y, x0 + 64, y0, out + 4096);
-          }
+          // A lane per store: one lane issuing both takes twice as long.
+          if (lane < 2 && y0 < a.T && x0 + 64 * lane < a.N)
+            tc::tma_store_2d(&map_y, x0 + 64 * lane, y0, out + 4096 * lane);
         } else if (row < a.T) {
           __half* o = a.y + (size_t)row * a.N + n0 + c0;
           const int left = a.N - (n0 + (int)c0);
@@ -667,7 +686,7 @@ __global__ void __launch_bounds__(Pair::threads, 1)
         if (ok && j2 == 0 && row < a.T) a.hs[(size_t)row * a.nbh + n0 / 128] = bs.scale;
       }
     }
-    if (lane == 0) tc::tma_store_wait_all();
+    if (lane < 2) tc::tma_store_wait_read();  // the grid's end waits for the writes
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
     if (warp == 0) {
