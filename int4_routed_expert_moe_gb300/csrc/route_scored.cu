@@ -9,6 +9,7 @@
 //   scores, the best top_groups kept; top-k of the kept experts by
 //   (v desc, index asc); w_j = s_{id_j} [/ (sum_j s_{id_j} + 1e-20)] * scale.
 #include <algorithm>
+#include <cfloat>
 #include <climits>
 
 #include "common.h"
@@ -45,8 +46,26 @@ __device__ __forceinline__ float load_logit(const void* row, int e) {
   return static_cast<const float*>(row)[e];
 }
 
-// Relative error about 2^-21; 0 below -87 (where exp(-v) overflows) or so.
-__device__ __forceinline__ float sigmoid_f(float v) { return __fdividef(1.0f, 1.0f + expf(-v)); }
+// The special-function unit's own 2^x and 1/x (relative errors about 2^-22);
+// with the rounding of v log2(e) a score is off by less than 1e-6 of itself
+// for |v| <= 10.
+constexpr float kLog2e = 1.4426950408889634f;
+__device__ __forceinline__ float exp_f(float v) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v * kLog2e));
+  return r;
+}
+__device__ __forceinline__ float sigmoid_f(float v) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + exp_f(-v)));
+  return r;
+}
+// The larger of the two, NaN if one is.
+__device__ __forceinline__ float fmax_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
 
 __device__ __forceinline__ float warp_max(float v) {
 #pragma unroll
@@ -87,17 +106,19 @@ constexpr int kWarpsPerBlock = 4;
 //
 // Top-k: the k-th largest of the lanes' maxima (k rounds of one warp
 // reduction) is a bound that at least k candidates reach; the candidates that
-// reach it are usually few more than k. They are compacted to shared memory,
-// and each lane ranks one of them by (v desc, index asc) against the others.
-// Where more than 32 reach the bound, k rounds of argmax instead.
+// reach it are usually few more than k. They are compacted to shared memory as
+// 64-bit keys (value, then lower index first), and each lane ranks one of them
+// against the others. Where more than 32 reach the bound, k rounds of argmax
+// instead. Bound by instruction issue: about 400 per token of 256 experts.
 template <int PER, bool HALF>
 __global__ void __launch_bounds__(32 * kWarpsPerBlock) route_scored_kernel(const ScoredArgs a) {
   constexpr bool kBiasRegs = PER <= 16;  // a lane's biases stay in registers over its tokens
-  __shared__ float2 cand_all[kWarpsPerBlock][32];
+  __shared__ unsigned long long cand_all[kWarpsPerBlock][32];
   const unsigned full = 0xffffffffu;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  float2* cand = cand_all[warp];
-  const int grp = lane >> a.lg_shift, sub = lane & ((1 << a.lg_shift) - 1);
+  unsigned long long* cand = cand_all[warp];
+  const int lanes = 1 << a.lg_shift;  // of a group
+  const int grp = lane >> a.lg_shift, sub = lane & (lanes - 1);
   const int first = grp * a.per + sub * a.chunk;
   const int n = grp < a.G ? max(0, min(a.chunk, a.per - sub * a.chunk)) : 0;
   griddep_wait();
@@ -106,12 +127,11 @@ __global__ void __launch_bounds__(32 * kWarpsPerBlock) route_scored_kernel(const
   bool bad_bias = false;
   if (a.bias) {
 #pragma unroll
-    for (int j = 0; j < PER; ++j)
-      if (j < n) {
-        const float b = a.bias[first + j];
-        bad_bias |= isnan(b) || b == INFINITY;
-        if (kBiasRegs) bias[j] = b;
-      }
+    for (int j = 0; j < PER; ++j) {
+      const float b = j < n ? a.bias[first + j] : 0.0f;
+      bad_bias |= !(b < INFINITY);  // NaN or +inf
+      if (kBiasRegs) bias[j] = b;
+    }
   }
   for (int t = blockIdx.x * kWarpsPerBlock + warp; t < a.T; t += gridDim.x * kWarpsPerBlock) {
     const uint8_t* row = static_cast<const uint8_t*>(a.logits) + (size_t)t * a.ld * (HALF ? 2 : 4);
@@ -122,40 +142,48 @@ __global__ void __launch_bounds__(32 * kWarpsPerBlock) route_scored_kernel(const
 #pragma unroll
       for (int j = 0; j < PER; ++j) v[j] = j < n ? load_logit<HALF>(row, first + j) : -INFINITY;
     }
-    bool bad = bad_bias;
-    float mx = -INFINITY;
+    float mx = v[0];
 #pragma unroll
-    for (int j = 0; j < PER; ++j) {
-      bad |= !(v[j] < INFINITY);  // NaN or +inf
-      mx = fmaxf(mx, v[j]);
-    }
+    for (int j = 1; j < PER; ++j) mx = fmax_nan(mx, v[j]);
+    const bool bad = bad_bias || !(mx < INFINITY);  // NaN or +inf
     float m = 0.0f, inv = 1.0f;
     if (!a.sigmoid) {
       m = warp_max(mx);
       float s = 0.0f;
 #pragma unroll
-      for (int j = 0; j < PER; ++j) s += v[j] > -INFINITY ? expf(v[j] - m) : 0.0f;
+      for (int j = 0; j < PER; ++j) s += v[j] > -INFINITY ? exp_f(v[j] - m) : 0.0f;
       inv = 1.0f / warp_sum(s);
     }
-    auto score = [&](float l) { return a.sigmoid ? sigmoid_f(l) : expf(l - m) * inv; };
+    auto sigmoid = [](float l) { return sigmoid_f(l); };
+    auto softmax = [&](float l) { return exp_f(l - m) * inv; };
     float g1 = mx, g2 = -INFINITY;  // the lane's two best for the group's value
     float top = mx;                 // the lane's best in the order
-    if (a.bias || a.rank_top2) {
-      g1 = top = -INFINITY;
+    auto add_bias = [&](auto score) {
+      g1 = -INFINITY;
 #pragma unroll
       for (int j = 0; j < PER; ++j) {
-        float o = v[j], r = o;
-        if (a.bias) {
-          const float b = kBiasRegs ? bias[kBiasRegs ? j : 0] : (j < n ? a.bias[first + j] : 0.0f);
-          r = o = j < n && o > -INFINITY && b > -INFINITY ? score(o) + b : -INFINITY;
-          v[j] = o;
-        } else {
-          r = o > -INFINITY ? score(o) : -INFINITY;
-        }
-        top = fmaxf(top, o);
+        const float b = kBiasRegs ? bias[kBiasRegs ? j : 0] : (j < n ? a.bias[first + j] : 0.0f);
+        v[j] = v[j] > -INFINITY ? score(v[j]) + b : -INFINITY;
+        g2 = fmaxf(g2, fminf(g1, v[j]));
+        g1 = fmaxf(g1, v[j]);
+      }
+      top = g1;
+    };
+    auto best_two = [&](auto score) {
+      g1 = -INFINITY;
+#pragma unroll
+      for (int j = 0; j < PER; ++j) {
+        const float r = v[j] > -INFINITY ? score(v[j]) : -INFINITY;
         g2 = fmaxf(g2, fminf(g1, r));
         g1 = fmaxf(g1, r);
       }
+    };
+    if (a.bias) {
+      if (a.sigmoid) add_bias(sigmoid);
+      else add_bias(softmax);
+    } else if (a.rank_top2) {
+      if (a.sigmoid) best_two(sigmoid);
+      else best_two(softmax);
     }
     if (__any_sync(full, bad) || !__any_sync(full, top > -INFINITY)) {
       if (lane < a.k) {
@@ -167,62 +195,63 @@ __global__ void __launch_bounds__(32 * kWarpsPerBlock) route_scored_kernel(const
     }
     bool kept = grp < a.G;
     if (a.top_g < a.G) {
-      for (int o = 1; o < (1 << a.lg_shift); o <<= 1) {
+      for (int o = 1; o < lanes; o <<= 1) {
         const float h1 = __shfl_xor_sync(full, g1, o), h2 = __shfl_xor_sync(full, g2, o);
         g2 = fmaxf(fminf(g1, h1), fmaxf(g2, h2));
         g1 = fmaxf(g1, h1);
       }
       const float gv = a.rank_top2 && g2 > -INFINITY ? g1 + g2 : g1;
+      // How many groups come before this one: its lanes share the comparisons.
       int before = 0;
-#pragma unroll 4
-      for (int h = 0; h < a.G; ++h) {
-        const float o = __shfl_sync(full, gv, h << a.lg_shift);
-        before += o > gv || (o == gv && h < grp);
+      for (int h0 = 0; h0 < a.G; h0 += lanes) {
+        const int h = h0 + sub;
+        const float o = __shfl_sync(full, gv, (h << a.lg_shift) & 31);
+        before += h < a.G && (o > gv || (o == gv && h < grp));
       }
+      for (int o = 1; o < lanes; o <<= 1) before += __shfl_xor_sync(full, before, o);
       kept = kept && before < a.top_g;
     }
 
-    const uint32_t key0 = kept && top > -INFINITY ? order_key(top) : 0u;  // a real key is above 0
-    uint32_t key = key0, bound = 0u;
+    uint32_t key = kept && top > -INFINITY ? order_key(top) : 0u, bound = 0u;  // a real key is above 0
+#pragma unroll 4
     for (int r = 0; r < a.k; ++r) {
       bound = __reduce_max_sync(full, key);
       if (key == bound) key = 0u;
     }
-    int count = 0;
-    if (bound == 0u) {  // fewer than k lanes hold a candidate: all of them
+    // Candidates: what reaches the bound, or (fewer than k lanes hold one) all.
+    const float lim = !kept ? INFINITY : bound != 0u ? key_value(bound) : -FLT_MAX;
+    int mine = 0;
 #pragma unroll
-      for (int j = 0; j < PER; ++j) {
-        const bool on = kept && v[j] > -INFINITY;
-        const unsigned ball = __ballot_sync(full, on);
-        const int pos = count + __popc(ball & ((1u << lane) - 1u));
-        if (on && pos < 32) cand[pos] = make_float2(v[j], __int_as_float(first + j));
-        count += __popc(ball);
-      }
-    } else {
-      const float lim = kept ? key_value(bound) : INFINITY;
+    for (int j = 0; j < PER; ++j) mine += v[j] >= lim;
+    int upto = mine;  // inclusive scan over the lanes
 #pragma unroll
-      for (int j = 0; j < PER; ++j) {
-        const bool on = v[j] >= lim;
-        const unsigned ball = __ballot_sync(full, on);
-        const int pos = count + __popc(ball & ((1u << lane) - 1u));
-        if (on && pos < 32) cand[pos] = make_float2(v[j], __int_as_float(first + j));
-        count += __popc(ball);
-      }
+    for (int o = 1; o < 32; o <<= 1) {
+      const int x = __shfl_up_sync(full, upto, o);
+      if (lane >= o) upto += x;
     }
+    const int count = __shfl_sync(full, upto, 31);
     int my_i = -1, my_r = 32;  // this lane's pick and its rank
     if (count <= 32) {
-      __syncwarp();
-      const float2 me = cand[lane < count ? lane : 0];
-      if (lane < count) {
-        my_i = __float_as_int(me.y);
-        my_r = 0;
-        for (int c = 0; c < count; ++c) {
-          const float2 o = cand[c];
-          my_r += ranks_before(o.x, __float_as_int(o.y), me.x, my_i);
-        }
-      } else if (lane < a.k) {
-        my_r = lane;  // no expert left for this pick
+      if (mine) {
+        int pos = upto - mine;
+#pragma unroll
+        for (int j = 0; j < PER; ++j)
+          if (v[j] >= lim)
+            cand[pos++] = ((unsigned long long)__float_as_uint(v[j]) << 32) | (uint32_t)(first + j);
       }
+      __syncwarp();
+      unsigned long long me = 0;
+      if (lane < count) {
+        me = cand[lane];
+        my_i = (int)(uint32_t)me;
+        me = ((unsigned long long)order_key(__uint_as_float((uint32_t)(me >> 32))) << 32) | (0xffffffffu - (uint32_t)me);
+        cand[lane] = me;
+        my_r = 0;
+      }
+      __syncwarp();
+#pragma unroll 4
+      for (int c = 0; c < count; ++c) my_r += cand[c] > me;
+      if (lane >= count) my_r = lane < a.k ? lane : 32;  // no expert left for this pick
       __syncwarp();
     } else {
       float bv = -INFINITY;
@@ -248,7 +277,11 @@ __global__ void __launch_bounds__(32 * kWarpsPerBlock) route_scored_kernel(const
       my_r = lane;
     }
     const bool picked = my_r < a.k && my_i >= 0;
-    float s = picked ? score(load_logit<HALF>(row, my_i)) : 0.0f;
+    float s = 0.0f;
+    if (picked) {
+      const float l = load_logit<HALF>(row, my_i);
+      s = a.sigmoid ? sigmoid(l) : softmax(l);
+    }
     if (a.renorm) s = s / (warp_sum(s) + 1e-20f);
     if (my_r < a.k) {
       a.ids[(size_t)t * a.k + my_r] = my_i;
@@ -260,7 +293,7 @@ __global__ void __launch_bounds__(32 * kWarpsPerBlock) route_scored_kernel(const
 template <int PER, bool HALF>
 cudaError_t launch_scored(const ScoredArgs& a, int sms, cudaStream_t st) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)std::min((a.T + kWarpsPerBlock - 1) / kWarpsPerBlock, sms * 12));
+  cfg.gridDim = dim3((unsigned)std::min((a.T + kWarpsPerBlock - 1) / kWarpsPerBlock, sms * 18));
   cfg.blockDim = dim3(32 * kWarpsPerBlock);
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
