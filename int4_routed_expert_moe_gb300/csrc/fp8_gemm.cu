@@ -623,36 +623,39 @@ __global__ void __launch_bounds__(Pair::threads, 1)
       const bool ok = *reinterpret_cast<volatile int*>(b.abort) == 0;
       if (!GATEUP) {
         if (!ok) continue;
-        if (a.N % 8 == 0) {
-          // Rows of 64 FP16 columns in the 128-byte swizzle, stored by TMA.
-          if (lane < 2) tc::tma_store_wait_read();
-          __syncwarp();
+        // Rows of 64 FP16 columns in the 128-byte swizzle.
+        if (lane < 2) tc::tma_store_wait_read();
+        __syncwarp();
 #pragma unroll
-          for (int c = 0; c < 16; ++c) {
-            uint32_t h[4];
+        for (int c = 0; c < 16; ++c) {
+          uint32_t h[4];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const float2 p = unpack2(sum[4 * c + e]);
-              h[e] = half2_bits(p.x, p.y);
-            }
-            *reinterpret_cast<uint4*>(out + (c >> 3) * 4096 + tc::sw128_offset(lane, c & 7)) =
-                make_uint4(h[0], h[1], h[2], h[3]);
+          for (int e = 0; e < 4; ++e) {
+            const float2 p = unpack2(sum[4 * c + e]);
+            h[e] = half2_bits(p.x, p.y);
           }
+          *reinterpret_cast<uint4*>(out + (c >> 3) * 4096 + tc::sw128_offset(lane, c & 7)) =
+              make_uint4(h[0], h[1], h[2], h[3]);
+        }
+        const int y0 = m0 + 32 * q4, x0 = n0 + (int)c0;
+        if (a.N % 8 == 0) {
           tc::fence_async_smem();
           __syncwarp();
-          const int y0 = m0 + 32 * q4, x0 = n0 + (int)c0;
           // A lane per store: one lane issuing both takes twice as long.
           if (lane < 2 && y0 < a.T && x0 + 64 * lane < a.N)
             tc::tma_store_2d(&map_y, x0 + 64 * lane, y0, out + 4096 * lane);
-        } else if (row < a.T) {
-          __half* o = a.y + (size_t)row * a.N + n0 + c0;
-          const int left = a.N - (n0 + (int)c0);
-#pragma unroll
-          for (int i = 0; i < 64; ++i) {
-            const float2 p = unpack2(sum[i]);
-            if (2 * i < left) o[2 * i] = __float2half_rn(p.x);
-            if (2 * i + 1 < left) o[2 * i + 1] = __float2half_rn(p.y);
+        } else {
+          // Rows that TMA cannot address (16-byte pitch): two columns per lane.
+          __syncwarp();
+          for (int i = 0; i < 2 * min(32, a.T - y0); ++i) {
+            const int rr = i >> 1, x = x0 + 64 * (i & 1) + 2 * lane;
+            const uint32_t v = *reinterpret_cast<const uint32_t*>(out + 4096 * (i & 1) + tc::sw128_offset(rr, lane >> 2) +
+                                                                  4 * (lane & 3));
+            __half* o = a.y + (size_t)(y0 + rr) * a.N + x;
+            if (x < a.N) o[0] = __ushort_as_half((unsigned short)v);
+            if (x + 1 < a.N) o[1] = __ushort_as_half((unsigned short)(v >> 16));
           }
+          __syncwarp();
         }
       } else {
         float h[64], up[64];
@@ -815,23 +818,48 @@ int code_map(CUtensorMap* m, const void* base, int K, int rows, int box_rows) {
   return encode_tensor_map(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, base, dims, str, box, CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
-// Tile width and cluster split of a product.
+// The kernel a product runs on: pairs (nt = 0), or single blocks with tiles of
+// nt columns and the K steps of a tile split over a cluster.
 struct Plan {
   int nt, splits;
 };
+// The cheapest by a model of the time (us), fitted to runs of every choice at
+// 17 to 512 tokens against 4096 x 2048, 2048 x 4096, 1001 x 2064, 512 x 1024
+// and 8192 x 8192 (us measured by choice, e.g. 64 tokens, 4096 x 2048: nt/splits
+// 128/4 6.1, 64/2 6.3, 32/1 6.9, 128/2 7.4, 256/4 8.1; 512 tokens, 8192 x 8192:
+// pairs 28.9, 256/1 35, 128/1 51):
+//   single blocks: 3.2 to start and end; a step takes 0.235 (barriers, issue) or
+//   what its bytes need at 68 GB/ms per SM; joining a split costs 0.5 and
+//   0.0125 per column;
+//   pairs: 4.2 to start and end, 0.38 per step, 1.5 per tile after the first
+//   (gate/up 2.0: SiLU and the quantisation).
 Plan plan_of(int T, int N, int nb, int sms, bool gateup) {
-  const int mt = (T + BM - 1) / BM;
-  Plan p = {256, 1};
-  if (gateup) {
-    const int tiles = mt * blocks128(N);
-    while (p.splits < kMaxSplits && p.splits * 2 <= nb && tiles * p.splits * 2 <= sms) p.splits *= 2;
-    return p;
+  const int mt = (T + BM - 1) / BM, kn_pair = gateup ? 128 : 256;
+  const int pair_tiles = ((T + 255) / 256) * ((N + kn_pair - 1) / kn_pair);
+  const int pair_waves = (pair_tiles + sms / 2 - 1) / (sms / 2);
+  const float per_tile = gateup ? 2.0f : 1.5f;
+  Plan best = {0, 1};
+  float t_best = 4.2f + (float)pair_waves * (0.38f * (float)nb + per_tile) - per_tile;
+  const float a_bytes = 128.0f * (float)std::min(T, BM);
+  for (int nt = gateup ? 256 : 32; nt <= 256; nt *= 2) {
+    const int kn = gateup ? 128 : nt, tiles = mt * ((N + kn - 1) / kn);
+    const float step = std::max(0.235f, (128.0f * (float)nt + a_bytes) / 68000.0f);
+    for (int s = 1; s <= kMaxSplits && s <= nb; s *= 2) {
+      // A split tile's blocks start together: about sms / 2 blocks fit in
+      // clusters of eight at a time, 9/10 of the SMs in clusters of four.
+      if (s > 1 && (long long)tiles * s > (s == 8 ? sms / 2 : s == 4 ? sms * 9 / 10 : sms)) break;
+      const int steps = (nb + s - 1) / s;
+      const int waves = (tiles + sms - 1) / sms;
+      const float t = 3.2f + (float)waves * (float)steps * step + (s > 1 ? 0.5f + 0.0125f * (float)nt : 0.0f) +
+                      (float)(waves - 1) * per_tile +
+                      (s == 1 && !gateup && N % 8 ? (float)waves * 0.03f * (float)nt : 0.0f);  // scattered 2-byte stores
+      if (t < t_best) {
+        t_best = t;
+        best = {nt, s};
+      }
+    }
   }
-  // The widest tile that still fills the SMs, then split K while they are not.
-  while (p.nt > 32 && mt * ((N + p.nt - 1) / p.nt) < sms / 2) p.nt /= 2;
-  const int tiles = mt * ((N + p.nt - 1) / p.nt);
-  while (p.splits < kMaxSplits && p.splits * 4 <= nb && tiles * p.splits * 2 <= sms) p.splits *= 2;
-  return p;
+  return best;
 }
 
 struct Operand {
@@ -959,9 +987,9 @@ int product(const Operand& x, const Operand& w, int T, int N, int K, __half* y, 
   a.T = T; a.N = N; a.K = K;
   a.y = y;
   a.flags = flags;
-  if (T > BM && ((T + 255) / 256) * ((N + 255) / 256) >= sms / 4) return launch_pair<false>(a, x, w, nullptr, sms, dev, st);
   const Plan p = plan_of(T, N, blocks128(K), sms, false);
   switch (p.nt) {
+    case 0: return launch_pair<false>(a, x, w, nullptr, sms, dev, st);
     case 256: return launch_gemm<256, false>(a, x, w, nullptr, p.splits, sms, dev, st);
     case 128: return launch_gemm<128, false>(a, x, w, nullptr, p.splits, sms, dev, st);
     case 64: return launch_gemm<64, false>(a, x, w, nullptr, p.splits, sms, dev, st);
@@ -979,14 +1007,15 @@ int gate_up(const Operand& x, const Operand& wg, const Operand& wu, int T, int I
   a.hq = hq; a.hs = hs;
   a.nbh = blocks128(Is);
   a.flags = flags;
-  if (T > BM && ((T + 255) / 256) * blocks128(Is) >= sms / 4) return launch_pair<true>(a, x, wg, &wu, sms, dev, st);
   const Plan p = plan_of(T, Is, blocks128(H), sms, true);
+  if (p.nt == 0) return launch_pair<true>(a, x, wg, &wu, sms, dev, st);
   return launch_gemm<256, true>(a, x, wg, &wu, p.splits, sms, dev, st);
 }
 
-// Workspace of the FFN after the header: x and h as codes and scales.
+// Workspace of the FFN after the header: x and h as codes and scales, and for
+// a few tokens h in FP32.
 struct FfnWs {
-  size_t xq, xs, hq, hs, total;
+  size_t xq, xs, hq, hs, hf, total;
 };
 FfnWs ffn_ws(int T, int H, int Is) {
   FfnWs w;
@@ -995,6 +1024,7 @@ FfnWs ffn_ws(int T, int H, int Is) {
   w.xs = o; o += round256((size_t)T * blocks128(H) * 4);
   w.hq = o; o += round256((size_t)T * Is);
   w.hs = o; o += round256((size_t)T * blocks128(Is) * 4);
+  w.hf = o; o += T <= kGemvMaxTokens ? round256((size_t)T * Is * 4) : 0;
   w.total = o;
   return w;
 }
@@ -1066,7 +1096,7 @@ int moe_shared_forward_fp8(const void* x, int T, int H, int Is, const void* wg, 
                      d = {static_cast<const uint8_t*>(wd), sd};
   if (T <= moe::kGemvMaxTokens)
     return moe::fp8_gemv_ffn(static_cast<const __half*>(x), T, H, Is, g.q, sg, u.q, su, d.q, sd, xq, xs, hq,
-                             hs, static_cast<__half*>(y), st);
+                             hs, reinterpret_cast<float*>(w8 + o.hf), static_cast<__half*>(y), st);
   int rc = moe::launch_quantize_fp8(static_cast<const __half*>(x), T, H, 1, xq, xs, st);
   if (rc != MOE_OK) return rc;
   if ((rc = moe::gate_up({xq, xs}, g, u, T, Is, H, hq, hs, flags, st)) != MOE_OK) return rc;

@@ -14,9 +14,9 @@ constexpr int kGemvMaxTokens = 16;
 int fp8_gemv(const uint8_t* xq, const float* xs, int T, const uint8_t* wq, const float* ws, int N, int K, __half* y,
              cudaStream_t st);
 // The shared FFN, T <= kGemvMaxTokens; xq, xs, hq, hs: scratch for x and h as
-// codes and scales.
+// codes and scales; h: FP32 scratch [T][Is].
 int fp8_gemv_ffn(const __half* x, int T, int H, int Is, const uint8_t* wg, const float* sg, const uint8_t* wu,
                  const float* su, const uint8_t* wd, const float* sd, uint8_t* xq, float* xs, uint8_t* hq, float* hs,
-                 __half* y, cudaStream_t st);
+                 float* h, __half* y, cudaStream_t st);
 
 }  // namespace moe

@@ -92,6 +92,9 @@ if not os.path.exists(_LIB_PATH):
     raise ImportError(f"{_LIB_PATH} is not built; run int4_routed_expert_moe_gb300.build.build()")
 _lib = ctypes.CDLL(_LIB_PATH)
 
+_F32, _F16, _I32, _U8 = torch.float32, torch.float16, torch.int32, torch.uint8
+_FP8 = torch.float8_e4m3fn
+
 _P = ctypes.c_void_p
 _I = ctypes.c_int
 _SZ = ctypes.c_size_t
@@ -289,27 +292,32 @@ def moe_route_config(score: str = "softmax", n_groups: int = 1, top_groups: int 
 
 
 def _logits(logits) -> tuple:
-    """(pointer, type, row stride) of a router's logits: rows may be strided."""
+    """(pointer, type, row stride, T, E) of a router's logits: rows may be strided."""
     if not isinstance(logits, torch.Tensor) or not logits.is_cuda:
         raise TypeError("logits must be a CUDA tensor")
-    if logits.dtype not in _LOGIT_TYPES:
+    kind = _LOGIT_TYPES.get(logits.dtype)
+    if kind is None:
         raise TypeError(f"logits must be float32 or float16, got {logits.dtype}")
-    if logits.dim() != 2 or (logits.shape[1] > 1 and logits.stride(1) != 1):
+    if logits.dim() != 2:
         raise ValueError("logits must be [T][E] with contiguous rows")
-    ld = logits.stride(0) if logits.shape[0] > 1 else logits.shape[1]
-    return logits.data_ptr(), _LOGIT_TYPES[logits.dtype], ld
+    T, E = logits.shape
+    ld, step = logits.stride()
+    if E > 1 and step != 1:
+        raise ValueError("logits must be [T][E] with contiguous rows")
+    return logits.data_ptr(), kind, ld if T > 1 else E, T, E
 
 
 def moe_route_scored(cfg: moe_route_cfg, logits: torch.Tensor, k: int, bias: torch.Tensor | None,
                      ids: torch.Tensor, weights: torch.Tensor, bad_tokens: torch.Tensor | None = None,
                      stream=None) -> None:
-    ptr, kind, ld = _logits(logits)
-    T, E = logits.shape
-    _check(_lib.moe_route_scored(cfg, ptr, kind, ld, T, E, k, _dev(bias, torch.float32, "bias", E, nullable=True),
-                                 _dev(ids, torch.int32, "ids", T * k),
-                                 _dev(weights, torch.float32, "weights", T * k),
-                                 _dev(bad_tokens, torch.int32, "bad_tokens", 1, nullable=True),
-                                 _stream(stream)), "moe_route_scored")
+    ptr, kind, ld, T, E = _logits(logits)
+    n = T * k
+    status = _lib.moe_route_scored(
+        cfg, ptr, kind, ld, T, E, k, None if bias is None else _dev(bias, _F32, "bias", E), _dev(ids, _I32, "ids", n),
+        _dev(weights, _F32, "weights", n), None if bad_tokens is None else _dev(bad_tokens, _I32, "bad_tokens", 1),
+        _stream(stream))
+    if status:
+        _check(status, "moe_route_scored")
 
 
 def moe_token_sort(ids: torch.Tensor, E: int, offsets: torch.Tensor, pair_tok: torch.Tensor,
@@ -391,8 +399,7 @@ def moe_layer_forward_scored(shape, x: torch.Tensor, cfg: moe_route_cfg, logits:
                              path: int = MOE_PATH_AUTO, stream=None) -> None:
     """moe_route_scored, then moe_expert_forward on its ids and weights."""
     H, I, g = shape
-    ptr, kind, ld = _logits(logits)
-    T, E = logits.shape
+    ptr, kind, ld, T, E = _logits(logits)
     s = _shape(shape)
     bb = moe_expert_block_bytes(shape)
     _check(_lib.moe_layer_forward_scored(
@@ -457,11 +464,10 @@ def moe_shared_forward(x: torch.Tensor, wg: torch.Tensor, wu: torch.Tensor, wd: 
 
 
 # ---- FP8 non-routed path -----------------------------------------------------
-_FP8 = torch.float8_e4m3fn
 
 
 def _nb(n: int) -> int:
-    return (n + 127) // 128
+    return (n + 127) >> 7
 
 
 def moe_quantize_fp8(x: torch.Tensor, q: torch.Tensor, scales: torch.Tensor, block_rows: int = 1,
@@ -469,9 +475,11 @@ def moe_quantize_fp8(x: torch.Tensor, q: torch.Tensor, scales: torch.Tensor, blo
     """x (fp16 [rows][cols]) to float8_e4m3fn codes q and scales
     [ceil(rows / block_rows)][ceil(cols / 128)]; block_rows 1 (activations) or 128 (weights)."""
     rows, cols = x.shape
-    _check(_lib.moe_quantize_fp8(_dev(x, torch.float16, "x"), rows, cols, block_rows, _dev(q, _FP8, "q", rows * cols),
-                                 _dev(scales, torch.float32, "scales", -(-rows // max(1, block_rows)) * _nb(cols)),
-                                 _stream(stream)), "moe_quantize_fp8")
+    status = _lib.moe_quantize_fp8(_dev(x, _F16, "x"), rows, cols, block_rows, _dev(q, _FP8, "q", rows * cols),
+                                   _dev(scales, _F32, "scales", -(-rows // max(1, block_rows)) * _nb(cols)),
+                                   _stream(stream))
+    if status:
+        _check(status, "moe_quantize_fp8")
 
 
 def moe_matmul_fp8_workspace_bytes(T: int, N: int, K: int) -> int:
@@ -482,14 +490,15 @@ def moe_matmul_fp8(xq: torch.Tensor, xs: torch.Tensor, wq: torch.Tensor, ws: tor
                    workspace: torch.Tensor, stream=None) -> None:
     """y [T][N] = x W^T from the codes xq [T][K], wq [N][K] and their scales."""
     T, K = xq.shape
-    N = wq.shape[0]
-    if wq.shape[1] != K:
-        raise ValueError(f"xq has {K} columns, wq {wq.shape[1]}")
+    N, Kw = wq.shape
+    if Kw != K:
+        raise ValueError(f"xq has {K} columns, wq {Kw}")
     nb = _nb(K)
-    _check(_lib.moe_matmul_fp8(
-        _dev(xq, _FP8, "xq"), _dev(xs, torch.float32, "xs", T * nb), T, _dev(wq, _FP8, "wq"),
-        _dev(ws, torch.float32, "ws", _nb(N) * nb), N, K, _dev(y, torch.float16, "y", T * N),
-        _dev(workspace, torch.uint8, "workspace"), workspace.numel(), _stream(stream)), "moe_matmul_fp8")
+    status = _lib.moe_matmul_fp8(_dev(xq, _FP8, "xq"), _dev(xs, _F32, "xs", T * nb), T, _dev(wq, _FP8, "wq"),
+                                 _dev(ws, _F32, "ws", _nb(N) * nb), N, K, _dev(y, _F16, "y", T * N),
+                                 _dev(workspace, _U8, "workspace"), workspace.numel(), _stream(stream))
+    if status:
+        _check(status, "moe_matmul_fp8")
 
 
 def moe_shared_fp8_workspace_bytes(T: int, H: int, Is: int) -> int:
@@ -502,12 +511,13 @@ def moe_shared_forward_fp8(x: torch.Tensor, wg: torch.Tensor, sg: torch.Tensor, 
     """moe_shared_forward with float8_e4m3fn weights and their 128 x 128 block scales."""
     T, H = x.shape
     Is = wg.shape[0]
-    ns = _nb(H) * _nb(Is)
-    _check(_lib.moe_shared_forward_fp8(
-        _dev(x, torch.float16, "x"), T, H, Is, _dev(wg, _FP8, "wg", Is * H), _dev(sg, torch.float32, "sg", ns),
-        _dev(wu, _FP8, "wu", Is * H), _dev(su, torch.float32, "su", ns), _dev(wd, _FP8, "wd", H * Is),
-        _dev(sd, torch.float32, "sd", ns), _dev(y, torch.float16, "y", T * H),
-        _dev(workspace, torch.uint8, "workspace"), workspace.numel(), _stream(stream)), "moe_shared_forward_fp8")
+    n, ns = Is * H, _nb(H) * _nb(Is)
+    status = _lib.moe_shared_forward_fp8(
+        _dev(x, _F16, "x"), T, H, Is, _dev(wg, _FP8, "wg", n), _dev(sg, _F32, "sg", ns), _dev(wu, _FP8, "wu", n),
+        _dev(su, _F32, "su", ns), _dev(wd, _FP8, "wd", n), _dev(sd, _F32, "sd", ns), _dev(y, _F16, "y", T * H),
+        _dev(workspace, _U8, "workspace"), workspace.numel(), _stream(stream))
+    if status:
+        _check(status, "moe_shared_forward_fp8")
 
 
 # ---- residency manager -----------------------------------------------------
