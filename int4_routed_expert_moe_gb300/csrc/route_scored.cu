@@ -67,10 +67,34 @@ __device__ __forceinline__ float fmax_nan(float a, float b) {
   return r;
 }
 
-__device__ __forceinline__ float warp_max(float v) {
+// Reductions over the L lanes of a token.
+template <int L>
+__device__ __forceinline__ float lanes_max(float v) {
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+  for (int o = L / 2; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
   return v;
+}
+template <int L>
+__device__ __forceinline__ float lanes_sum(float v) {
+#pragma unroll
+  for (int o = L / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+template <int L>
+__device__ __forceinline__ uint32_t lanes_max(uint32_t v) {
+  if (L == 32) return __reduce_max_sync(0xffffffffu, v);
+#pragma unroll
+  for (int o = L / 2; o > 0; o >>= 1) v = max(v, __shfl_xor_sync(0xffffffffu, v, o));
+  return v;
+}
+template <int L>
+__device__ __forceinline__ uint32_t lanes_min(uint32_t v) {
+  return ~lanes_max<L>(~v);
+}
+template <int L>
+__device__ __forceinline__ bool lanes_any(bool p) {
+  const unsigned b = __ballot_sync(0xffffffffu, p);
+  return L == 32 ? b != 0 : ((b >> (threadIdx.x & 31 & ~(L - 1))) & ((1u << (L & 31)) - 1u)) != 0;
 }
 
 // N consecutive values at p, 16 bytes at a time (p 16-byte aligned).
@@ -98,25 +122,35 @@ __device__ __forceinline__ void load_vec(const void* p, float (&v)[N]) {
 }
 
 constexpr int kWarpsPerBlock = 4;
+constexpr int kHalfWarpTokens = 4096, kHalfWarpChunk = 4;  // see route_scored_kernel
 
-// One warp per token (looping over tokens when there are many). The lanes are
-// split evenly over the groups (rounded up to a power of two), and a lane
-// holds `chunk` consecutive experts of its group, so a group's two best are a
-// butterfly over its own lanes.
+// L lanes per token, 32 / L tokens per warp (looping over tokens when there
+// are many). The lanes are split evenly over the groups (rounded up to a power
+// of two), and a lane holds `chunk` consecutive experts of its group, so a
+// group's two best are a butterfly over its own lanes.
 //
-// Top-k: the k-th largest of the lanes' maxima (k rounds of one warp
-// reduction) is a bound that at least k candidates reach; the candidates that
-// reach it are usually few more than k. They are compacted to shared memory as
-// 64-bit keys (value, then lower index first), and each lane ranks one of them
-// against the others. Where more than 32 reach the bound, k rounds of argmax
-// instead. Bound by instruction issue: about 400 per token of 256 experts.
-template <int PER, bool HALF>
+// Top-k: the k-th largest of the lanes' two best (k rounds of one reduction)
+// is a bound that at least k candidates reach (or all, where there are fewer);
+// the candidates that reach it are usually few more than k. Their indexes are
+// compacted to shared memory, and each lane ranks one of them by (v desc,
+// index asc), a 64-bit key, against the others. Where more than L reach the
+// bound, k rounds of argmax instead.
+//
+// Bound by instruction issue (some 650 per token of 256 experts: 23.4 us for
+// 32768 tokens, whose logits alone would take 5 us). Half a warp per token pays
+// the reductions, the scan and the ranking once for two tokens, but holds twice
+// the experts per lane. Measured, us for 32768 tokens, warp against half: 20
+// experts 13.5 / 8.8, 64 experts 15.5 / 10.2, 256 experts 23.4 / 24.3, 512
+// experts 43 / 83; up to 2048 tokens of 64 experts 2.8 / 3.1. So half a warp
+// where that leaves a lane at most 4 experts and there are 4096 tokens.
+template <int PER, bool HALF, int L>
 __global__ void __launch_bounds__(32 * kWarpsPerBlock) route_scored_kernel(const ScoredArgs a) {
   constexpr bool kBiasRegs = PER <= 16;  // a lane's biases stay in registers over its tokens
-  __shared__ unsigned long long cand_all[kWarpsPerBlock][32];
+  constexpr int kTok = 32 / L;           // tokens per warp
+  __shared__ unsigned long long cand_all[kWarpsPerBlock * kTok][L];
   const unsigned full = 0xffffffffu;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  unsigned long long* cand = cand_all[warp];
+  const int lane = threadIdx.x & (L - 1), slot = threadIdx.x / L;
+  unsigned long long* cand = cand_all[slot];
   const int lanes = 1 << a.lg_shift;  // of a group
   const int grp = lane >> a.lg_shift, sub = lane & (lanes - 1);
   const int first = grp * a.per + sub * a.chunk;
@@ -133,8 +167,10 @@ __global__ void __launch_bounds__(32 * kWarpsPerBlock) route_scored_kernel(const
       if (kBiasRegs) bias[j] = b;
     }
   }
-  for (int t = blockIdx.x * kWarpsPerBlock + warp; t < a.T; t += gridDim.x * kWarpsPerBlock) {
-    const uint8_t* row = static_cast<const uint8_t*>(a.logits) + (size_t)t * a.ld * (HALF ? 2 : 4);
+  for (int t0 = blockIdx.x * kWarpsPerBlock * kTok; t0 < a.T; t0 += gridDim.x * kWarpsPerBlock * kTok) {
+    const int t = t0 + slot;
+    const bool in = t < a.T;  // the last tokens' warps may be half empty
+    const uint8_t* row = static_cast<const uint8_t*>(a.logits) + (size_t)(in ? t : 0) * a.ld * (HALF ? 2 : 4);
     float v[PER];  // logits, then what orders the experts (-inf: not to be chosen)
     if (a.vec && n == PER) {
       load_vec<PER, HALF>(row + (size_t)first * (HALF ? 2 : 4), v);
@@ -148,52 +184,45 @@ __global__ void __launch_bounds__(32 * kWarpsPerBlock) route_scored_kernel(const
     const bool bad = bad_bias || !(mx < INFINITY);  // NaN or +inf
     float m = 0.0f, inv = 1.0f;
     if (!a.sigmoid) {
-      m = warp_max(mx);
+      m = lanes_max<L>(mx);
       float s = 0.0f;
 #pragma unroll
       for (int j = 0; j < PER; ++j) s += v[j] > -INFINITY ? exp_f(v[j] - m) : 0.0f;
-      inv = 1.0f / warp_sum(s);
+      inv = 1.0f / lanes_sum<L>(s);
     }
     auto sigmoid = [](float l) { return sigmoid_f(l); };
     auto softmax = [&](float l) { return exp_f(l - m) * inv; };
-    float g1 = mx, g2 = -INFINITY;  // the lane's two best for the group's value
-    float top = mx;                 // the lane's best in the order
+    // The lane's two best: in the order (p1, p2), and for the group's value.
+    float p1 = -INFINITY, p2 = -INFINITY, g1, g2;
+    auto two = [](float& x1, float& x2, float x) {
+      x2 = fmaxf(x2, fminf(x1, x));
+      x1 = fmaxf(x1, x);
+    };
     auto add_bias = [&](auto score) {
-      g1 = -INFINITY;
 #pragma unroll
       for (int j = 0; j < PER; ++j) {
         const float b = kBiasRegs ? bias[kBiasRegs ? j : 0] : (j < n ? a.bias[first + j] : 0.0f);
         v[j] = v[j] > -INFINITY ? score(v[j]) + b : -INFINITY;
-        g2 = fmaxf(g2, fminf(g1, v[j]));
-        g1 = fmaxf(g1, v[j]);
-      }
-      top = g1;
-    };
-    auto best_two = [&](auto score) {
-      g1 = -INFINITY;
-#pragma unroll
-      for (int j = 0; j < PER; ++j) {
-        const float r = v[j] > -INFINITY ? score(v[j]) : -INFINITY;
-        g2 = fmaxf(g2, fminf(g1, r));
-        g1 = fmaxf(g1, r);
+        two(p1, p2, v[j]);
       }
     };
     if (a.bias) {
       if (a.sigmoid) add_bias(sigmoid);
       else add_bias(softmax);
-    } else if (a.rank_top2) {
-      if (a.sigmoid) best_two(sigmoid);
-      else best_two(softmax);
+    } else {
+#pragma unroll
+      for (int j = 0; j < PER; ++j) two(p1, p2, v[j]);
     }
-    if (__any_sync(full, bad) || !__any_sync(full, top > -INFINITY)) {
-      if (lane < a.k) {
-        a.ids[(size_t)t * a.k + lane] = -1;
-        a.weights[(size_t)t * a.k + lane] = 0.0f;
-      }
-      if (lane == 0 && a.bad) atomicAdd(a.bad, 1);
-      continue;
+    g1 = p1;
+    g2 = p2;
+    if (!a.bias && a.rank_top2) {  // the scores grow with the logits: the same two experts
+      if (g1 > -INFINITY) g1 = a.sigmoid ? sigmoid(g1) : softmax(g1);
+      if (g2 > -INFINITY) g2 = a.sigmoid ? sigmoid(g2) : softmax(g2);
     }
-    bool kept = grp < a.G;
+    // Both votes by all the lanes: the halves of a warp may see different tokens.
+    const bool any_bad = lanes_any<L>(bad), any_live = lanes_any<L>(p1 > -INFINITY);
+    const bool dead = any_bad || !any_live;
+    bool kept = grp < a.G && !dead;
     if (a.top_g < a.G) {
       for (int o = 1; o < lanes; o <<= 1) {
         const float h1 = __shfl_xor_sync(full, g1, o), h2 = __shfl_xor_sync(full, g2, o);
@@ -205,55 +234,48 @@ __global__ void __launch_bounds__(32 * kWarpsPerBlock) route_scored_kernel(const
       int before = 0;
       for (int h0 = 0; h0 < a.G; h0 += lanes) {
         const int h = h0 + sub;
-        const float o = __shfl_sync(full, gv, (h << a.lg_shift) & 31);
+        const float o = __shfl_sync(full, gv, (h << a.lg_shift) & (L - 1), L);
         before += h < a.G && (o > gv || (o == gv && h < grp));
       }
       for (int o = 1; o < lanes; o <<= 1) before += __shfl_xor_sync(full, before, o);
       kept = kept && before < a.top_g;
     }
 
-    uint32_t key = kept && top > -INFINITY ? order_key(top) : 0u, bound = 0u;  // a real key is above 0
+    // A real key is above 0.
+    uint32_t key = kept && p1 > -INFINITY ? order_key(p1) : 0u, key2 = kept && p2 > -INFINITY ? order_key(p2) : 0u;
+    uint32_t bound = 0u;
 #pragma unroll 4
     for (int r = 0; r < a.k; ++r) {
-      bound = __reduce_max_sync(full, key);
-      if (key == bound) key = 0u;
+      bound = lanes_max<L>(key);
+      if (key == bound) {
+        key = key2;
+        key2 = 0u;
+      }
     }
-    // Candidates: what reaches the bound, or (fewer than k lanes hold one) all.
-    const float lim = !kept ? INFINITY : bound != 0u ? key_value(bound) : -FLT_MAX;
+    // Candidates: what reaches the bound, or (fewer than k in the lanes' two best) all.
+    // (No logit compares with a NaN, not even the +inf of a bad token.)
+    const float lim = !kept ? __int_as_float(0x7fffffff) : bound != 0u ? key_value(bound) : -FLT_MAX;
     int mine = 0;
 #pragma unroll
     for (int j = 0; j < PER; ++j) mine += v[j] >= lim;
-    int upto = mine;  // inclusive scan over the lanes
+    int upto = mine;  // inclusive scan over the token's lanes
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int x = __shfl_up_sync(full, upto, o);
+    for (int o = 1; o < L; o <<= 1) {
+      const int x = __shfl_up_sync(full, upto, o, L);
       if (lane >= o) upto += x;
     }
-    const int count = __shfl_sync(full, upto, 31);
-    int my_i = -1, my_r = 32;  // this lane's pick and its rank
-    if (count <= 32) {
-      if (mine) {
-        int pos = upto - mine;
+    const int count = __shfl_sync(full, upto, L - 1, L);
+    const bool few = count <= L;
+    if (few && mine) {
+      int pos = upto - mine;
 #pragma unroll
-        for (int j = 0; j < PER; ++j)
-          if (v[j] >= lim)
-            cand[pos++] = ((unsigned long long)__float_as_uint(v[j]) << 32) | (uint32_t)(first + j);
-      }
-      __syncwarp();
-      unsigned long long me = 0;
-      if (lane < count) {
-        me = cand[lane];
-        my_i = (int)(uint32_t)me;
-        me = ((unsigned long long)order_key(__uint_as_float((uint32_t)(me >> 32))) << 32) | (0xffffffffu - (uint32_t)me);
-        cand[lane] = me;
-        my_r = 0;
-      }
-      __syncwarp();
-#pragma unroll 4
-      for (int c = 0; c < count; ++c) my_r += cand[c] > me;
-      if (lane >= count) my_r = lane < a.k ? lane : 32;  // no expert left for this pick
-      __syncwarp();
-    } else {
+      for (int j = 0; j < PER; ++j)
+        if (v[j] >= lim) cand[pos++] = (unsigned long long)(unsigned)(first + j);
+    }
+    __syncwarp();
+    int my_i = -1, my_r = L;  // this lane's pick and its rank
+    if (few && lane < count) my_i = (int)(uint32_t)cand[lane];
+    if (__any_sync(full, !few)) {
       float bv = -INFINITY;
       int bi = INT_MAX;
       auto best_after = [&](float lv, int li) {  // the lane's best that ranks after (lv, li)
@@ -267,33 +289,53 @@ __global__ void __launch_bounds__(32 * kWarpsPerBlock) route_scored_kernel(const
           }
       };
       if (kept) best_after(INFINITY, -1);
-      for (int r = 0; r < a.k; ++r) {  // more than 32 candidates, k <= 32: every round finds one
+      for (int r = 0; r < a.k; ++r) {
         const uint32_t bk = bi != INT_MAX ? order_key(bv) : 0u;
-        const uint32_t kmax = __reduce_max_sync(full, bk);
-        const int win = (int)__reduce_min_sync(full, bk == kmax ? (uint32_t)bi : 0xffffffffu);
-        if (lane == r) my_i = win;
-        if (bi == win) best_after(bv, win);
+        const uint32_t kmax = lanes_max<L>(bk);
+        const uint32_t win = lanes_min<L>(bk == kmax && kmax != 0u ? (uint32_t)bi : 0xffffffffu);
+        if (!few && lane == r) my_i = (int)win;  // more candidates than k: every round finds one
+        if ((uint32_t)bi == win) best_after(bv, (int)win);
       }
-      my_r = lane;
+      if (!few) my_r = lane;
     }
-    const bool picked = my_r < a.k && my_i >= 0;
+    // The pick's score from its logit again: the same value as above.
     float s = 0.0f;
-    if (picked) {
+    unsigned long long me = 0;
+    if (my_i >= 0) {
       const float l = load_logit<HALF>(row, my_i);
       s = a.sigmoid ? sigmoid(l) : softmax(l);
+      const float o = a.bias ? s + a.bias[my_i] : l;
+      me = ((unsigned long long)order_key(o) << 32) | (0xffffffffu - (uint32_t)my_i);
     }
-    if (a.renorm) s = s / (warp_sum(s) + 1e-20f);
-    if (my_r < a.k) {
+    __syncwarp();
+    if (few) cand[lane] = me;
+    __syncwarp();
+    if (few) {
+      if (my_i >= 0) {
+        my_r = 0;
+#pragma unroll 4
+        for (int c = 0; c < count; ++c) my_r += cand[c] > me;
+      } else {
+        my_r = lane;  // no expert left for this pick
+      }
+    }
+    __syncwarp();
+    const bool out = my_r < a.k;
+    if (!out) s = 0.0f;
+    if (a.renorm) s = s / (lanes_sum<L>(s) + 1e-20f);
+    if (in && out) {
       a.ids[(size_t)t * a.k + my_r] = my_i;
       a.weights[(size_t)t * a.k + my_r] = s * a.scale;
     }
+    if (in && dead && lane == 0 && a.bad) atomicAdd(a.bad, 1);
   }
 }
 
-template <int PER, bool HALF>
+template <int PER, bool HALF, int L>
 cudaError_t launch_scored(const ScoredArgs& a, int sms, cudaStream_t st) {
+  constexpr int kTokens = kWarpsPerBlock * (32 / L);  // per block and round
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)std::min((a.T + kWarpsPerBlock - 1) / kWarpsPerBlock, sms * 18));
+  cfg.gridDim = dim3((unsigned)std::min((a.T + kTokens - 1) / kTokens, sms * 18));
   cfg.blockDim = dim3(32 * kWarpsPerBlock);
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
@@ -301,17 +343,18 @@ cudaError_t launch_scored(const ScoredArgs& a, int sms, cudaStream_t st) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, route_scored_kernel<PER, HALF>, a);
+  return cudaLaunchKernelEx(&cfg, route_scored_kernel<PER, HALF, L>, a);
 }
 
 template <bool HALF>
-cudaError_t launch_scored(const ScoredArgs& a, int sms, cudaStream_t st) {
-  if (a.chunk <= 2) return launch_scored<2, HALF>(a, sms, st);
-  if (a.chunk <= 4) return launch_scored<4, HALF>(a, sms, st);
-  if (a.chunk <= 8) return launch_scored<8, HALF>(a, sms, st);
-  if (a.chunk <= 16) return launch_scored<16, HALF>(a, sms, st);
-  if (a.chunk <= 32) return launch_scored<32, HALF>(a, sms, st);
-  return launch_scored<64, HALF>(a, sms, st);
+cudaError_t launch_scored(const ScoredArgs& a, int L, int sms, cudaStream_t st) {
+  if (L == 16) return launch_scored<kHalfWarpChunk, HALF, 16>(a, sms, st);
+  if (a.chunk <= 2) return launch_scored<2, HALF, 32>(a, sms, st);
+  if (a.chunk <= 4) return launch_scored<4, HALF, 32>(a, sms, st);
+  if (a.chunk <= 8) return launch_scored<8, HALF, 32>(a, sms, st);
+  if (a.chunk <= 16) return launch_scored<16, HALF, 32>(a, sms, st);
+  if (a.chunk <= 32) return launch_scored<32, HALF, 32>(a, sms, st);
+  return launch_scored<64, HALF, 32>(a, sms, st);
 }
 
 }  // namespace
@@ -357,10 +400,17 @@ extern "C" int moe_route_scored(const moe_route_cfg* cfg, const void* logits, in
   a.T = T; a.E = E; a.k = k;
   a.G = cfg->n_groups;
   a.per = E / cfg->n_groups;
-  int shift = 5;  // lanes per group: 32 over the groups rounded up to a power of two
-  while ((32 >> shift) < a.G) --shift;
-  a.lg_shift = shift;
-  a.chunk = (a.per + (1 << shift) - 1) >> shift;
+  auto split = [&](int L) {  // lanes per group: L over the groups rounded up to a power of two
+    a.lg_shift = L == 32 ? 5 : 4;
+    while ((L >> a.lg_shift) < a.G) --a.lg_shift;
+    a.chunk = (a.per + (1 << a.lg_shift) - 1) >> a.lg_shift;
+  };
+  int L = 32;
+  if (T >= moe::kHalfWarpTokens && k <= 16 && a.G <= 16) {
+    split(16);
+    if (a.chunk <= moe::kHalfWarpChunk) L = 16;
+  }
+  if (L == 32) split(32);
   // 16-byte loads where every lane's run of experts starts on 16 bytes.
   const int esz = logit_type == MOE_F16 ? 2 : 4;
   a.vec = reinterpret_cast<uintptr_t>(logits) % 16 == 0 && ld * esz % 16 == 0 && a.chunk * esz % 16 == 0 &&
@@ -377,8 +427,8 @@ extern "C" int moe_route_scored(const moe_route_cfg* cfg, const void* logits, in
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   int dev = 0, sms = 0;
   if ((rc = moe::current_device_sms(&dev, &sms)) != MOE_OK) return rc;
-  const cudaError_t e = logit_type == MOE_F16 ? moe::launch_scored<true>(a, sms, st)
-                                             : moe::launch_scored<false>(a, sms, st);
+  const cudaError_t e = logit_type == MOE_F16 ? moe::launch_scored<true>(a, L, sms, st)
+                                             : moe::launch_scored<false>(a, L, sms, st);
   if (e != cudaSuccess) return moe::fail(MOE_ERR_CUDA, "moe_route_scored launch: %s", cudaGetErrorString(e));
   return MOE_OK;
 }

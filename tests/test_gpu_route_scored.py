@@ -75,6 +75,26 @@ def test_many_tokens(T):
     _check(l, 6, _bias(rng, 64), score="sigmoid", n_groups=4, top_groups=2, group_rank="top2", scale=1.5)
 
 
+@pytest.mark.parametrize("T,E,G,tg,k,biased,rank", [(4096, 60, 6, 3, 4, False, "max"), (4097, 64, 1, 1, 16, True, "max"),
+                                                     (5001, 48, 16, 5, 9, True, "top2"), (4100, 20, 1, 1, 7, False, "max")])
+def test_many_tokens_few_experts(T, E, G, tg, k, biased, rank):
+    # Half a warp per token; odd token counts, masked experts and tokens, a NaN and an infinity among them.
+    rng = np.random.default_rng(T + E)
+    l = rng.normal(size=(T, E)).astype(np.float32)
+    l[rng.random(l.shape) < 0.4] = -np.inf
+    l[5::97] = -np.inf
+    l[7, 0], l[T - 1, E - 1], l[T // 2] = np.nan, np.inf, 0.25
+    bias = _bias(rng, E) if biased else None
+    cfg = dict(score="sigmoid", n_groups=G, top_groups=tg, group_rank=rank, scale=2.0)
+    got = _run(l, k, bias, **cfg)
+    with np.errstate(over="ignore", invalid="ignore"):
+        ref = f8.route_scored(l, k, bias=bias, **cfg)
+        clear = f8.closest_call(l, k, bias=bias, **cfg) > MARGIN
+    clear[T // 2] = True
+    assert clear.mean() > 0.9 and np.array_equal(got[0][clear], ref[0][clear])
+    assert np.allclose(got[1], ref[1], rtol=RTOL, atol=1e-12) and got[2] == ref[2]
+
+
 def test_equals_moe_route_without_bias_and_groups():
     l = np.random.default_rng(5).normal(size=(300, 64)).astype(np.float32)
     l[:, 40:] = l[:, :24]  # exact ties
