@@ -3,14 +3,19 @@
 // with E4M3 codes, one scale per 1 x 128 block of x and per 128 x 128 block of
 // W, FP32 sums.
 //
-// Tensor-core kernel: 128 tokens (the MMA's M) by NT rows of W (its N); both
-// operands come by TMA in the 128-byte-swizzled K-major layout, one scale
-// block (128 codes, 128 bytes) per pipeline step. The scales change every
-// step, so a step's four MMAs (K = 32 each) start a fresh FP32 accumulator in
-// tensor memory, and promotion warps read it back and add it, times its
-// scale, to sums in registers. A token is a lane of tensor memory, hence one
-// thread; the weight scale is the same for 128 columns: the scale of a step
-// is one number per thread, and promotion one packed FMA per two sums.
+// Tensor-core kernels: tokens are the MMA's M, rows of W its N; both operands
+// come by TMA in the 128-byte-swizzled K-major layout, one scale block (128
+// codes, 128 bytes) per pipeline step. The scales change every step, so a
+// step's four MMAs (K = 32 each) start a fresh FP32 accumulator in tensor
+// memory, and promotion warps read it back and add it, times its scale, to
+// sums in registers. A token is a lane of tensor memory, hence one thread; the
+// weight scale is the same for 128 columns: the scale of a step is one number
+// per thread, and promotion one packed FMA per two sums.
+//
+// fp8_gemm_kernel: a block and 128 tokens by NT columns, the K steps of a tile
+// split over a cluster where the tiles are few. fp8_pair_kernel: two blocks and
+// 256 x 256. plan_of picks; up to 16 tokens take fp8_gemv.cu instead (64 tokens
+// against 4096 x 2048: 6.2 us here; one token there 2.8 us, here 6.5).
 #include <algorithm>
 #include <mutex>
 
@@ -468,8 +473,18 @@ __global__ void __launch_bounds__(Geo<NT>::threads, 1)
 // Two blocks of a cluster run one tile with cta_group::2 MMAs: each holds its
 // 128 tokens (A) and half of the weight rows (B), and each accumulates its
 // tokens against all 256 rows. Against a block on its own with a 128 x 256
-// tile, a step's shared-memory traffic (TMA writes and MMA reads) falls from
-// 96 KB to 64 KB per SM in the 512 cycles its MMAs take.
+// tile (2.25 PFLOP/s with the promotion left out), a step's TMA writes fall
+// from 48 KB to 32 KB per SM, and so do the operand bytes its MMAs read from it.
+//
+// Measured: a step's MMAs end every 710 cycles, back to back and whatever the
+// promotion does, against 512 at the tensor pipe's nominal rate (the pipe is
+// active 64 % of the time): 32 KB written and what the two tensor cores read of
+// both blocks' operands keep the shared memory busy. The promotion needs 8 % on
+// top (its FMAs issue every other cycle: 260 of a step's cycles per scheduler).
+// 8192 x 8192 x 4096: 190 us, 2.9 PFLOP/s, 75 % of twice the measured BF16
+// rate; under sustained load the power limit takes it to 215 us.
+// 2048 x 4096 x 2048: 18.4 us; its 128 tiles are 1.7 waves of 76 pairs, a tile
+// is 16 steps, and starting, switching tiles and ending take 5 us.
 // Warps: 0 TMA, 1 tensor memory and (in the leading block) MMA issue, 2-3
 // scales, 4-11 promotion (a lane quarter, 128 columns each).
 struct Pair {
