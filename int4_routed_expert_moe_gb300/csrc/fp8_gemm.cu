@@ -1039,7 +1039,8 @@ FfnWs ffn_ws(int T, int H, int Is) {
   w.xs = o; o += round256((size_t)T * blocks128(H) * 4);
   w.hq = o; o += round256((size_t)T * Is);
   w.hs = o; o += round256((size_t)T * blocks128(Is) * 4);
-  w.hf = o; o += T <= kGemvMaxTokens ? round256((size_t)T * Is * 4) : 0;
+  // In every size, so that a workspace for T tokens serves fewer.
+  w.hf = o; o += round256((size_t)std::min(T, kGemvMaxTokens) * Is * 4);
   w.total = o;
   return w;
 }

@@ -59,3 +59,7 @@ def test_fp8_workspace_sizes():
     assert moe.moe_shared_fp8_workspace_bytes(4, 96, 64) == 0
     T, H, Is = 100, 512, 320
     assert moe.moe_shared_fp8_workspace_bytes(T, H, Is) >= 256 + T * (H + Is) + T * (4 + 3) * 4
+    # A workspace for T tokens serves any smaller batch.
+    for H, Is in ((64, 64), (512, 320), (64, 4096)):
+        sizes = [moe.moe_shared_fp8_workspace_bytes(T, H, Is) for T in range(0, 70)]
+        assert sizes == sorted(sizes)

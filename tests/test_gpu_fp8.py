@@ -169,6 +169,18 @@ def test_product_large_sampled():
     _check_product(y[r], xq[r], xs[r], wq, ws)
 
 
+@pytest.mark.parametrize("T,N,K", [(2048, 1001, 1040), (2048, 1004, 528), (1900, 1288, 272), (600, 4096, 272)])
+def test_product_many_tokens_sampled(T, N, K):
+    # Many-token tiles with ragged edges: rows that TMA can store and rows that it cannot (N odd, N even).
+    rng = np.random.default_rng(T + N)
+    xq, xs = _quantize(_acts(rng, T, K), 1)
+    wq, ws = _quantize(_weights(rng, N, K), 128)
+    y = _matmul(xq, xs, wq, ws)
+    r = np.unique(np.r_[0:4, 30:34, 126:130, 254:258, T // 2, T - 140:T - 120, T - 3:T])
+    _check_product(y[r], xq[r], xs[r], wq, ws)
+    assert not (y == 777.0).any()
+
+
 def test_product_scales_of_every_block():
     # Codes 1.0 throughout, scales distinct powers of two per block: each block's sum is exact,
     # so every misplaced scale shows.
@@ -321,7 +333,8 @@ def _check_ffn(y, x, w):
 
 @pytest.mark.parametrize("T,H,Is", [(1, 64, 64), (1, 2048, 1024), (2, 256, 192), (4, 320, 4096), (16, 1024, 640),
                                     (31, 128, 1344), (64, 512, 128), (65, 2048, 320), (128, 192, 256), (130, 512, 320),
-                                    (300, 1024, 1024), (513, 256, 512)])
+                                    (300, 1024, 1024), (513, 256, 512), (8, 512, 1344), (12, 64, 192), (9, 1088, 64),
+                                    (3, 64, 704), (1024, 128, 192)])
 def test_ffn_matches_oracle(T, H, Is):
     rng = np.random.default_rng(T + H + Is)
     x = rng.normal(size=(T, H)).astype(np.float16)
@@ -378,6 +391,45 @@ def test_ffn_equals_its_parts():
     parts = _matmul(hq, hs, w[4], w[5])
     y = _ffn(x, w)
     assert np.abs(parts.astype(float) - y).max() <= 2e-2 * np.abs(parts).max()
+
+
+def test_ffn_workspace_serves_calls_of_other_sizes():
+    # One workspace for a decode step, a prefill and a decode step again.
+    rng = np.random.default_rng(21)
+    H, Is = 256, 320
+    w = _ffn_weights(rng, H, Is)
+    args = [_codes(a) if a.dtype == np.uint8 else torch.from_numpy(a).cuda() for a in w]
+    ws = torch.zeros(moe.moe_shared_fp8_workspace_bytes(400, H, Is), dtype=torch.uint8, device="cuda")
+    assert ws.numel() >= moe.moe_shared_fp8_workspace_bytes(16, H, Is)
+    for T in (1, 400, 5, 16, 90, 1):
+        x = rng.normal(size=(T, H)).astype(np.float16)
+        y = torch.empty((T, H), dtype=torch.float16, device="cuda")
+        moe.moe_shared_forward_fp8(torch.from_numpy(x).cuda(), *args, y, ws)
+        assert moe.moe_workspace_flags(ws) == 0
+        _check_ffn(y.cpu().numpy(), x, w)
+
+
+def test_calls_in_a_graph_repeat():
+    # Quantisation, product and FFN captured once and replayed on new inputs in the same buffers.
+    rng = np.random.default_rng(22)
+    H, Is = 512, 256
+    w = _ffn_weights(rng, H, Is)
+    args = [_codes(a) if a.dtype == np.uint8 else torch.from_numpy(a).cuda() for a in w]
+    for T in (2, 40, 300):
+        x = torch.zeros((T, H), dtype=torch.float16, device="cuda")
+        y = torch.empty_like(x)
+        ws = torch.zeros(moe.moe_shared_fp8_workspace_bytes(T, H, Is), dtype=torch.uint8, device="cuda")
+        moe.moe_shared_forward_fp8(x, *args, y, ws)
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            moe.moe_shared_forward_fp8(x, *args, y, ws)
+        for _ in range(2):
+            xn = rng.normal(size=(T, H)).astype(np.float16)
+            x.copy_(torch.from_numpy(xn))
+            g.replay()
+            torch.cuda.synchronize()
+            _check_ffn(y.cpu().numpy(), xn, w)
 
 
 def test_ffn_refusals():
