@@ -393,8 +393,9 @@ size_t moe_matmul_fp8_workspace_bytes(int T, int N, int K);
 int moe_matmul_fp8(const void* xq, const float* xs, int T, const void* wq, const float* ws, int N,
                    int K, void* y, void* workspace, size_t workspace_bytes, void* stream);
 /* moe_shared_forward with FP8 weights: x is quantised in 1 x 128 blocks,
- * h = silu(W_g x) * (W_u x) is formed in FP32 and quantised the same way, and
- * y = W_d h. Both products as moe_matmul_fp8.
+ * h = silu(W_g x) * (W_u x) is formed in FP32 and quantised the same way (a
+ * block of h with amax < 448 * 2^-126 as one of zeros), and y = W_d h. Both
+ * products as moe_matmul_fp8.
  * x device fp16 [T][H]; wg, wu device codes [Is][H] with scales sg, su
  * [ceil(Is/128)][ceil(H/128)]; wd device codes [H][Is] with scales sd
  * [ceil(H/128)][ceil(Is/128)]; y device fp16 [T][H] out.

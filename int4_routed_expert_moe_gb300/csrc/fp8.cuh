@@ -12,6 +12,7 @@ namespace fp8 {
 
 constexpr int kBlock = 128;       // elements of K per scale
 constexpr float kMax = 448.0f;    // largest E4M3 value
+constexpr float kMinAmax = 0x1p-126f * kMax;  // below, the scale is no normal number
 
 // Running maximum of |x| over eight FP16 values, as two 16-bit patterns: the
 // patterns of non-negative values order as the values do, infinities and NaN
@@ -27,15 +28,19 @@ struct BlockScale {
   float scale;  // amax / 448: what a code is multiplied by
   float inv;    // 448 / amax: what a value is multiplied by
 };
-// A block of zeros has scale 0 and codes 0; a block that holds an infinity or
-// NaN has scale and codes NaN, so that what is computed from it says so.
+// A block of zeros has scale 0 and codes 0, and so has one whose scale would be
+// below FP32's normal numbers (an intermediate h may come to that, FP16 values
+// cannot): 448 / amax would overflow, and its zeros times infinity be NaN. A
+// block that holds an infinity or NaN has scale and codes NaN, so that what is
+// computed from it says so.
 __device__ __forceinline__ BlockScale block_scale(float amax) {
   BlockScale b;
   if (!(amax < INFINITY)) {
     b.scale = b.inv = __int_as_float(0x7fffffff);
   } else {
-    b.scale = amax / kMax;
-    b.inv = amax > 0.0f ? kMax / amax : 0.0f;
+    const bool some = amax >= kMinAmax;
+    b.scale = some ? amax / kMax : 0.0f;
+    b.inv = some ? kMax / amax : 0.0f;
   }
   return b;
 }

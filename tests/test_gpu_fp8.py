@@ -371,6 +371,20 @@ def test_ffn_zero_and_nonfinite_tokens(T):
         _check_ffn(y[keep], x[keep], w)
 
 
+@pytest.mark.parametrize("Is", [64, 1024, 4608])
+@pytest.mark.parametrize("T", [1, 9, 60, 300])
+def test_ffn_vanishing_intermediate(T, Is):
+    # Gate and up near 1e-20: h near 1e-40 and in places 0, where 448 / amax is
+    # past FP32. y rounds to 0 in FP16, and nothing in it is NaN.
+    rng = np.random.default_rng(T + Is)
+    x = rng.normal(size=(T, 256)).astype(np.float16)
+    w = _ffn_weights(rng, 256, Is)
+    w[1], w[3] = np.full_like(w[1], 1e-22), np.full_like(w[3], 1e-22)
+    w[2][::5] = 0
+    assert np.abs(f8.shared_ffn(x, *w)["y"]).max() < 2.0 ** -25
+    assert not _ffn(x, w).any()
+
+
 @pytest.mark.parametrize("T", [1, 60, 300])
 def test_ffn_repeats_bit_for_bit(T):
     rng = np.random.default_rng(T)
