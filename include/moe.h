@@ -367,7 +367,8 @@ int moe_shared_forward(const void* x, int T, int H, int Is, const void* wg,
  * moe_shared_forward; these calls serve checkpoints that ship them in FP8.)
  *
  * moe_quantize_fp8: per block, amax = max |x|, s = amax / 448 and
- * q = E4M3(x * (448 / amax)), rounded to nearest even; every step in FP32.
+ * q = E4M3(x * (448 * (1 / amax))), rounded to nearest even; every step in
+ * FP32 (PyTorch's own x * (448.0 / amax) gives the same codes).
  * A block of zeros has s = 0 and codes 0; one that holds an infinity or NaN
  * has s = NaN and codes NaN.
  * x       device fp16 [rows][cols]

@@ -26,13 +26,19 @@ __device__ __forceinline__ uint32_t amax_bits(const uint4& v, uint32_t m) {
 
 struct BlockScale {
   float scale;  // amax / 448: what a code is multiplied by
-  float inv;    // 448 / amax: what a value is multiplied by
+  float inv;    // 448 * (1 / amax): what a value is multiplied by
 };
 // A block of zeros has scale 0 and codes 0, and so has one whose scale would be
 // below FP32's normal numbers (an intermediate h may come to that, FP16 values
 // cannot): 448 / amax would overflow, and its zeros times infinity be NaN. A
 // block that holds an infinity or NaN has scale and codes NaN, so that what is
 // computed from it says so.
+// inv is the reciprocal, rounded, times 448, rounded: what PyTorch computes for
+// 448.0 / amax, so that the codes are those of x * (448.0 / amax) there, bit for
+// bit. One rounded division gives other codes only where x * 448 / amax is at or
+// within 2^-22 of a tie (7e-5 of FP16 normal values), and both codes are as near
+// to x: distance 0.025715586 of |x| either way. In a product of one token such
+// a code is 1 % of the result, so the two choices are not left to chance.
 __device__ __forceinline__ BlockScale block_scale(float amax) {
   BlockScale b;
   if (!(amax < INFINITY)) {
@@ -40,7 +46,7 @@ __device__ __forceinline__ BlockScale block_scale(float amax) {
   } else {
     const bool some = amax >= kMinAmax;
     b.scale = some ? amax / kMax : 0.0f;
-    b.inv = some ? kMax / amax : 0.0f;
+    b.inv = some ? __frcp_rn(amax) * kMax : 0.0f;
   }
   return b;
 }

@@ -1,6 +1,6 @@
 // FP16 to FP8 (E4M3) with one FP32 scale per block: 1 x 128 for activations,
 // 128 x 128 for weights. Per block: amax = max |x|, s = amax / 448,
-// q = E4M3(x * (448 / amax)) rounded to nearest even, so that x ~ q * s and
+// q = E4M3(x * (448 * (1 / amax))) rounded to nearest even, so that x ~ q * s and
 // the largest value takes the type's largest code.
 //
 // Memory-bound: 2 bytes read and 1 written per element; every value is read

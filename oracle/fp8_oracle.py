@@ -62,7 +62,7 @@ def quantize(x: np.ndarray, block_rows: int, dtype=np.float32) -> tuple:
                 continue
             scales[i, j] = amax / dtype(MAX)
             if amax > 0:
-                codes[sl] = encode(b * (dtype(MAX) / amax))
+                codes[sl] = encode(b * (dtype(1) / amax * dtype(MAX)))  # as PyTorch computes MAX / amax
     return codes, scales
 
 

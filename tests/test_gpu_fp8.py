@@ -83,6 +83,22 @@ def test_quantize_nonfinite_block(v, br):
     assert np.array_equal(np.isnan(a), np.isnan(b)) and np.array_equal(np.nan_to_num(a), np.nan_to_num(b))
 
 
+@pytest.mark.parametrize("br", [1, 128])
+def test_quantize_codes_equal_eager(br):
+    # The codes of x * (448.0 / amax) in PyTorch, ties between two codes included:
+    # amax with few significant bits makes many of them.
+    g = torch.Generator(device="cuda").manual_seed(8)
+    x = torch.randn((1024, 2048), generator=g, device="cuda").half()
+    x[:512] = (x[:512] * 32).round().clamp(-96, 96) / 32
+    x[::128, ::128] = torch.tensor([3.0, 3.5, 7.0, 5.25], device="cuda").half().repeat(4)
+    b = x.float().view(1024 // br, br, 16, 128)
+    want = (b * (448.0 / b.abs().amax((1, 3), keepdim=True))).to(torch.float8_e4m3fn).view(1024, 2048)
+    q = torch.empty_like(want)
+    s = torch.empty((1024 // br, 16), device="cuda")
+    moe.moe_quantize_fp8(x, q, s, br)
+    assert torch.equal(q.view(torch.uint8), want.view(torch.uint8))
+
+
 def test_quantize_beyond_32_bit_offsets():
     R, C = 300_000, 8192  # 2.46e9 elements
     x = torch.empty((R, C), dtype=torch.float16, device="cuda").fill_(0.5)
