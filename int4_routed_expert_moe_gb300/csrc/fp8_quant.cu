@@ -23,7 +23,8 @@ __global__ void __launch_bounds__(256) quantize_rows_kernel(const __half* __rest
                                                             float* __restrict__ scales) {
   griddep_wait();
   griddep_launch_dependents();
-  const unsigned u = (blockIdx.x * 256u + threadIdx.x) >> 3;
+  // The call admits 2^30 - 1 units: their threads would not fit 32 bits.
+  const unsigned u = blockIdx.x * 32u + (threadIdx.x >> 3);
   const int sub = threadIdx.x & 7;
   const unsigned r = u / (unsigned)cblocks;
   const int cb = (int)(u - r * (unsigned)cblocks), c0 = cb * 128 + sub * 16;

@@ -114,6 +114,23 @@ def test_quantize_beyond_32_bit_offsets():
     assert (s[5] == 0.5 / 448).all() and (q[R - 7].float() == 448).all()
 
 
+def test_quantize_more_than_2_29_blocks():
+    # 2^29 + 1000 rows of one block each (16 columns): block numbers times eight lanes pass 32 bits.
+    R, C = (1 << 29) + 1000, 16
+    x = torch.full((R, C), 0.5, dtype=torch.float16, device="cuda")
+    rows = [0, 1, 999, 1000, (1 << 28) + 3, (1 << 29) - 1, 1 << 29, (1 << 29) + 1, (1 << 29) + 500, R - 1]
+    part = _acts(np.random.default_rng(4), len(rows), C)
+    x[rows] = torch.from_numpy(part).cuda()
+    q = torch.zeros((R, C), dtype=torch.uint8, device="cuda").view(torch.float8_e4m3fn)
+    s = torch.full((R, 1), 9.0, device="cuda")
+    moe.moe_quantize_fp8(x, q, s, 1)
+    rq, rs = f8.quantize(part, 1)
+    assert np.array_equal(s[rows].cpu().numpy(), rs)
+    assert np.array_equal(f8.decode(q.view(torch.uint8)[rows].cpu().numpy()), f8.decode(rq))
+    assert int((s == 0.5 / 448).sum()) >= R - len(rows)  # every other row holds halves
+    assert (q.view(torch.uint8)[R - 1000:R - 600:7] == 0x7E).float().mean() > 0.9
+
+
 def test_quantize_other_stream():
     x = _acts(np.random.default_rng(3), 100, 512)
     a, b = _quantize(x, 1), _quantize(x, 1, torch.cuda.Stream())
