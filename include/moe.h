@@ -163,7 +163,7 @@ int moe_route(const float* logits, int T, int E, int k, int renorm,
  * bias    device fp32 [E] or NULL
  * ids, weights, bad_tokens as moe_route: a token is bad if a logit or a bias
  *         is NaN or +inf, or if no expert can be picked.
- * Limits: E <= 1024, k <= 32, 1 <= top_groups <= n_groups <= 32, n_groups
+ * Limits: T up to 2^31 - 1, E <= 1024, k <= 32, 1 <= top_groups <= n_groups <= 32, n_groups
  * dividing E, k <= top_groups * E / n_groups; scale finite. FP32 throughout.
  */
 enum { MOE_SCORE_SOFTMAX = 0, MOE_SCORE_SIGMOID = 1 };

@@ -167,9 +167,11 @@ __global__ void __launch_bounds__(32 * kWarpsPerBlock) route_scored_kernel(const
       if (kBiasRegs) bias[j] = b;
     }
   }
-  for (int t0 = blockIdx.x * kWarpsPerBlock * kTok; t0 < a.T; t0 += gridDim.x * kWarpsPerBlock * kTok) {
-    const int t = t0 + slot;
-    const bool in = t < a.T;  // the last tokens' warps may be half empty
+  // Unsigned: the step after the last tokens may pass 2^31, not 2^32.
+  const unsigned T = (unsigned)a.T, step = gridDim.x * kWarpsPerBlock * kTok;
+  for (unsigned t0 = blockIdx.x * kWarpsPerBlock * kTok; t0 < T; t0 += step) {
+    const unsigned t = t0 + slot;
+    const bool in = t < T;  // the last tokens' warps may be half empty
     const uint8_t* row = static_cast<const uint8_t*>(a.logits) + (size_t)(in ? t : 0) * a.ld * (HALF ? 2 : 4);
     float v[PER];  // logits, then what orders the experts (-inf: not to be chosen)
     if (a.vec && n == PER) {
@@ -335,7 +337,7 @@ template <int PER, bool HALF, int L>
 cudaError_t launch_scored(const ScoredArgs& a, int sms, cudaStream_t st) {
   constexpr int kTokens = kWarpsPerBlock * (32 / L);  // per block and round
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)std::min((a.T + kTokens - 1) / kTokens, sms * 18));
+  cfg.gridDim = dim3(std::min(((unsigned)a.T + kTokens - 1) / kTokens, (unsigned)sms * 18));
   cfg.blockDim = dim3(32 * kWarpsPerBlock);
   cfg.stream = st;
   cudaLaunchAttribute attr[1];

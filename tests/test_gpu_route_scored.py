@@ -189,6 +189,27 @@ def test_rows_beyond_32_bit_offsets():
     assert np.array_equal(got[0], ref[0]) and np.allclose(got[1], ref[1], rtol=RTOL)
 
 
+def test_token_count_at_the_end_of_32_bits():
+    # 2^31 - 1 tokens of one expert: the token number of the step after the last ones passes 2^31.
+    T, dev, part = (1 << 31) - 1, torch.device("cuda"), 1 << 26
+    l = torch.empty((T, 1), dtype=torch.float16, device=dev)
+    for i in range(0, T, part):
+        n = min(part, T - i)
+        l[i:i + n, 0] = (torch.arange(i, i + n, device=dev) % 1009).float() / 128 - 4
+    nan = torch.tensor([5, T // 2, T - 30000, T - 1], device=dev)
+    l[nan] = float("nan")
+    ids = torch.full((T, 1), -7, dtype=torch.int32, device=dev)
+    w = torch.full((T, 1), 7.0, device=dev)
+    bad = torch.zeros(1, dtype=torch.int32, device=dev)
+    moe.moe_route_scored(moe.moe_route_config(score="sigmoid", renorm=False), l, 1, None, ids, w, bad)
+    assert int(bad) == 4 and (ids[nan] == -1).all() and not w[nan].any()
+    ids[nan], w[nan], l[nan] = 0, 0.5, 0.0
+    for i in range(0, T, part):
+        assert not ids[i:i + part].any()
+        ref = torch.sigmoid(l[i:i + part].double())
+        assert ((w[i:i + part] - ref).abs() <= RTOL * ref).all()
+
+
 def test_other_stream_and_repeatability():
     l = np.random.default_rng(4).normal(size=(500, 128)).astype(np.float32)
     lt = torch.from_numpy(l).cuda()
