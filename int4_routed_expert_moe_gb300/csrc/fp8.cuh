@@ -54,6 +54,17 @@ __device__ __forceinline__ BlockScale block_scale(uint32_t amax_half_bits) {
   return block_scale(__half2float(__ushort_as_half((unsigned short)amax_half_bits)));
 }
 
+// silu(v) = v / (1 + 2^(-v log2 e)) of the FFN's kernels, with the
+// special-function unit's own 2^x and 1/x (relative errors about 2^-22, and the
+// exponent's rounding, 2^-24 |v|). Below v = -87.3 the reciprocal is 0, and so
+// is the result; NaN and -infinity give NaN.
+__device__ __forceinline__ float silu(float v) {
+  float e, r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(v * -1.4426950408889634f));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + e));
+  return v * r;
+}
+
 // Two values to two E4M3 codes (a in the low byte), nearest even, saturating.
 __device__ __forceinline__ uint32_t encode2(float a, float b) {
   uint16_t r;

@@ -154,34 +154,19 @@ __device__ __forceinline__ float fmax_nan(float a, float b) {
   return r;
 }
 // h = silu(gate) * up of N values in place of gate, and their largest
-// magnitude (NaN or infinite if one of them is).
-// The special-function unit's own 2^x and 1/x (relative errors about 2^-22).
-constexpr float kLog2e = 1.4426950408889634f;
-__device__ __forceinline__ float exp2_approx(float v) {
-  float r;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
-  return r;
-}
-__device__ __forceinline__ float rcp_approx(float v) {
-  float r;
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
-  return r;
-}
-// silu(v) = v / (1 + exp(-v)); two values share one reciprocal, 1/a = b / (ab):
-// the special-function unit paces this epilogue (16 results per cycle and SM).
-// exp is capped at 2^60, so that ab stays finite: silu is then off by less
-// than 2^-53.
+// magnitude (NaN or infinite if one of them is). A reciprocal shared by two
+// SiLUs, 1/a = b / (ab), saves a quarter of the special-function results, but
+// ab overflows at strongly negative gates: with the exponent capped for that
+// silu(-60) came out 9e7 times too large, and a test for such gates costs more
+// than the reciprocals (2048 tokens of 2048 x 4096, us: capped 53.3, one
+// reciprocal each 53.6, shared behind a test 54.1).
 template <int N>
 __device__ __forceinline__ float swiglu(float (&gt)[N], const float (&up)[N]) {
   float m = 0.0f;
 #pragma unroll
-  for (int i = 0; i < N; i += 2) {
-    const float d0 = 1.0f + exp2_approx(fminf(gt[i] * -kLog2e, 60.0f));
-    const float d1 = 1.0f + exp2_approx(fminf(gt[i + 1] * -kLog2e, 60.0f));
-    const float r = rcp_approx(d0 * d1);
-    gt[i] = gt[i] * (r * d1) * up[i];
-    gt[i + 1] = gt[i + 1] * (r * d0) * up[i + 1];
-    m = fmax_nan(m, fmax_nan(fabsf(gt[i]), fabsf(gt[i + 1])));
+  for (int i = 0; i < N; ++i) {
+    gt[i] = fp8::silu(gt[i]) * up[i];
+    m = fmax_nan(m, fabsf(gt[i]));
   }
   return m;
 }

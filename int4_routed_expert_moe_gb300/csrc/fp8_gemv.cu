@@ -281,7 +281,7 @@ __global__ void __launch_bounds__(32 * kWarps, 2) fp8_gemv_kernel(const GemvArgs
     if (on && n0 + n < a.N) a.y[(size_t)t * a.N + n0 + n] = __float2half_rn(v[0]);
     return;
   }
-  const float h = silu_fast(v[0]) * v[NP - 1];
+  const float h = fp8::silu(v[0]) * v[NP - 1];
   if (HF) {
     if (on && n0 + n < a.N) a.h[(size_t)t * a.N + n0 + n] = h;
     return;

@@ -418,6 +418,29 @@ def test_ffn_vanishing_intermediate(T, Is):
     assert not _ffn(x, w).any()
 
 
+@pytest.mark.parametrize("T,H,Is", [(4, 256, 192), (4, 256, 4608), (16, 256, 640), (60, 256, 320), (64, 2048, 512),
+                                    (300, 256, 320), (2100, 256, 2304)])
+@pytest.mark.parametrize("gate,up", [(-45.0, 1e17), (-60.0, 1e24), (-80.0, 1e33), (-1e5, 1e15), (-1e12, 1e8)])
+def test_ffn_strongly_negative_gates(T, H, Is, gate, up):
+    # silu(-45) is -1.3e-18 and silu(-1e5) is 0: with up large enough y shows it. Every gate here is near
+    # `gate` and every up near `up`. A gate is off by up to 2^-20 of itself, h so by that much times |gate| (2e-4 at
+    # most; where |gate| is 1e5 it is 0 all the same), and each element by one step of its code more: an eighth.
+    rng = np.random.default_rng(T + Is)
+    x = rng.uniform(0.9, 1.1, (T, H)).astype(np.float16)
+    w = _ffn_weights(rng, H, Is)
+    w[0], w[2] = np.full_like(w[0], 0xB8), np.full_like(w[2], 0x38)  # codes -1 and 1
+    w[2][1::3] = 0xB8                                                # some ups negative
+    w[1], w[3] = np.full_like(w[1], -gate / H), np.full_like(w[3], up / H)
+    w[4] = w[4] & 0x7F                                               # W_d positive: sums do not cancel
+    w[5] = w[5] / 32                                                 # y within FP16
+    with np.errstate(over="ignore"):
+        r = f8.shared_ffn(x, *w)
+    assert (np.abs(r["y"]) > 1e-5).all() if gate > -1e4 else not r["y"].any()
+    y = _ffn(x, w).astype(np.float64)
+    assert np.isfinite(y).all()
+    assert (np.abs(y - r["y"]) <= 0.13 * r["ay"] + 2.0 ** -11 * np.abs(r["y"]) + 2.0 ** -25).all()
+
+
 @pytest.mark.parametrize("T", [1, 60, 300])
 def test_ffn_repeats_bit_for_bit(T):
     rng = np.random.default_rng(T)
