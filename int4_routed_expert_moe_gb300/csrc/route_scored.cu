@@ -132,9 +132,9 @@ constexpr int kHalfWarpTokens = 4096, kHalfWarpChunk = 4;  // see route_scored_k
 // Top-k: the k-th largest of the lanes' two best (k rounds of one reduction)
 // is a bound that at least k candidates reach (or all, where there are fewer);
 // the candidates that reach it are usually few more than k. Their indexes are
-// compacted to shared memory, and each lane ranks one of them by (v desc,
-// index asc), a 64-bit key, against the others. Where more than L reach the
-// bound, k rounds of argmax instead.
+// compacted to shared memory with their values, and each lane ranks one of
+// them by (v desc, index asc), a 64-bit key, against the others. Where more
+// than L reach the bound, k rounds of argmax instead.
 //
 // Bound by instruction issue (some 650 per token of 256 experts: 23.4 us for
 // 32768 tokens, whose logits alone would take 5 us). Half a warp per token pays
@@ -193,7 +193,8 @@ __global__ void __launch_bounds__(32 * kWarpsPerBlock) route_scored_kernel(const
       inv = 1.0f / lanes_sum<L>(s);
     }
     auto sigmoid = [](float l) { return sigmoid_f(l); };
-    auto softmax = [&](float l) { return exp_f(l - m) * inv; };
+    // Rounded before the bias is added: one FMA would order by other values than the score.
+    auto softmax = [&](float l) { return __fmul_rn(exp_f(l - m), inv); };
     // The lane's two best: in the order (p1, p2), and for the group's value.
     float p1 = -INFINITY, p2 = -INFINITY, g1, g2;
     auto two = [](float& x1, float& x2, float x) {
@@ -204,7 +205,7 @@ __global__ void __launch_bounds__(32 * kWarpsPerBlock) route_scored_kernel(const
 #pragma unroll
       for (int j = 0; j < PER; ++j) {
         const float b = kBiasRegs ? bias[kBiasRegs ? j : 0] : (j < n ? a.bias[first + j] : 0.0f);
-        v[j] = v[j] > -INFINITY ? score(v[j]) + b : -INFINITY;
+        v[j] = v[j] > -INFINITY ? __fadd_rn(score(v[j]), b) : -INFINITY;
         two(p1, p2, v[j]);
       }
     };
@@ -272,11 +273,17 @@ __global__ void __launch_bounds__(32 * kWarpsPerBlock) route_scored_kernel(const
       int pos = upto - mine;
 #pragma unroll
       for (int j = 0; j < PER; ++j)
-        if (v[j] >= lim) cand[pos++] = (unsigned long long)(unsigned)(first + j);
+        if (v[j] >= lim)
+          cand[pos++] = ((unsigned long long)__float_as_uint(v[j]) << 32) | (unsigned)(first + j);
     }
     __syncwarp();
     int my_i = -1, my_r = L;  // this lane's pick and its rank
-    if (few && lane < count) my_i = (int)(uint32_t)cand[lane];
+    unsigned long long me = 0;
+    if (few && lane < count) {
+      const unsigned long long c = cand[lane];
+      my_i = (int)(uint32_t)c;
+      me = ((unsigned long long)order_key(__uint_as_float((uint32_t)(c >> 32))) << 32) | (0xffffffffu - (uint32_t)c);
+    }
     if (__any_sync(full, !few)) {
       float bv = -INFINITY;
       int bi = INT_MAX;
@@ -300,14 +307,10 @@ __global__ void __launch_bounds__(32 * kWarpsPerBlock) route_scored_kernel(const
       }
       if (!few) my_r = lane;
     }
-    // The pick's score from its logit again: the same value as above.
-    float s = 0.0f;
-    unsigned long long me = 0;
+    float s = 0.0f;  // the pick's score, from its logit again
     if (my_i >= 0) {
       const float l = load_logit<HALF>(row, my_i);
       s = a.sigmoid ? sigmoid(l) : softmax(l);
-      const float o = a.bias ? s + a.bias[my_i] : l;
-      me = ((unsigned long long)order_key(o) << 32) | (0xffffffffu - (uint32_t)my_i);
     }
     __syncwarp();
     if (few) cand[lane] = me;

@@ -117,6 +117,29 @@ def test_ties_go_to_the_lowest_index():
         assert got[0].tolist() == [[0, 1, 2, 3, 4], [0, 1, 2, 3, 4], [40, 41, 42, 43, 44]]
 
 
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("T", [4000, 5000])
+def test_close_values_keep_their_order(score, T):
+    # Two experts whose score + bias are within a few FP32 roundings of each other: whichever
+    # comes first does so for one pick and for two.
+    rng = np.random.default_rng(T)
+    for b in rng.uniform(0.02, 0.4, 40):
+        if score == "softmax":  # s0 - s1 = tanh(d / 2) = b
+            d = 2 * np.arctanh(b)
+            base = rng.uniform(-2, 2, T)
+        else:                   # s0 - s1 = b around s1 = base
+            base = rng.uniform(-1, 0.2, T)
+            s1 = 1 / (1 + np.exp(-base))
+            d = -np.log(1 / (s1 + b) - 1) - base
+        l = np.stack([base + d, base], 1).astype(np.float32)
+        for _ in range(3):  # a few representable values to either side
+            l[:, 0] = np.where(rng.random(T) < 0.5, np.nextafter(l[:, 0], np.float32(9)), np.nextafter(l[:, 0], np.float32(-9)))
+        bias = [0.0, b]
+        one, two = _run(l, 1, bias, score=score)[0], _run(l, 2, bias, score=score)[0]
+        assert set(np.unique(one)) <= {0, 1} and (two.sum(1) == 1).all()
+        assert np.array_equal(one[:, 0], two[:, 0]), int((one[:, 0] != two[:, 0]).sum())
+
+
 def test_saturated_scores_are_ordered_by_logit():
     # 1 / (1 + exp(-40)) rounds to 1 in FP32: the logits still order the experts.
     l = (40.0 + np.random.default_rng(2).permutation(64)[None]).astype(np.float32)
