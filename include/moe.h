@@ -164,7 +164,14 @@ int moe_route(const float* logits, int T, int E, int k, int renorm,
  * ids, weights, bad_tokens as moe_route: a token is bad if a logit or a bias
  *         is NaN or +inf, or if no expert can be picked.
  * Limits: T up to 2^31 - 1, E <= 1024, k <= 32, 1 <= top_groups <= n_groups <= 32, n_groups
- * dividing E, k <= top_groups * E / n_groups; scale finite. FP32 throughout.
+ * dividing E, k <= top_groups * E / n_groups; scale finite.
+ * FP32 throughout. A weight is within 2e-6 of itself (a softmax takes l - max l
+ * rounded to FP32; scores below 2^-126 count as 0). The scores that order the
+ * experts are within (7 + 1.2 |l|) 2^-24 of themselves, at most 3e-7 (softmax:
+ * l - max l for l, and the normaliser's rounding): experts or groups whose
+ * values are closer than that may come in either order, the same one in every
+ * call with the same T, E, k and settings. (Batches of 4096 tokens and more may
+ * add a softmax's exponentials in another order than smaller ones.)
  */
 enum { MOE_SCORE_SOFTMAX = 0, MOE_SCORE_SIGMOID = 1 };
 enum { MOE_GROUP_MAX = 0, MOE_GROUP_TOP2 = 1 };

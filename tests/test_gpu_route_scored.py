@@ -117,6 +117,30 @@ def test_ties_go_to_the_lowest_index():
         assert got[0].tolist() == [[0, 1, 2, 3, 4], [0, 1, 2, 3, 4], [40, 41, 42, 43, 44]]
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, torch.float16])
+@pytest.mark.parametrize("T", [64, 4100])
+@pytest.mark.parametrize("score,renorm,units", [("sigmoid", False, 8), ("sigmoid", True, 20), ("softmax", False, 30)])
+def test_weights_of_large_logits(score, renorm, units, T, dtype):
+    # Logits of up to 80 either way, all representable in FP16 and their differences in FP32: what is left are the
+    # roundings, in units of 2^-24 of the weight. Sigmoid: the exponential 2 (one ulp), the sum 1, the reciprocal
+    # 2, the scale 1; renormalised: 5 each for the score and for the sum, 5 to add it up, the division and the
+    # scale; softmax: the exponential 2, the normaliser's exponentials 4 + 1.44 |l - max| (of weight
+    # exp(l - max) each: 14 on average at most), 8 to add them up, three products.
+    rng = np.random.default_rng(T + units)
+    c = np.linspace(-80, 78, T)[:, None] if score == "sigmoid" else 0.0
+    l = c + (rng.uniform(0, 2, (T, 32)) if score == "sigmoid" else rng.uniform(-80, 80, (T, 32)))
+    l = np.round(l * 16) / 16
+    lt = torch.from_numpy(l.astype(np.float32)).to(dtype).cuda()
+    got = _run(lt, 12, score=score, renorm=renorm, scale=1.5)
+    ref = f8.route_scored(l, 12, score=score, renorm=renorm, scale=1.5)
+    assert np.array_equal(got[0], ref[0])
+    big = ref[1] > 2.0 ** -125
+    assert big.mean() > 0.2
+    assert (np.abs(got[1] - ref[1])[big] <= units * 2.0 ** -24 * ref[1][big]).all(), (
+        np.abs(got[1] / ref[1] - 1)[big].max() * 2 ** 24)
+    assert (got[1][~big] <= 2.0 ** -124).all()
+
+
 @pytest.mark.parametrize("score", ["softmax", "sigmoid"])
 @pytest.mark.parametrize("T", [4000, 5000])
 def test_close_values_keep_their_order(score, T):
