@@ -505,16 +505,36 @@ def moe_shared_fp8_workspace_bytes(T: int, H: int, Is: int) -> int:
     return _lib.moe_shared_fp8_workspace_bytes(T, H, Is)
 
 
+def _shared_fp8_shapes(H: int, Is: int, w: dict) -> None:
+    """ValueError for the operand that is too small, or would be read with a row pitch that is not its own."""
+    for n, (rows, cols) in dict(g=(Is, H), u=(Is, H), d=(H, Is)).items():
+        for name, shape, flat in (("w" + n, (rows, cols), False), ("s" + n, (_nb(rows), _nb(cols)), True)):
+            t = w[name]
+            if not isinstance(t, torch.Tensor):
+                raise (ValueError if t is None else TypeError)(f"{name} must be a CUDA tensor")
+            # Scales may come as rows end to end, and with rows to spare.
+            if t.shape != shape and not (flat and t.numel() >= shape[0] * shape[1]
+                                         and (t.dim() != 2 or t.shape[1] == shape[1])):
+                raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+
+
 def moe_shared_forward_fp8(x: torch.Tensor, wg: torch.Tensor, sg: torch.Tensor, wu: torch.Tensor, su: torch.Tensor,
                            wd: torch.Tensor, sd: torch.Tensor, y: torch.Tensor, workspace: torch.Tensor,
                            stream=None) -> None:
     """moe_shared_forward with float8_e4m3fn weights and their 128 x 128 block scales."""
     T, H = x.shape
     Is = wg.shape[0]
-    n, ns = Is * H, _nb(H) * _nb(Is)
+    up, down, sup, sdown = (Is, H), (H, Is), (_nb(Is), _nb(H)), (_nb(H), _nb(Is))
+    try:  # the usual case in few steps
+        usual = (wg.shape == wu.shape == up and wd.shape == down and sg.shape == su.shape == sup
+                 and sd.shape == sdown)
+    except AttributeError:
+        usual = False
+    if not usual:
+        _shared_fp8_shapes(H, Is, dict(wg=wg, sg=sg, wu=wu, su=su, wd=wd, sd=sd))
     status = _lib.moe_shared_forward_fp8(
-        _dev(x, _F16, "x"), T, H, Is, _dev(wg, _FP8, "wg", n), _dev(sg, _F32, "sg", ns), _dev(wu, _FP8, "wu", n),
-        _dev(su, _F32, "su", ns), _dev(wd, _FP8, "wd", n), _dev(sd, _F32, "sd", ns), _dev(y, _F16, "y", T * H),
+        _dev(x, _F16, "x"), T, H, Is, _dev(wg, _FP8, "wg"), _dev(sg, _F32, "sg"), _dev(wu, _FP8, "wu"),
+        _dev(su, _F32, "su"), _dev(wd, _FP8, "wd"), _dev(sd, _F32, "sd"), _dev(y, _F16, "y", T * H),
         _dev(workspace, _U8, "workspace"), workspace.numel(), _stream(stream))
     if status:
         _check(status, "moe_shared_forward_fp8")

@@ -2,6 +2,7 @@
 import ctypes
 
 import pytest
+import torch
 
 from tests._lib import binding
 
@@ -63,3 +64,22 @@ def test_fp8_workspace_sizes():
     for H, Is in ((64, 64), (512, 320), (64, 4096)):
         sizes = [moe.moe_shared_fp8_workspace_bytes(T, H, Is) for T in range(0, 70)]
         assert sizes == sorted(sizes)
+
+
+def test_shared_fp8_weight_and_scale_shapes():
+    # Checked before any pointer is taken, so tensors of the host do: a matrix of another shape would be
+    # read with the wrong row pitch, or transposed.
+    T, H, Is = 3, 256, 640
+    code = lambda *s: torch.zeros(s, dtype=torch.uint8).view(torch.float8_e4m3fn)
+    x, y, ws = torch.zeros((T, H), dtype=torch.float16), torch.zeros((T, H), dtype=torch.float16), torch.zeros(1 << 20)
+    good = dict(wg=code(Is, H), sg=torch.zeros(5, 2), wu=code(Is, H), su=torch.zeros(5, 2), wd=code(H, Is),
+                sd=torch.zeros(2, 5))
+    call = lambda **kw: moe.moe_shared_forward_fp8(x, *{**good, **kw}.values(), y, ws)
+    for kw in (dict(wd=code(Is, H)), dict(wg=code(Is, 2 * H)), dict(wu=code(Is, H + 64)), dict(wu=code(2 * Is, H)),
+               dict(wu=code(Is - 64, H)), dict(wd=code(H, Is + 64)), dict(wd=code(2 * H, Is)),
+               dict(sd=torch.zeros(5, 2)), dict(sg=torch.zeros(2, 5)), dict(su=torch.zeros(5, 3))):
+        with pytest.raises(ValueError, match=next(iter(kw))):
+            call(**kw)
+    for kw in ({}, dict(sg=torch.zeros(10), sd=torch.zeros(64)), dict(su=torch.zeros(6, 2))):
+        with pytest.raises(TypeError, match="CUDA"):  # shapes and scales that are read as they are meant
+            call(**kw)
