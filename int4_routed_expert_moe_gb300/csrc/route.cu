@@ -21,8 +21,8 @@ __global__ void __launch_bounds__(128) route_kernel(
   griddep_wait();
   griddep_launch_dependents();
   const int lane = threadIdx.x & 31;
-  const int t = (blockIdx.x * blockDim.x + threadIdx.x) >> 5;
-  if (t >= T) return;
+  const unsigned t = blockIdx.x * 4u + (threadIdx.x >> 5);
+  if (t >= (unsigned)T) return;
   const float* row = logits + (size_t)t * E;
 
   float v[PER_LANE];
@@ -77,7 +77,7 @@ template <int PL>
 cudaError_t launch_route(const float* logits, int T, int E, int k, int renorm,
                          int32_t* ids, float* w, int32_t* bad, cudaStream_t st) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((T + 3) / 4);
+  cfg.gridDim = dim3(((unsigned)T + 3) / 4);
   cfg.blockDim = dim3(128);
   cfg.stream = st;
   cudaLaunchAttribute attr[1];

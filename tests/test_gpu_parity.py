@@ -59,6 +59,20 @@ def test_route_ties_and_nonfinite():
     assert ids[1].tolist() == [3, 2] and np.all(w[0] == 0)
 
 
+def test_route_of_more_than_2_27_tokens():
+    # 2^27 + 1000 tokens of two experts: token numbers times 32 lanes pass 32 bits.
+    T, dev = (1 << 27) + 1000, torch.device("cuda")
+    l = torch.zeros((T, 2), device=dev)
+    l[1::3, 1] = 1.0
+    ids = torch.full((T, 1), -7, dtype=torch.int32, device=dev)
+    w = torch.full((T, 1), 7.0, device=dev)
+    moe.moe_route(l, 1, False, ids, w)
+    want = (torch.arange(T, device=dev) % 3 == 1).int()
+    assert torch.equal(ids[:, 0], want)
+    s = 1 / (1 + np.exp(-1.0))  # softmax of (0, 1); of (0, 0) a half: within 4 FP32 roundings
+    assert ((w[:, 0] - torch.where(want > 0, s, 0.5)).abs() <= 2.0 ** -22).all()
+
+
 @pytest.mark.parametrize("T,k,E", [(4, 2, 8), (512, 8, 64), (256, 10, 512), (1, 8, 64),
                                    (4096, 16, 1024), (0, 8, 64), (1000, 3, 7)])
 def test_token_sort_matches_oracle(T, k, E):
