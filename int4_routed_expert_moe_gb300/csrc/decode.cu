@@ -284,6 +284,9 @@ int gemv_forward(const ForwardArgs& a) {
   const size_t smem_b = (size_t)k * I * 2 + (size_t)k * (I / 32) * 8 + (size_t)k * sizeof(void*) + (size_t)k * 4;
   if (smem_b > 200 * 1024)
     return fail(MOE_ERR_UNSUPPORTED, "GEMV path: k*I = %d too large for one block's shared memory", k * I);
+  if ((long long)T * k > 65535)
+    return fail(MOE_ERR_UNSUPPORTED, "GEMV path: T*k = %lld above the grid's 65535", (long long)T * k);
+  if (a.check_only) return MOE_OK;
   const dim3 grid_a((I + kWarps - 1) / kWarps, T * k);
   cudaError_t e;
   const int nit = (H / 32 + 31) / 32;

@@ -1338,6 +1338,7 @@ int fused_forward_routed(const ForwardArgs& fa, const float* logits, int renorm,
   a.rgu = (a.I + a.G - 1) / a.G;
   a.rdn = (a.H + a.G - 1) / a.G;
   if (!carve(a)) return fail(MOE_ERR_UNSUPPORTED, "streamed decode: shapes exceed shared memory");
+  if (fa.check_only) return MOE_OK;
   cudaError_t e;
   cudaStream_t st = fa.stream;
   if (xc == 1) e = hc == 1 ? launch_stream2<1, 1>(dev, a, st) : launch_stream2<1, 2>(dev, a, st);

@@ -85,6 +85,18 @@ int expert_args(const char* who, const moe_expert_shape* s, const void* x, int T
   return MOE_OK;
 }
 
+// The experts on path p (see pick_path).
+int run_experts(const moe::ForwardArgs& a, int p) {
+  if (p == MOE_PATH_GEMV) {
+    const int rc = moe::fused_forward(a);
+    if (rc != MOE_ERR_UNSUPPORTED) return rc;
+    moe::clear_error();  // shapes beyond the fused kernel's shared memory
+    return moe::gemv_forward(a);
+  }
+  if (p == MOE_PATH_GEMV_UNFUSED) return moe::gemv_forward(a);
+  return moe::grouped_forward(a);
+}
+
 }  // namespace
 
 extern "C" {
@@ -105,14 +117,7 @@ int moe_expert_forward(const moe_expert_shape* s, const void* x, int T,
   if (workspace_bytes < need)
     return moe::fail(MOE_ERR_CAPACITY, "moe_expert_forward: workspace %zu < %zu bytes", workspace_bytes, need);
   a.ws_bytes = workspace_bytes;
-  if (p == MOE_PATH_GEMV) {
-    const int frc = moe::fused_forward(a);
-    if (frc != MOE_ERR_UNSUPPORTED) return frc;
-    moe::clear_error();  // shapes beyond the fused kernel's shared memory
-    return moe::gemv_forward(a);
-  }
-  if (p == MOE_PATH_GEMV_UNFUSED) return moe::gemv_forward(a);
-  return moe::grouped_forward(a);
+  return run_experts(a, p);
 }
 
 int moe_expert_forward_zero_copy(const moe_expert_shape* s, const void* x, int T,
@@ -211,10 +216,14 @@ int moe_layer_forward_scored(const moe_expert_shape* s, const void* x, const moe
   const size_t need = moe_forward_workspace_bytes(s, T, k, E, path);
   if (workspace_bytes < need)
     return moe::fail(MOE_ERR_CAPACITY, "moe_layer_forward_scored: workspace %zu < %zu bytes", workspace_bytes, need);
+  a.ws_bytes = workspace_bytes;
+  a.check_only = true;  // the path's own limits too
+  const int p = moe::pick_path(path, T, k);
+  if ((rc = run_experts(a, p)) != MOE_OK) return rc;
+  a.check_only = false;
   rc = moe_route_scored(cfg, logits, logit_type, ld, T, E, k, bias, ids, weights, nullptr, stream);
   if (rc != MOE_OK) return rc;
-  return moe_expert_forward(s, x, T, ids, weights, k, E, pool, slot_of, n_slots, y_shared, y, workspace,
-                            workspace_bytes, path, stream);
+  return run_experts(a, p);
 }
 
 int moe_workspace_clear_flags(void* workspace, void* stream) {

@@ -697,6 +697,7 @@ int grouped_forward(const ForwardArgs& a) {
     return fail(MOE_ERR_UNSUPPORTED, "grouped path: needs E <= 1024 and T*k <= 65536 (E=%d, T*k=%d)", a.E, P);
   if (reinterpret_cast<uintptr_t>(a.y) % 16 || reinterpret_cast<uintptr_t>(a.y_shared) % 16)
     return fail(MOE_ERR_ARG, "grouped path: y and y_shared must be 16-byte aligned");
+  if (a.check_only) return MOE_OK;
   const GroupedWs w = grouped_ws(a.H, a.I, a.T, a.k, a.E);
   uint8_t* ws = static_cast<uint8_t*>(a.ws);
   int32_t* flags = reinterpret_cast<int32_t*>(ws);

@@ -55,6 +55,7 @@ struct ForwardArgs {
   // Two-kernel GEMV only: device alias of the layer's page-locked host source
   // [E][block]; experts without a slot are read from it in place. NULL: none.
   const uint8_t* host = nullptr;
+  bool check_only = false;  // the path's own limits alone: nothing is enqueued
 };
 
 size_t gemv_workspace_bytes(int H, int I, int T, int k);

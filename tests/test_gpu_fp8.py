@@ -555,6 +555,27 @@ def test_layer_with_scored_router_and_fp8_shared_path(T):
     assert err <= 5e-3 * np.abs(ref).max(), err
 
 
+@pytest.mark.parametrize("what", ["pairs", "grid", "alignment"])
+def test_layer_scored_refuses_what_its_path_does_not_take_before_enqueueing(what):
+    # More pairs than the grouped path sorts, or than the GEMV path's grid has rows; an output that the grouped
+    # path cannot store 16 bytes at a time.
+    shape, E, k = (256, 128, 64), 16, 8
+    T = 64 if what == "alignment" else 65536 // k + (what == "pairs")
+    path = moe.MOE_PATH_GEMV_UNFUSED if what == "grid" else moe.MOE_PATH_AUTO
+    lp = LayerPool(moe, 31, 0, shape, E)
+    x = torch.zeros((T, 256), dtype=torch.float16, device="cuda")
+    ids = torch.full((T, k), -9, dtype=torch.int32, device="cuda")
+    y = torch.zeros(T * 256 + 8, dtype=torch.float16, device="cuda")
+    y = y[1:T * 256 + 1] if what == "alignment" else y[:T * 256]
+    ws = torch.zeros(moe.moe_forward_workspace_bytes(shape, T, k, E, path), dtype=torch.uint8, device="cuda")
+    with pytest.raises(moe.MoeError) as ei:
+        moe.moe_layer_forward_scored(shape, x, moe.moe_route_config(), torch.zeros((T, E), device="cuda"), k, None, ids,
+                                     torch.zeros((T, k), device="cuda"), lp.pool, lp.slot_of, E, None, y, ws, path)
+    assert ei.value.status == (moe.MOE_ERR_ARG if what == "alignment" else moe.MOE_ERR_UNSUPPORTED)
+    torch.cuda.synchronize()
+    assert (ids == -9).all()
+
+
 def test_layer_scored_refuses_before_enqueueing():
     shape, E, k = (256, 128, 64), 16, 4
     lp = LayerPool(moe, 31, 0, shape, E)
