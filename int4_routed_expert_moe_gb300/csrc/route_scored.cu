@@ -237,7 +237,8 @@ __global__ void __launch_bounds__(32 * kWarpsPerBlock) route_scored_kernel(const
         g2 = fmaxf(fminf(g1, h1), fmaxf(g2, h2));
         g1 = fmaxf(g1, h1);
       }
-      const float gv = a.rank_top2 && g2 > -INFINITY ? g1 + g2 : g1;
+      // Two biases of FP32's lowest value do not add up to what a group without experts is worth.
+      const float gv = a.rank_top2 && g2 > -INFINITY ? fmaxf(g1 + g2, -FLT_MAX) : g1;
       // How many groups come before this one: its lanes share the comparisons.
       int before = 0;
       for (int h0 = 0; h0 < a.G; h0 += lanes) {

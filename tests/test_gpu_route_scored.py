@@ -196,6 +196,18 @@ def test_masks_and_bad_tokens(score, biased, G, rank):
     assert got[0][6].tolist() == [17] + [-1] * 5
 
 
+@pytest.mark.parametrize("T", [3, 4100])
+def test_bias_of_the_lowest_value_ranks_above_no_expert(T):
+    # Two experts biased by FP32's lowest value: their sum is still above that of a group without experts.
+    l = np.zeros((T, 8), np.float32)
+    l[:, :2] = l[:, 6:] = -np.inf
+    bias = np.full(8, np.finfo(np.float32).min)
+    cfg = dict(score="sigmoid", n_groups=4, top_groups=1, group_rank="top2")
+    got = _run(l, 2, bias, **cfg)
+    assert (got[0] == [2, 3]).all() and np.allclose(got[1], 0.5) and got[2] == 0
+    assert f8.route_scored(l[:1], 2, bias=bias, **cfg)[0].tolist() == [[2, 3]]
+
+
 def test_bias_masks_and_bad_bias():
     l = np.random.default_rng(8).normal(size=(9, 16)).astype(np.float32)
     bias = np.zeros(16, np.float32)
