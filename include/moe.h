@@ -166,7 +166,7 @@ int moe_route(const float* logits, int T, int E, int k, int renorm,
  * Limits: T up to 2^31 - 1, E <= 1024, k <= 32, 1 <= top_groups <= n_groups <= 32, n_groups
  * dividing E, k <= top_groups * E / n_groups; scale finite.
  * FP32 throughout. A weight is within 2e-6 of itself (a softmax takes l - max l
- * rounded to FP32; scores below 2^-126 count as 0). The scores that order the
+ * rounded to FP32; scores below 2^-126 may count as 0). The scores that order the
  * experts are within (7 + 1.2 |l|) 2^-24 of themselves, at most 3e-7 (softmax:
  * l - max l for l, and the normaliser's rounding): experts or groups whose
  * values are closer than that may come in either order, the same one in every

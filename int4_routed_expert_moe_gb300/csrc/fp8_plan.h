@@ -23,7 +23,8 @@ struct Plan {
 //   what its bytes need at 68 GB/ms per SM; joining a split costs 0.5 and
 //   0.0125 per column;
 //   pairs: 4.2 to start and end, 0.38 per step, 1.5 per tile after the first
-//   (gate/up 2.0: SiLU and the quantisation).
+//   (gate/up 2.0: SiLU and the quantisation). The products' runs alone were
+//   fitted; gate/up takes their terms and that one of its own.
 inline Plan plan_of(int T, int N, int nb, int sms, bool gateup) {
   const int mt = (T + kPlanTokens - 1) / kPlanTokens, kn_pair = gateup ? 128 : 256;
   const int pair_tiles = ((T + 255) / 256) * ((N + kn_pair - 1) / kn_pair);

@@ -141,13 +141,14 @@ constexpr int kHalfWarpTokens = 4096, kHalfWarpChunk = 4;  // see route_scored_k
 // them by (v desc, index asc), a 64-bit key, against the others. Where more
 // than L reach the bound, k rounds of argmax instead.
 //
-// Bound by instruction issue (some 650 per token of 256 experts: 23.4 us for
+// Bound by instruction issue (some 660 per token of 256 experts: 22.9 us for
 // 32768 tokens, whose logits alone would take 5 us). Half a warp per token pays
 // the reductions, the scan and the ranking once for two tokens, but holds twice
-// the experts per lane. Measured, us for 32768 tokens, warp against half: 20
-// experts 13.5 / 8.8, 64 experts 15.5 / 10.2, 256 experts 23.4 / 24.3, 512
-// experts 43 / 83; up to 2048 tokens of 64 experts 2.8 / 3.1. So half a warp
-// where that leaves a lane at most 4 experts and there are 4096 tokens.
+// the experts per lane. Measured with sigmoid scores and a bias, us for 32768
+// tokens, warp against half: 20 experts 13.4 / 8.6, 64 experts 17.7 / 11.5, 256
+// experts 23.0 / 21.8 (16 experts per lane), 512 experts 37 / 74 (32); 64
+// experts, 2048 tokens 3.1 / 3.3, 4096 tokens 5.1 / 3.6. So half a warp where
+// that leaves a lane at most 4 experts and there are 4096 tokens.
 template <int PER, bool HALF, int L>
 __global__ void __launch_bounds__(32 * kWarpsPerBlock) route_scored_kernel(const ScoredArgs a) {
   constexpr bool kBiasRegs = PER <= 16;  // a lane's biases stay in registers over its tokens
