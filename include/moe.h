@@ -416,6 +416,128 @@ int moe_shared_forward_fp8(const void* x, int T, int H, int Is, const void* wg, 
                            const void* wu, const float* su, const void* wd, const float* sd,
                            void* y, void* workspace, size_t workspace_bytes, void* stream);
 
+/* ---- norms before and after a block ---------------------------------------
+ * The FP16 steps round the routed layer, one pass over each token's row:
+ *   RMS:    norm(v) = v / sqrt(mean(v^2) + eps) * (w + weight_offset)
+ *   layer:  norm(v) = (v - mean(v)) / sqrt(mean((v - mean(v))^2) + eps) * (w + weight_offset) + b
+ * moe_norm (before a block): y = norm(x), as FP16 (y), as E4M3 codes with a
+ * scale per 1 x 128 block (q, scales: as moe_quantize_fp8, from the FP32
+ * values), or both.
+ * moe_norm_residual (after a block, with what comes before the next one):
+ *   a = branch, or norm(branch) with post_w, post_b if post_w is not NULL;
+ *   h = residual_scale * residual + scale * gate * a;
+ *   y = norm(h) with w, b, as FP16, as codes, or both, if y or q is not NULL.
+ * All in FP32; each output is rounded once, y from h before h's own rounding.
+ * x, residual, h  device [T][H] of x_type / stream_type (MOE_F16 or MOE_F32);
+ *           residual may be NULL (then h = scale * gate * a), h may be NULL
+ *           (not stored)
+ * branch    device fp16 [T][H]
+ * w, post_w device fp16 [H]; b, post_b device fp16 [H] or NULL, only with
+ *           MOE_NORM_LAYER
+ * gate      per gate_kind: MOE_GATE_TOKEN device fp32 [T], MOE_GATE_CHANNEL
+ *           device fp16 [H], MOE_GATE_ELEMENT device fp16 [T][H];
+ *           MOE_GATE_NONE: 1
+ * y         device fp16 [T][H] out; q device codes [T][H] out; scales device
+ *           fp32 [T][ceil(H / 128)] out (with q)
+ * h may be the residual's own buffer, y that of branch or of an FP16 x; other
+ * overlaps are not allowed.
+ * A row with an infinity or NaN gives what the formulas give; a row whose sum
+ * of squares is beyond FP32 has the reciprocal 0.
+ * Limits: H a multiple of 8 up to 16384 (of 16 with q); buffers 16-byte
+ * aligned, token gates and scales 4-byte; eps >= 0; eps, offset, scale and
+ * residual_scale finite. T = 0 enqueues nothing.
+ */
+enum { MOE_NORM_RMS = 0, MOE_NORM_LAYER = 1 };
+enum { MOE_GATE_NONE = 0, MOE_GATE_TOKEN = 1, MOE_GATE_CHANNEL = 2, MOE_GATE_ELEMENT = 3 };
+typedef struct {
+  int32_t kind;         /* MOE_NORM_* */
+  float eps;
+  float weight_offset;  /* 1 for weights stored around zero */
+} moe_norm_cfg;
+int moe_norm(const moe_norm_cfg* cfg, const void* x, int x_type, int T, int H, const void* w,
+             const void* b, void* y, void* q, float* scales, void* stream);
+int moe_norm_residual(const moe_norm_cfg* cfg, const void* branch, const void* residual,
+                      int stream_type, int T, int H, const void* post_w, const void* post_b,
+                      const void* gate, int gate_kind, float scale, float residual_scale, void* h,
+                      const void* w, const void* b, void* y, void* q, float* scales, void* stream);
+
+/* ---- FP16 product with bias, activation and residual -----------------------
+ * y = act(x W^T + bias) + residual: the router's gate (FP32 logits) and the
+ * other dense FP16 projections round the routed layer.
+ * x        device fp16, row t at x + t * ldx elements (ldx >= K, a multiple of 8)
+ * w        device fp16 [N][K]
+ * bias     device fp32 [N] or NULL
+ * act      MOE_ACT_*: none, max(v, 0), v sigmoid(v), v Phi(v) (gelu),
+ *          v/2 (1 + tanh(sqrt(2/pi) (v + 0.044715 v^3))) (gelu_tanh), sigmoid(v)
+ * residual device, of y's type, row t at residual + t * ldr (ldr >= N), or
+ *          NULL; may be y itself with ldr = ldy
+ * y        device, y_type MOE_F16 or MOE_F32, row t at y + t * ldy (ldy >= N);
+ *          columns past N are left as they were
+ * Products and sums in FP32, bias, activation and residual too; one rounding.
+ * NaN in x W^T gives NaN for every activation.
+ * workspace >= moe_linear_workspace_bytes(T, N, K), 256-aligned, zero-filled
+ * before its first use; its first 4 bytes are the sticky error word (bit 2: a
+ * bounded device wait expired, y is not valid). One that serves T tokens
+ * serves fewer.
+ * Limits: T <= 2^20, N <= 65536, K a multiple of 8 up to 65536; strides up to
+ * 2^31 - 1 elements; x, w, y and residual 16-byte aligned, bias 4-byte. Errors:
+ * MOE_ERR_ARG, MOE_ERR_CAPACITY, MOE_ERR_CUDA.
+ */
+enum { MOE_ACT_NONE = 0, MOE_ACT_RELU = 1, MOE_ACT_SILU = 2, MOE_ACT_GELU = 3, MOE_ACT_GELU_TANH = 4,
+       MOE_ACT_SIGMOID = 5 };
+size_t moe_linear_workspace_bytes(int T, int N, int K);
+int moe_linear(const void* x, long long ldx, int T, int K, const void* w, int N, const float* bias,
+               int act, const void* residual, long long ldr, void* y, int y_type, long long ldy,
+               void* workspace, size_t workspace_bytes, void* stream);
+
+/* ---- balance loss and per-expert counts -----------------------------------
+ * What keeps a router's experts evenly used, by sequence. The tokens of
+ * sequence s are offsets[s] .. offsets[s+1] - 1; p are the router's
+ * probabilities, softmax(l) or sigmoid(l_e) / sum_j sigmoid(l_j):
+ *   c_se = picks of expert e by the sequence's tokens (ids == e, every choice)
+ *   n_s  = its tokens whose logits hold no NaN or +inf and are not all -inf
+ *   P_se = sum over those tokens of p_te / n_s (0 if n_s = 0)
+ *   loss = coef * mean over the sequences with n_s > 0 of sum_e f_se P_se,
+ *          f_se = E c_se / (k n_s)   (0 if there are none)
+ * and, with f held fixed and g the loss's own gradient,
+ *   d loss / d l_te = g coef / (S' n_s) p_te (f_se - sum_j f_sj p_tj)
+ *                     (sigmoid: times 1 - sigmoid(l_te)), S' sequences with n_s > 0.
+ * logits   device, logit_type MOE_F32 or MOE_F16, row t at logits + t * ld (ld >= E)
+ * ids      device int32 [T][k], as moe_route and moe_route_scored give them;
+ *          ids outside [0, E) count for nothing
+ * offsets  device int32 [S+1], not decreasing, within [0, T]; NULL: one
+ *          sequence of all T tokens (S = 1). Tokens before offsets[0] and from
+ *          offsets[S] on belong to no sequence. (Others are clamped to [0, T];
+ *          what decreasing ones give is not defined, but stays in bounds.)
+ * counts   device int32 [S][E] out: c; tokens device int32 [S] out: n;
+ * mean     device fp32 [S][E] out: P, or NULL; loss device fp32 [1] out, or NULL
+ * The backward call takes counts and tokens as the forward call left them.
+ * grad_loss device fp32 [1] or NULL (1)
+ * dlogits  device fp32, row t at dlogits + t * ldd (ldd >= E): written, or
+ *          added to if accumulate. Rows of a sequence's tokens that n_s leaves
+ *          out get 0 (or stay); rows of no sequence stay as they were.
+ * FP32 per token; sums over tokens in a fixed order that depends on T, E and
+ * the offsets alone: the same inputs give the same bits.
+ * workspace >= moe_balance_workspace_bytes(T, E, S), 256-aligned, zero-filled
+ * before its first use and left reusable. Calls that share one must be ordered.
+ * Limits: T <= 2^27, T * k <= 2^31 - 1, E <= 1024, k <= min(E, 32),
+ * 1 <= S <= 65535; coef finite. T = 0 is a batch without tokens: counts,
+ * tokens, mean and loss are zeros.
+ */
+typedef struct {
+  int32_t score;  /* MOE_SCORE_* */
+  float coef;
+} moe_balance_cfg;
+size_t moe_balance_workspace_bytes(int T, int E, int S);
+int moe_balance_loss(const moe_balance_cfg* cfg, const void* logits, int logit_type, long long ld,
+                     int T, int E, const int32_t* ids, int k, const int32_t* offsets, int S,
+                     int32_t* counts, int32_t* tokens, float* mean, float* loss, void* workspace,
+                     size_t workspace_bytes, void* stream);
+int moe_balance_loss_backward(const moe_balance_cfg* cfg, const void* logits, int logit_type,
+                              long long ld, int T, int E, int k, const int32_t* offsets, int S,
+                              const int32_t* counts, const int32_t* tokens, const float* grad_loss,
+                              float* dlogits, long long ldd, int accumulate, void* stream);
+
 /* ---- residency manager ----------------------------------------------------
  * Per-layer GPU slot pools fed from a complete, immutable host source
  * ("03 / Arquitetura", ADR 0009). One decode step of one layer:

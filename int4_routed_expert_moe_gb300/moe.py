@@ -57,6 +57,19 @@ class moe_route_cfg(ctypes.Structure):
         ("scale", ctypes.c_float)]
 
 
+MOE_NORM_RMS, MOE_NORM_LAYER = 0, 1
+MOE_GATE_NONE, MOE_GATE_TOKEN, MOE_GATE_CHANNEL, MOE_GATE_ELEMENT = 0, 1, 2, 3
+(MOE_ACT_NONE, MOE_ACT_RELU, MOE_ACT_SILU, MOE_ACT_GELU, MOE_ACT_GELU_TANH, MOE_ACT_SIGMOID) = range(6)
+
+
+class moe_norm_cfg(ctypes.Structure):
+    _fields_ = [("kind", ctypes.c_int32), ("eps", ctypes.c_float), ("weight_offset", ctypes.c_float)]
+
+
+class moe_balance_cfg(ctypes.Structure):
+    _fields_ = [("score", ctypes.c_int32), ("coef", ctypes.c_float)]
+
+
 MOE_POLICY_DECAY, MOE_POLICY_LRU, MOE_POLICY_PINNED = 0, 1, 2
 
 
@@ -100,6 +113,10 @@ _I = ctypes.c_int
 _SZ = ctypes.c_size_t
 _SHAPE = ctypes.POINTER(moe_expert_shape)
 _CFG = ctypes.POINTER(moe_route_cfg)
+_NORM = ctypes.POINTER(moe_norm_cfg)
+_BAL = ctypes.POINTER(moe_balance_cfg)
+_LL = ctypes.c_longlong
+_F = ctypes.c_float
 
 _SIGS = {
     "moe_status_string": (ctypes.c_char_p, [_I]),
@@ -129,6 +146,13 @@ _SIGS = {
     "moe_matmul_fp8": (_I, [_P, _P, _I, _P, _P, _I, _I, _P, _P, _SZ, _P]),
     "moe_shared_fp8_workspace_bytes": (_SZ, [_I, _I, _I]),
     "moe_shared_forward_fp8": (_I, [_P, _I, _I, _I, _P, _P, _P, _P, _P, _P, _P, _P, _SZ, _P]),
+    "moe_norm": (_I, [_NORM, _P, _I, _I, _I, _P, _P, _P, _P, _P, _P]),
+    "moe_norm_residual": (_I, [_NORM, _P, _P, _I, _I, _I, _P, _P, _P, _I, _F, _F, _P, _P, _P, _P, _P, _P, _P]),
+    "moe_linear_workspace_bytes": (_SZ, [_I, _I, _I]),
+    "moe_linear": (_I, [_P, _LL, _I, _I, _P, _I, _P, _I, _P, _LL, _P, _I, _LL, _P, _SZ, _P]),
+    "moe_balance_workspace_bytes": (_SZ, [_I, _I, _I]),
+    "moe_balance_loss": (_I, [_BAL, _P, _I, _LL, _I, _I, _P, _I, _P, _I, _P, _P, _P, _P, _P, _SZ, _P]),
+    "moe_balance_loss_backward": (_I, [_BAL, _P, _I, _LL, _I, _I, _I, _P, _I, _P, _P, _P, _P, _LL, _I, _P]),
     "moe_residency_create": (_I, [ctypes.POINTER(moe_residency_cfg), _P, _P, _P, _P, _P,
                                   ctypes.POINTER(_P)]),
     "moe_residency_prepare": (_I, [_P, _I, _P, _I]),
@@ -538,6 +562,183 @@ def moe_shared_forward_fp8(x: torch.Tensor, wg: torch.Tensor, sg: torch.Tensor, 
         _dev(workspace, _U8, "workspace"), workspace.numel(), _stream(stream))
     if status:
         _check(status, "moe_shared_forward_fp8")
+
+
+# ---- norms round a block -------------------------------------------------------
+_NORMS = {"rms": MOE_NORM_RMS, "layer": MOE_NORM_LAYER}
+
+
+def moe_norm_config(kind: str = "rms", eps: float = 1e-6, weight_offset: float = 0.0) -> moe_norm_cfg:
+    """A norm's settings (made once, passed to every call)."""
+    return moe_norm_cfg(_NORMS[kind], float(eps), float(weight_offset))
+
+
+def _stream_rows(x, name: str) -> tuple:
+    """(pointer, type, T, H) of a residual stream: float16 or float32 [T][H]."""
+    if not isinstance(x, torch.Tensor):
+        raise TypeError(f"{name} must be a CUDA tensor")
+    kind = _LOGIT_TYPES.get(x.dtype)
+    if kind is None:
+        raise TypeError(f"{name} must be float32 or float16, got {x.dtype}")
+    T, H = x.shape
+    return _dev(x, x.dtype, name), kind, T, H
+
+
+def _norm_outputs(y, q, scales, n: int, nb: int) -> tuple:
+    return (None if y is None else _dev(y, _F16, "y", n), None if q is None else _dev(q, _FP8, "q", n),
+            None if scales is None else _dev(scales, _F32, "scales", nb))
+
+
+def moe_norm(cfg: moe_norm_cfg, x: torch.Tensor, w: torch.Tensor, b: torch.Tensor | None = None,
+             y: torch.Tensor | None = None, q: torch.Tensor | None = None, scales: torch.Tensor | None = None,
+             stream=None) -> None:
+    """norm(x) of x [T][H] (float16 or float32) as float16 y, as float8_e4m3fn codes q with scales
+    [T][ceil(H / 128)], or both."""
+    ptr, kind, T, H = _stream_rows(x, "x")
+    py, pq, ps = _norm_outputs(y, q, scales, T * H, T * _nb(H))
+    status = _lib.moe_norm(cfg, ptr, kind, T, H, _dev(w, _F16, "w", H), None if b is None else _dev(b, _F16, "b", H),
+                           py, pq, ps, _stream(stream))
+    if status:
+        _check(status, "moe_norm")
+
+
+def _gate(gate, T: int, H: int) -> tuple:
+    """(pointer, kind): float32 [T] per token, float16 [H] per channel, float16 [T][H] per element."""
+    if not isinstance(gate, torch.Tensor):
+        raise TypeError("gate must be a CUDA tensor")
+    if gate.dtype is _F32 and gate.shape in ((T,), (T, 1)):
+        return _dev(gate, _F32, "gate"), MOE_GATE_TOKEN
+    if gate.dtype is _F16 and gate.shape == (H,):
+        return _dev(gate, _F16, "gate"), MOE_GATE_CHANNEL
+    if gate.dtype is _F16 and gate.shape == (T, H):
+        return _dev(gate, _F16, "gate"), MOE_GATE_ELEMENT
+    raise ValueError(f"gate must be float32 [{T}], float16 [{H}] or float16 [{T}][{H}], got {gate.dtype} "
+                     f"{list(gate.shape)}")
+
+
+def moe_norm_residual(cfg: moe_norm_cfg, branch: torch.Tensor, residual: torch.Tensor | None,
+                      h: torch.Tensor | None, post_w: torch.Tensor | None = None, post_b: torch.Tensor | None = None,
+                      gate: torch.Tensor | None = None, scale: float = 1.0, residual_scale: float = 1.0,
+                      w: torch.Tensor | None = None, b: torch.Tensor | None = None, y: torch.Tensor | None = None,
+                      q: torch.Tensor | None = None, scales: torch.Tensor | None = None, stream=None) -> None:
+    """h = residual_scale * residual + scale * gate * (branch or its norm with post_w); then, with y or q, the
+    norm of h with w as moe_norm gives it. residual and h: float16 or float32 [T][H], of one type."""
+    T, H = branch.shape
+    n = T * H
+    typ = _F16
+    for name, t in (("residual", residual), ("h", h)):
+        if t is not None:
+            if not isinstance(t, torch.Tensor):
+                raise TypeError(f"{name} must be a CUDA tensor")
+            if t.shape != (T, H):
+                raise ValueError(f"{name} must be [{T}][{H}], got {list(t.shape)}")
+            typ = t.dtype
+    if typ not in _LOGIT_TYPES:
+        raise TypeError(f"residual and h must be float32 or float16, got {typ}")
+    py, pq, ps = _norm_outputs(y, q, scales, n, T * _nb(H))
+    pg, kind = (None, MOE_GATE_NONE) if gate is None else _gate(gate, T, H)
+    status = _lib.moe_norm_residual(
+        cfg, _dev(branch, _F16, "branch"), None if residual is None else _dev(residual, typ, "residual"),
+        _LOGIT_TYPES[typ], T, H, None if post_w is None else _dev(post_w, _F16, "post_w", H),
+        None if post_b is None else _dev(post_b, _F16, "post_b", H), pg, kind, scale, residual_scale,
+        None if h is None else _dev(h, typ, "h"), None if w is None else _dev(w, _F16, "w", H),
+        None if b is None else _dev(b, _F16, "b", H), py, pq, ps, _stream(stream))
+    if status:
+        _check(status, "moe_norm_residual")
+
+
+# ---- FP16 product with its epilogue ----------------------------------------------
+_ACTS = {"none": MOE_ACT_NONE, "relu": MOE_ACT_RELU, "silu": MOE_ACT_SILU, "gelu": MOE_ACT_GELU,
+         "gelu_tanh": MOE_ACT_GELU_TANH, "sigmoid": MOE_ACT_SIGMOID}
+
+
+def _rows(t, name: str, shape: tuple, dtypes) -> tuple:
+    """(pointer, row stride) of a [rows][columns] tensor whose rows may be strided."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name} must be {' or '.join(str(d) for d in dtypes)}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+    ld, step = t.stride()
+    rows, cols = shape
+    if cols > 1 and step != 1:
+        raise ValueError(f"{name} must have contiguous rows")
+    return t.data_ptr(), ld if rows > 1 else cols
+
+
+def moe_linear_workspace_bytes(T: int, N: int, K: int) -> int:
+    return _lib.moe_linear_workspace_bytes(T, N, K)
+
+
+def moe_linear(x: torch.Tensor, w: torch.Tensor, bias: torch.Tensor | None, y: torch.Tensor, workspace: torch.Tensor,
+               act: str = "none", residual: torch.Tensor | None = None, stream=None) -> None:
+    """y [T][N] (float16 or float32) = act(x W^T + bias) + residual, x [T][K] and w [N][K] float16, bias
+    float32 [N], residual of y's type. Rows of x, y and residual may be strided."""
+    T, K = x.shape
+    N, Kw = w.shape
+    if Kw != K:
+        raise ValueError(f"x has {K} columns, w {Kw}")
+    px, ldx = _rows(x, "x", (T, K), (_F16,))
+    py, ldy = _rows(y, "y", (T, N), (_F16, _F32))
+    pr, ldr = (None, 0) if residual is None else _rows(residual, "residual", (T, N), (y.dtype,))
+    status = _lib.moe_linear(px, ldx, T, K, _dev(w, _F16, "w"), N, None if bias is None else _dev(bias, _F32, "bias", N),
+                             _ACTS[act], pr, ldr, py, _LOGIT_TYPES[y.dtype], ldy, _dev(workspace, _U8, "workspace"),
+                             workspace.numel(), _stream(stream))
+    if status:
+        _check(status, "moe_linear")
+
+
+# ---- balance loss ------------------------------------------------------------------
+def moe_balance_config(score: str = "softmax", coef: float = 1.0) -> moe_balance_cfg:
+    """A balance loss's settings (made once, passed to every call)."""
+    return moe_balance_cfg(_SCORES[score], float(coef))
+
+
+def moe_balance_workspace_bytes(T: int, E: int, S: int = 1) -> int:
+    return _lib.moe_balance_workspace_bytes(T, E, S)
+
+
+def _sequences(offsets) -> tuple:
+    """(pointer, S) of the sequences' offsets; None: one sequence of all tokens."""
+    if offsets is None:
+        return None, 1
+    return _dev(offsets, _I32, "offsets"), offsets.numel() - 1
+
+
+def moe_balance_loss(cfg: moe_balance_cfg, logits: torch.Tensor, ids: torch.Tensor, offsets: torch.Tensor | None,
+                     counts: torch.Tensor, tokens: torch.Tensor, mean: torch.Tensor | None,
+                     loss: torch.Tensor | None, workspace: torch.Tensor, stream=None) -> None:
+    """Per sequence: counts int32 [S][E] of the picks ids [T][k], tokens int32 [S] that count, mean float32
+    [S][E] of the router's probabilities; loss float32 [1] of all."""
+    ptr, kind, ld, T, E = _logits(logits)
+    k = ids.shape[1]
+    if ids.shape[0] != T:
+        raise ValueError(f"ids must be [{T}][k], got {list(ids.shape)}")
+    po, S = _sequences(offsets)
+    status = _lib.moe_balance_loss(
+        cfg, ptr, kind, ld, T, E, _dev(ids, _I32, "ids"), k, po, S, _dev(counts, _I32, "counts", S * E),
+        _dev(tokens, _I32, "tokens", S), None if mean is None else _dev(mean, _F32, "mean", S * E),
+        None if loss is None else _dev(loss, _F32, "loss", 1), _dev(workspace, _U8, "workspace"), workspace.numel(),
+        _stream(stream))
+    if status:
+        _check(status, "moe_balance_loss")
+
+
+def moe_balance_loss_backward(cfg: moe_balance_cfg, logits: torch.Tensor, k: int, offsets: torch.Tensor | None,
+                              counts: torch.Tensor, tokens: torch.Tensor, grad_loss: torch.Tensor | None,
+                              dlogits: torch.Tensor, accumulate: bool = False, stream=None) -> None:
+    """dlogits float32 [T][E] (rows may be strided) = the loss's gradient, or added to it; counts and tokens as
+    moe_balance_loss left them."""
+    ptr, kind, ld, T, E = _logits(logits)
+    po, S = _sequences(offsets)
+    pd, ldd = _rows(dlogits, "dlogits", (T, E), (_F32,))
+    status = _lib.moe_balance_loss_backward(
+        cfg, ptr, kind, ld, T, E, k, po, S, _dev(counts, _I32, "counts", S * E), _dev(tokens, _I32, "tokens", S),
+        None if grad_loss is None else _dev(grad_loss, _F32, "grad_loss", 1), pd, ldd, int(bool(accumulate)),
+        _stream(stream))
+    if status:
+        _check(status, "moe_balance_loss_backward")
 
 
 # ---- residency manager -----------------------------------------------------
