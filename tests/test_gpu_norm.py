@@ -39,8 +39,10 @@ def _half(v):
     return 2.0 ** -11 * np.abs(v) + 2.0 ** -25
 
 
-def _y_bound(h, e_h, y, r, w, kind):
+def _y_bound(h, e_h, y, r, w, kind, b=None):
     """Error of y in FP32, from h's."""
+    e_h = e_h + np.zeros(h.shape)
+    y = np.abs(y) + (0.0 if b is None else np.abs(b.astype(np.float64)))  # the product before the bias at most
     if kind == "layer":
         e_h = e_h + 2.0 ** -19 * np.abs(h).mean(1, keepdims=True)
     # r's error from h's: relative 2 rms(e_h) r at most.
@@ -74,7 +76,7 @@ def test_norm(T, H, f32, kind):
     x, off = _stream(rng, T, H, f32), 1.0 if H % 24 == 0 else 0.0
     w, b = _vec(rng, H, 1 - off), _vec(rng, H, 0.0) if kind == "layer" else None
     y, r = bo.norm(x, w, b, kind, 1e-5, off)
-    e = _y_bound(x.astype(np.float64), 0.0, y, r, w.astype(np.float64) + off, kind)
+    e = _y_bound(x.astype(np.float64), 0.0, y, r, w.astype(np.float64) + off, kind, b)
     cfg = moe.moe_norm_config(kind, 1e-5, off)
     out = torch.full((T, H), 7.0, dtype=torch.float16, device="cuda")
     fp8 = H % 16 == 0
@@ -106,9 +108,9 @@ def test_norm_residual(T, H, kind, f32, post, gate):
     e_h = 2.0 ** -21 * m
     if post:  # the post norm's error, through the gate
         a, ra = bo.norm(br, pw, pb, kind, 1e-6)
-        e_h = e_h + np.abs(sc * bo.gate_of(g, T, H)) * _y_bound(br.astype(np.float64), 0.0, a, ra, pw, kind)
+        e_h = e_h + np.abs(sc * bo.gate_of(g, T, H)) * _y_bound(br.astype(np.float64), 0.0, a, ra, pw, kind, pb)
     y, r = bo.norm(h, w, b, kind, 1e-6)
-    e_y = _y_bound(h, e_h, y, r, w, kind)
+    e_y = _y_bound(h, e_h, y, r, w, kind, b)
     dh = torch.full((T, H), 7.0, dtype=torch.float32 if f32 else torch.float16, device="cuda")
     dy = torch.full((T, H), 7.0, dtype=torch.float16, device="cuda")
     moe.moe_norm_residual(moe.moe_norm_config(kind, 1e-6), _cuda(br), _cuda(res), dh, _cuda(pw) if post else None,
