@@ -1,47 +1,9 @@
-// y = act(x W^T + bias) + residual, FP16 operands, FP32 sums.
-//
-// Plain form: a block of 16 x 16 threads per 16 tokens and 16 rows of W, both
-// operands through shared memory, one sum per thread.
-#include <algorithm>
-
+// moe_linear: argument checks and the choice between the weight stream
+// (linear_stream.cu, up to 16 tokens) and the tensor-memory kernels
+// (linear_gemm.cu).
 #include "common.h"
-#include "device.cuh"
 #include "kernels.h"
 #include "linear.cuh"
-
-namespace moe {
-namespace {
-
-__global__ void __launch_bounds__(256) linear_plain_kernel(const LinearArgs a) {
-  griddep_wait();
-  __shared__ float xs[16][17], ws[16][17];
-  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-  const int n0 = blockIdx.x * 16;
-  for (int m0 = blockIdx.y * 16; m0 < a.T; m0 += gridDim.y * 16) {
-    float s = 0.0f;
-    for (int k0 = 0; k0 < a.K; k0 += 16) {
-      const bool in = k0 + tx < a.K;
-      xs[ty][tx] = in && m0 + ty < a.T ? __half2float(a.x[(size_t)(m0 + ty) * a.ldx + k0 + tx]) : 0.0f;
-      ws[ty][tx] = in && n0 + ty < a.N ? __half2float(a.w[(size_t)(n0 + ty) * a.K + k0 + tx]) : 0.0f;
-      __syncthreads();
-#pragma unroll
-      for (int i = 0; i < 16; ++i) s = fmaf(xs[ty][i], ws[tx][i], s);
-      __syncthreads();
-    }
-    const int t = m0 + ty, n = n0 + tx;
-    if (t < a.T && n < a.N) {
-      if (a.bias) s += a.bias[n];
-      s = activate(a.act, s);
-      if (a.residual) s += a.y32 ? static_cast<const float*>(a.residual)[(size_t)t * a.ldr + n]
-                                 : __half2float(static_cast<const __half*>(a.residual)[(size_t)t * a.ldr + n]);
-      if (a.y32) static_cast<float*>(a.y)[(size_t)t * a.ldy + n] = s;
-      else static_cast<__half*>(a.y)[(size_t)t * a.ldy + n] = __float2half_rn(s);
-    }
-  }
-}
-
-}  // namespace
-}  // namespace moe
 
 extern "C" {
 
@@ -86,9 +48,10 @@ int moe_linear(const void* x, long long ldx, int T, int K, const void* w, int N,
   a.y32 = y_type == MOE_F32;
   a.ldy = ldy;
   a.flags = static_cast<int32_t*>(workspace);
-  const dim3 grid((unsigned)((N + 15) / 16), (unsigned)std::min((T + 15) / 16, 65535));
-  moe::linear_plain_kernel<<<grid, 256, 0, static_cast<cudaStream_t>(stream)>>>(a);
-  return moe::check_launch("linear");
+  const int esz = a.y32 ? 4 : 2;
+  a.vec = ldy * esz % 16 == 0 && (!residual || ldr * esz % 16 == 0);
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  return T <= moe::kLinearStreamTokens ? moe::linear_stream(a, st) : moe::linear_gemm(a, st);
 }
 
 }  // extern "C"

@@ -2,6 +2,7 @@
 #pragma once
 
 #include <cuda_fp16.h>
+#include <cuda_runtime.h>
 
 #include <cstdint>
 
@@ -22,18 +23,112 @@ struct LinearArgs {
   void* y;
   bool y32;
   long long ldy;
+  bool vec;  // rows of y and of the residual start on 16 bytes
   int32_t* flags;
 };
 
-// The activations in FP32. NaN gives NaN (relu: v > 0 ? v : 0 v).
-__device__ __forceinline__ float activate(int act, float v) {
+constexpr int kLinearStreamTokens = 16;  // up to here the weight stream, above the tensor-memory kernels
+int linear_stream(const LinearArgs& a, cudaStream_t st);
+int linear_gemm(const LinearArgs& a, cudaStream_t st);
+
+// The activations in FP32, of N values at a time. NaN gives NaN (relu: v > 0 ?
+// v : 0 v). silu and sigmoid divide by the special-function unit's reciprocal
+// (2 units in the last place; 0 where 1 + e^-v is beyond 2^126, v < -87).
+template <int N>
+__device__ __forceinline__ void activate(int act, float (&v)[N]) {
   switch (act) {
-    case MOE_ACT_RELU: return v > 0.0f ? v : 0.0f * v;
-    case MOE_ACT_SILU: return v / (1.0f + expf(-v));
-    case MOE_ACT_GELU: return 0.5f * v * (1.0f + erff(v * 0.70710678f));
-    case MOE_ACT_GELU_TANH: return 0.5f * v * (1.0f + tanhf(0.79788456f * (v + 0.044715f * v * v * v)));
-    case MOE_ACT_SIGMOID: return 1.0f / (1.0f + expf(-v));
-    default: return v;
+    case MOE_ACT_RELU:
+#pragma unroll
+      for (int i = 0; i < N; ++i) v[i] = v[i] > 0.0f ? v[i] : 0.0f * v[i];
+      break;
+    case MOE_ACT_SILU:
+#pragma unroll
+      for (int i = 0; i < N; ++i) v[i] = __fdividef(v[i], 1.0f + expf(-v[i]));
+      break;
+    case MOE_ACT_GELU:
+#pragma unroll
+      for (int i = 0; i < N; ++i) v[i] = 0.5f * v[i] * (1.0f + erff(v[i] * 0.70710678f));
+      break;
+    case MOE_ACT_GELU_TANH:  // (1 + tanh u) / 2 = 1 / (1 + e^-2u)
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        const float u = 0.79788456f * (v[i] + 0.044715f * v[i] * v[i] * v[i]);
+        v[i] = __fdividef(v[i], 1.0f + expf(-2.0f * u));
+      }
+      break;
+    case MOE_ACT_SIGMOID:
+#pragma unroll
+      for (int i = 0; i < N; ++i) v[i] = __fdividef(1.0f, 1.0f + expf(-v[i]));
+      break;
+    default: break;
+  }
+}
+
+// N values of row t from column n: bias, activation, residual, one rounding,
+// stored. N a multiple of 8 (of 4 for FP32) starting at such a column.
+template <int N>
+__device__ __forceinline__ void finish(const LinearArgs& a, int t, int n, float (&v)[N]) {
+  const int left = a.N - n;
+  if (left <= 0) return;
+  if (a.bias) {
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      if (i < left) v[i] += a.bias[n + i];
+  }
+  activate(a.act, v);
+  const size_t at = (size_t)t * (size_t)a.ldy + n, ra = (size_t)t * (size_t)a.ldr + n;
+  if (a.y32) {
+    const float* r = static_cast<const float*>(a.residual) + ra;
+    float* y = static_cast<float*>(a.y) + at;
+#pragma unroll
+    for (int i = 0; i < N; i += 4) {
+      if (a.vec && i + 4 <= left) {
+        if (a.residual) {
+          const float4 q = *reinterpret_cast<const float4*>(r + i);
+          v[i] += q.x; v[i + 1] += q.y; v[i + 2] += q.z; v[i + 3] += q.w;
+        }
+        *reinterpret_cast<float4*>(y + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+      } else {
+#pragma unroll
+        for (int e = i; e < i + 4; ++e)
+          if (e < left) y[e] = a.residual ? v[e] + r[e] : v[e];
+      }
+    }
+  } else {
+    const __half* r = static_cast<const __half*>(a.residual) + ra;
+    __half* y = static_cast<__half*>(a.y) + at;
+    if constexpr (N % 8 == 0) {
+#pragma unroll
+      for (int i = 0; i < N; i += 8) {
+        if (a.vec && i + 8 <= left) {
+          if (a.residual) {
+            const uint4 q = *reinterpret_cast<const uint4*>(r + i);
+            const uint32_t u[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const float2 p = __half22float2(u32_as_h2(u[e]));
+              v[i + 2 * e] += p.x;
+              v[i + 2 * e + 1] += p.y;
+            }
+          }
+          uint32_t h[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const half2 p = __floats2half2_rn(v[i + 2 * e], v[i + 2 * e + 1]);
+            h[e] = *reinterpret_cast<const uint32_t*>(&p);
+          }
+          *reinterpret_cast<uint4*>(y + i) = make_uint4(h[0], h[1], h[2], h[3]);
+        } else {
+#pragma unroll
+          for (int e = i; e < i + 8; ++e)
+            if (e < left) y[e] = __float2half_rn(a.residual ? v[e] + __half2float(r[e]) : v[e]);
+        }
+      }
+    } else {
+#pragma unroll
+      for (int e = 0; e < N; ++e)
+        if (e < left) y[e] = __float2half_rn(a.residual ? v[e] + __half2float(r[e]) : v[e]);
+    }
   }
 }
 

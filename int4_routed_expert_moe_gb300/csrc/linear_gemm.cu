@@ -1,0 +1,614 @@
+// y = act(x W^T + bias) + residual on the tensor cores, more than 16 tokens.
+//
+// Tokens are the MMA's M, rows of W its N. Both operands come by TMA in the
+// 128-byte-swizzled K-major layout, 64 columns (128 bytes) per pipeline step,
+// and a tile's sums stay in tensor memory until its last step; a second
+// accumulator takes the next tile meanwhile.
+//
+// linear_gemm_kernel: a block and 128 tokens by NT columns, the K steps of a
+// tile split over a cluster where the tiles are few. linear_pair_kernel: two
+// blocks and 256 x 256. linear_plan picks.
+#include <algorithm>
+#include <mutex>
+
+#include "common.h"
+#include "device.cuh"
+#include "kernels.h"
+#include "linear.cuh"
+#include "linear_plan.h"
+#include "tc.cuh"
+
+namespace moe {
+namespace {
+
+constexpr int BM = kLinearTokens;
+constexpr int BK = 64;
+constexpr uint32_t kABytes = BM * BK * 2;
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// 16 bytes of another block's shared memory, at this block's address `a`.
+__device__ __forceinline__ float4 ld_cluster(uint32_t a, uint32_t rank) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(tc::map_rank(a, rank))
+               : "memory");
+  return v;
+}
+
+struct TileArgs {
+  int nb;            // steps along K
+  int mt, tiles;     // token tiles, tiles in all
+  int splits;        // blocks of a cluster share one tile's steps
+  uint32_t a_bytes;  // bytes of the token tile's box
+  bool y_tma, r_tma; // pair kernel: rows of y / the residual that TMA can address
+};
+
+// Geometry by tile width. Warp 0 issues TMA, warp 1 owns tensor memory and
+// issues the MMAs, the others run the epilogue.
+template <int NT>
+struct Geo {
+  static constexpr int epi = NT >= 128 ? 8 : 4;
+  static constexpr int cols = NT / (epi / 4);  // per epilogue warp
+  static constexpr int threads = 64 + 32 * epi;
+  static constexpr uint32_t stage = kABytes + (uint32_t)NT * BK * 2;
+  static constexpr int stages = NT == 256 ? 4 : NT == 128 ? 6 : 8;
+  static constexpr uint32_t tmem_cols = 2 * NT;
+  static constexpr uint32_t off_ctrl = (uint32_t)stages * stage;
+  static constexpr size_t smem = (size_t)off_ctrl + 1024 + 1024;  // control block, alignment
+  static constexpr int red_pitch = NT + 4;                        // floats per row of a partial tile
+  static_assert((size_t)BM * red_pitch * 4 <= off_ctrl, "partial tile fits the stage area");
+};
+
+struct Bars {
+  uint64_t *full, *empty, *acc_full, *acc_empty, *res;
+  uint32_t* tmem_slot;
+  int* abort;
+};
+__device__ __forceinline__ Bars bars_at(uint8_t* p, int stages) {
+  Bars b;
+  uint64_t* q = reinterpret_cast<uint64_t*>(p);
+  b.full = q; q += stages;
+  b.empty = q; q += stages;
+  b.acc_full = q; q += 2;
+  b.acc_empty = q; q += 2;
+  b.res = q; q += 8;
+  b.tmem_slot = reinterpret_cast<uint32_t*>(q);
+  b.abort = reinterpret_cast<int*>(b.tmem_slot + 1);
+  return b;
+}
+__device__ __forceinline__ bool is_aborted(const Bars& b) { return *reinterpret_cast<volatile int*>(b.abort) != 0; }
+__device__ __forceinline__ void set_aborted(const Bars& b, int32_t* flags) {
+  atomicOr(flags, 4);
+  *reinterpret_cast<volatile int*>(b.abort) = 1;
+}
+// Bounded wait by every lane of a warp, one verdict; it ends early once another
+// role of the block has given up.
+__device__ __forceinline__ bool wait(const Bars& b, uint64_t* bar, uint32_t parity, int32_t* flags) {
+  bool ok = tc::bar_try_wait(bar, parity);
+  if (!ok) {
+    const uint64_t t0 = tc::global_ns();
+    while (!(ok = tc::bar_try_wait(bar, parity))) {
+      if (is_aborted(b)) break;
+      if (tc::global_ns() - t0 > tc::kWaitNs) {
+        set_aborted(b, flags);
+        break;
+      }
+    }
+  }
+  return __all_sync(0xffffffffu, ok);
+}
+
+template <int NT>
+__global__ void __launch_bounds__(Geo<NT>::threads, 1)
+    linear_gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_w,
+                       const LinearArgs a, const TileArgs ta) {
+  using G = Geo<NT>;
+  extern __shared__ uint8_t smraw[];
+  uint8_t* sm = tc::align1024(smraw);
+  const Bars b = bars_at(sm + G::off_ctrl, G::stages);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    tc::tma_prefetch_desc(&map_x);
+    tc::tma_prefetch_desc(&map_w);
+    for (int s = 0; s < G::stages; ++s) {
+      tc::bar_init(&b.full[s], 1);
+      tc::bar_init(&b.empty[s], 1);
+    }
+    for (int s = 0; s < 2; ++s) {
+      tc::bar_init(&b.acc_full[s], 1);
+      tc::bar_init(&b.acc_empty[s], G::epi);
+    }
+    *b.abort = 0;
+    tc::bar_init_fence();
+  }
+  if (warp == 1) tc::tmem_alloc(b.tmem_slot, G::tmem_cols);
+  tc::tc_fence_before();
+  __syncthreads();
+  tc::tc_fence_after();
+  const uint32_t tmem = *b.tmem_slot;
+  griddep_wait();
+  griddep_launch_dependents();
+
+  const int S = ta.splits;
+  const int rank = S > 1 ? (int)cluster_rank() : 0;
+  const int kb0 = ta.nb * rank / S, kb1 = ta.nb * (rank + 1) / S;
+  const int first = (int)blockIdx.x / S, stride = (int)gridDim.x / S;
+
+  if (warp == 0) {
+    int g = 0;
+    bool ok = true;
+    for (int tile = first; tile < ta.tiles && ok; tile += stride) {
+      const int m0 = (tile % ta.mt) * BM, n0 = (tile / ta.mt) * NT;
+      for (int kb = kb0; kb < kb1; ++kb, ++g) {
+        const int s = g % G::stages;
+        if (g >= G::stages && !(ok = wait(b, &b.empty[s], ((g / G::stages) - 1) & 1, a.flags))) break;
+        if (tc::elect_one()) {
+          uint8_t* st = sm + (size_t)s * G::stage;
+          tc::bar_expect_tx(&b.full[s], ta.a_bytes + NT * BK * 2);
+          tc::tma_load_2d(st, &map_x, kb * BK, m0, &b.full[s]);
+          tc::tma_load_2d(st + kABytes, &map_w, kb * BK, n0, &b.full[s]);
+        }
+        __syncwarp();
+      }
+    }
+    if (!ok && lane == 0)  // loads still in flight land before the block leaves (bounded)
+      for (int i = g > G::stages ? g - G::stages : 0; i < g; ++i)
+        tc::bar_wait(&b.full[i % G::stages], (i / G::stages) & 1);
+  } else if (warp == 1) {
+    constexpr uint32_t idesc = tc::idesc_f16(BM, NT);
+    int g = 0, u = 0;
+    bool ok = true;
+    for (int tile = first; tile < ta.tiles && ok; tile += stride, ++u) {
+      if (u >= 2 && !wait(b, &b.acc_empty[u & 1], ((u >> 1) - 1) & 1, a.flags)) break;
+      for (int kb = kb0; kb < kb1; ++kb, ++g) {
+        const int s = g % G::stages;
+        if (!(ok = wait(b, &b.full[s], (g / G::stages) & 1, a.flags))) break;
+        tc::tc_fence_after();
+        const uint32_t base = tc::smem_addr(sm + (size_t)s * G::stage);
+        const uint64_t ad = tc::sw128_desc(base), bd = tc::sw128_desc(base + kABytes);
+        if (tc::elect_one()) {
+#pragma unroll
+          for (int kk = 0; kk < BK / 16; ++kk)
+            tc::mma_f16(tmem + (uint32_t)((u & 1) * NT), ad + 2 * kk, bd + 2 * kk, idesc, kb > kb0 || kk > 0);
+          tc::mma_commit(&b.empty[s]);
+          if (kb == kb1 - 1) tc::mma_commit(&b.acc_full[u & 1]);
+        }
+        __syncwarp();
+      }
+    }
+  } else {
+    const int q4 = warp & 3, c0 = G::cols * ((warp - 2) >> 2);
+    const uint32_t tl = tmem + ((uint32_t)(32 * q4) << 16) + (uint32_t)c0;
+    int u = 0;
+    for (int tile = first; tile < ta.tiles; tile += stride, ++u) {
+      const int m0 = (tile % ta.mt) * BM, n0 = (tile / ta.mt) * NT;
+      const int r = 32 * q4 + lane, row = m0 + r;
+      if (!wait(b, &b.acc_full[u & 1], (u >> 1) & 1, a.flags)) break;
+      tc::tc_fence_after();
+      if (S > 1) {  // partial tile to shared memory (every stage has been consumed)
+        float* red = reinterpret_cast<float*>(sm) + (size_t)r * G::red_pitch + c0;
+#pragma unroll 1
+        for (int c = 0; c < G::cols; c += 32) {
+          uint32_t d[32];
+          __syncwarp();
+          tc::tmem_ld32(tl + (uint32_t)c, d);
+          tc::tmem_ld32_wait(d);
+          if (row < a.T) {
+#pragma unroll
+            for (int i = 0; i < 32; i += 4) *reinterpret_cast<uint4*>(red + c + i) = make_uint4(d[i], d[i + 1], d[i + 2], d[i + 3]);
+          }
+        }
+        break;
+      }
+#pragma unroll 1
+      for (int c = 0; c < G::cols; c += 32) {
+        uint32_t d[32];
+        __syncwarp();
+        tc::tmem_ld32(tl + (uint32_t)((u & 1) * NT + c), d);
+        tc::tmem_ld32_wait(d);
+        if (c + 32 == G::cols) {
+          tc::tc_fence_before();
+          __syncwarp();
+          if (lane == 0) tc::bar_arrive(&b.acc_empty[u & 1]);
+        }
+        if (row < a.T) {
+          float v[32];
+#pragma unroll
+          for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(d[i]);
+          finish(a, row, n0 + c0 + c, v);
+        }
+      }
+    }
+  }
+  if (S > 1) {
+    // The cluster's partial tiles, added in rank order (the same order every
+    // time), each block finishing its share of the tile.
+    __syncwarp();
+    cluster_sync();
+    const int m0 = (first % ta.mt) * BM, n0 = (first / ta.mt) * NT;
+    const int rows = min(BM, a.T - m0);
+    const uint32_t red = tc::smem_addr(sm);
+    constexpr int kQ = NT / 8;  // pieces of 8 columns per row
+    for (int i = rank * G::threads + (int)threadIdx.x; i < rows * kQ; i += S * G::threads) {
+      const int r = i / kQ, c = (i % kQ) * 8;
+      if (n0 + c >= a.N) continue;
+      float v[8] = {};
+      for (int p = 0; p < S; ++p) {
+        const uint32_t at = red + (uint32_t)(r * G::red_pitch + c) * 4;
+        const float4 f = ld_cluster(at, (uint32_t)p), h = ld_cluster(at + 16, (uint32_t)p);
+        v[0] += f.x; v[1] += f.y; v[2] += f.z; v[3] += f.w;
+        v[4] += h.x; v[5] += h.y; v[6] += h.z; v[7] += h.w;
+      }
+      finish(a, m0 + r, n0 + c, v);
+    }
+    __syncwarp();
+    cluster_sync();  // nobody leaves while its partial tile is read
+  }
+  tc::gemm_teardown(tmem, G::tmem_cols);
+}
+
+// ---- SM pairs: 256 tokens by 256 rows of W ----------------------------------
+// Two blocks of a cluster run one tile with cta_group::2 MMAs: each holds its
+// 128 tokens (A) and half of the weight rows (B), and each accumulates its
+// tokens against all 256 rows. Warps: 0 TMA, 1 tensor memory and (in the
+// leading block) MMA issue, 4-11 epilogue (a lane quarter, 128 columns each).
+struct Pair {
+  static constexpr int epi = 8, threads = 384;
+  static constexpr int stages = 5;
+  static constexpr uint32_t stage = kABytes + 128 * BK * 2;
+  static constexpr uint32_t off_out = stages * stage;  // [epi][2][32 rows][128 bytes]
+  static constexpr uint32_t off_ctrl = off_out + epi * 8192;
+  static constexpr size_t smem = (size_t)off_ctrl + 1024 + 1024;
+  static_assert(smem <= 232448, "shared memory of a block");
+};
+
+__device__ __forceinline__ void mma_f16_pair(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                             bool accumulate) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n}\n"
+      ::"r"(d_tmem), "l"(a_desc), "l"(b_desc), "r"(idesc), "r"((uint32_t)accumulate)
+      : "memory");
+}
+
+// An epilogue warp's 32 rows by 32 columns, chunk c of its staging area: rows
+// of 128 bytes in the 128-byte swizzle, 64 FP16 columns (two chunks) or 32
+// FP32 columns (one).
+template <typename Y>
+__device__ __forceinline__ uint8_t* piece(uint8_t* out, int c, int lane, int i) {
+  if (sizeof(Y) == 2) return out + (c >> 1) * 4096 + tc::sw128_offset(lane, 4 * (c & 1) + i);
+  return out + c * 4096 + tc::sw128_offset(lane, i);
+}
+
+template <typename Y>
+__global__ void __launch_bounds__(Pair::threads, 1)
+    linear_pair_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_w,
+                       const __grid_constant__ CUtensorMap map_y, const __grid_constant__ CUtensorMap map_r,
+                       const LinearArgs a, const TileArgs ta) {
+  using G = Pair;
+  extern __shared__ uint8_t smraw[];
+  uint8_t* sm = tc::align1024(smraw);
+  const Bars b = bars_at(sm + G::off_ctrl, G::stages);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = (int)cluster_rank();
+  if (threadIdx.x == 0) {
+    tc::tma_prefetch_desc(&map_x);
+    tc::tma_prefetch_desc(&map_w);
+    tc::tma_prefetch_desc(&map_y);
+    tc::tma_prefetch_desc(&map_r);
+    for (int s = 0; s < G::stages; ++s) {
+      tc::bar_init(&b.full[s], 1);
+      tc::bar_init(&b.empty[s], 1);
+    }
+    for (int s = 0; s < 2; ++s) {
+      tc::bar_init(&b.acc_full[s], 1);
+      tc::bar_init(&b.acc_empty[s], 2 * G::epi);
+    }
+    for (int s = 0; s < G::epi; ++s) tc::bar_init(&b.res[s], 1);
+    *b.abort = 0;
+    tc::bar_init_fence();
+  }
+  if (warp == 1) tc::tmem_alloc2(b.tmem_slot, 512);
+  tc::tc_fence_before();
+  __syncthreads();
+  cluster_sync();
+  tc::tc_fence_after();
+  const uint32_t tmem = *b.tmem_slot;
+  griddep_wait();
+  griddep_launch_dependents();
+
+  const int nb = ta.nb;
+  const int first = (int)blockIdx.x / 2, stride = (int)gridDim.x / 2;
+  if (warp == 0) {
+    // Both blocks' loads complete on the leading block's barrier.
+    int g = 0;
+    bool ok = true;
+    for (int tile = first; tile < ta.tiles && ok; tile += stride) {
+      const int m0 = (tile % ta.mt) * 256 + rank * BM, n0 = (tile / ta.mt) * 256 + rank * 128;
+      for (int kb = 0; kb < nb; ++kb, ++g) {
+        const int s = g % G::stages;
+        if (g >= G::stages && !(ok = wait(b, &b.empty[s], ((g / G::stages) - 1) & 1, a.flags))) break;
+        if (tc::elect_one()) {
+          uint8_t* st = sm + (size_t)s * G::stage;
+          const uint32_t full = tc::map_rank(tc::smem_addr(&b.full[s]), 0);
+          if (rank == 0) tc::bar_expect_tx(&b.full[s], 2 * G::stage);
+          tc::tma_load_2d_pair(st, &map_x, kb * BK, m0, full);
+          tc::tma_load_2d_pair(st + kABytes, &map_w, kb * BK, n0, full);
+        }
+        __syncwarp();
+      }
+    }
+    // After a wait that ran out, the loads still in flight land before the
+    // block leaves: 2 ms, since no barrier of this block counts them.
+    if (!ok) {
+      const uint64_t t0 = tc::global_ns();
+      for (int i = 0; i < 1000000 && tc::global_ns() - t0 < 2000000ull; ++i) {
+      }
+    }
+  } else if (warp == 1) {
+    if (rank == 0) {
+      constexpr uint32_t idesc = tc::idesc_f16(256, 256);
+      int g = 0, u = 0;
+      bool ok = true;
+      for (int tile = first; tile < ta.tiles && ok; tile += stride, ++u) {
+        if (u >= 2 && !wait(b, &b.acc_empty[u & 1], ((u >> 1) - 1) & 1, a.flags)) break;
+        for (int kb = 0; kb < nb; ++kb, ++g) {
+          const int s = g % G::stages;
+          if (!(ok = wait(b, &b.full[s], (g / G::stages) & 1, a.flags))) break;
+          tc::tc_fence_after();
+          const uint32_t base = tc::smem_addr(sm + (size_t)s * G::stage);
+          const uint64_t ad = tc::sw128_desc(base), bd = tc::sw128_desc(base + kABytes);
+          if (tc::elect_one()) {
+#pragma unroll
+            for (int kk = 0; kk < BK / 16; ++kk)
+              mma_f16_pair(tmem + (uint32_t)((u & 1) * 256), ad + 2 * kk, bd + 2 * kk, idesc, kb > 0 || kk > 0);
+            tc::mma_commit_pair(&b.empty[s]);
+            if (kb == nb - 1) tc::mma_commit_pair(&b.acc_full[u & 1]);
+          }
+          __syncwarp();
+        }
+      }
+    }
+  } else if (warp >= 4) {
+    constexpr int kBox = 128 / (int)sizeof(Y);                  // columns per staged row
+    constexpr int kPass = 2 * kBox, kChunks = kPass / 32;       // columns and chunks per staging pass
+    const int q4 = warp & 3, e8 = warp - 4, j2 = e8 >> 2;
+    const uint32_t tl = tmem + ((uint32_t)(32 * q4) << 16) + (uint32_t)(128 * j2);
+    const uint32_t acc_empty0 = tc::map_rank(tc::smem_addr(&b.acc_empty[0]), 0);
+    uint8_t* out = sm + G::off_out + e8 * 8192;
+    int u = 0, loads = 0;
+    for (int tile = first; tile < ta.tiles; tile += stride, ++u) {
+      const int y0 = (tile % ta.mt) * 256 + rank * BM + 32 * q4, row = y0 + lane;
+      const int x0 = (tile / ta.mt) * 256 + 128 * j2;
+      bool got = false;
+#pragma unroll 1
+      for (int p = 0; p < 128 / kPass; ++p) {
+        const int xp = x0 + p * kPass;
+        // The stores of the last pass have read the staging area; the
+        // residual's tile comes into it, and the results take its place.
+        if (lane < 2) tc::tma_store_wait_read();
+        __syncwarp();
+        const bool some = y0 < a.T && xp < a.N, load = some && ta.r_tma;
+        if (load) {
+          if (lane == 0) {
+            const int boxes = xp + kBox < a.N ? 2 : 1;
+            tc::fence_async_smem();
+            tc::bar_expect_tx(&b.res[e8], 4096u * boxes);
+            for (int j = 0; j < boxes; ++j) tc::tma_load_2d(out + 4096 * j, &map_r, xp + kBox * j, y0, &b.res[e8]);
+          }
+          __syncwarp();
+        }
+        if (!got) got = wait(b, &b.acc_full[u & 1], (u >> 1) & 1, a.flags);
+        tc::tc_fence_after();
+        if (load && !wait(b, &b.res[e8], loads++ & 1, a.flags)) got = false;
+        const bool last = p == 128 / kPass - 1;
+#pragma unroll 1
+        for (int c = 0; c < kChunks; ++c) {
+          uint32_t d[32];
+          __syncwarp();
+          tc::tmem_ld32(tl + (uint32_t)((u & 1) * 256 + p * kPass + 32 * c), d);
+          tc::tmem_ld32_wait(d);
+          if (last && c == kChunks - 1) {
+            tc::tc_fence_before();
+            __syncwarp();
+            if (lane == 0) tc::bar_arrive_cluster(acc_empty0 + 8 * (u & 1));
+          }
+          const int n = xp + 32 * c;
+          float v[32];
+#pragma unroll
+          for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(d[i]);
+          if (a.bias) {
+            const float bias = n + lane < a.N ? a.bias[n + lane] : 0.0f;
+#pragma unroll
+            for (int i = 0; i < 32; ++i) v[i] += __shfl_sync(0xffffffffu, bias, i);
+          }
+          activate(a.act, v);
+          if (a.residual && !ta.r_tma && row < a.T) {
+            const Y* r = static_cast<const Y*>(a.residual) + (size_t)row * (size_t)a.ldr + n;
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              if (n + i < a.N) v[i] += (float)r[i];
+          }
+          if (sizeof(Y) == 2) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              uint4* s = reinterpret_cast<uint4*>(piece<Y>(out, c, lane, i));
+              if (load) {
+                const uint4 q = *s;
+                const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                  const float2 f = __half22float2(u32_as_h2(w[e]));
+                  v[8 * i + 2 * e] += f.x;
+                  v[8 * i + 2 * e + 1] += f.y;
+                }
+              }
+              uint32_t h[4];
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const half2 f = __floats2half2_rn(v[8 * i + 2 * e], v[8 * i + 2 * e + 1]);
+                h[e] = *reinterpret_cast<const uint32_t*>(&f);
+              }
+              *s = make_uint4(h[0], h[1], h[2], h[3]);
+            }
+          } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              float4* s = reinterpret_cast<float4*>(piece<Y>(out, c, lane, i));
+              float4 f = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+              if (load) {
+                const float4 q = *s;
+                f.x += q.x; f.y += q.y; f.z += q.z; f.w += q.w;
+              }
+              *s = f;
+            }
+          }
+        }
+        if (!got || is_aborted(b)) continue;
+        if (ta.y_tma) {
+          tc::fence_async_smem();
+          __syncwarp();
+          // A lane per store: one lane issuing both takes twice as long.
+          if (lane < 2 && some && xp + kBox * lane < a.N) tc::tma_store_2d(&map_y, xp + kBox * lane, y0, out + 4096 * lane);
+        } else {
+          // Rows that TMA cannot address (pitch no multiple of 16 bytes): one element per lane.
+          __syncwarp();
+          for (int rr = 0; rr < min(32, a.T - y0); ++rr)
+#pragma unroll
+            for (int j = 0; j < kPass / 32; ++j) {
+              const int x = 32 * j + lane, box = x / kBox, col = (x % kBox) * (int)sizeof(Y);
+              const Y v = *reinterpret_cast<const Y*>(out + 4096 * box + tc::sw128_offset(rr, col >> 4) + (col & 15));
+              if (xp + x < a.N) static_cast<Y*>(a.y)[(size_t)(y0 + rr) * (size_t)a.ldy + xp + x] = v;
+            }
+          __syncwarp();
+        }
+      }
+    }
+    if (lane < 2) tc::tma_store_wait_read();  // the grid's end waits for the writes
+  }
+  tc::tc_fence_before();
+  __syncwarp();
+  cluster_sync();  // neither block leaves while the other's MMAs, loads or arrivals can reach it
+  tc::tc_fence_after();
+  if (warp == 1) tc::tmem_dealloc2(tmem, 512);
+}
+
+// A row-major matrix [rows][cols], rows ld elements apart, in boxes of 128-byte rows.
+int row_map(CUtensorMap* m, const void* base, bool f32, int cols, int rows, long long ld, int box_rows) {
+  const int esz = f32 ? 4 : 2;
+  const uint64_t dims[2] = {(uint64_t)cols, (uint64_t)rows};
+  const uint64_t str[1] = {(uint64_t)ld * esz};
+  const uint32_t box[2] = {128u / esz, (uint32_t)box_rows};
+  return encode_tensor_map(m, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, base, dims, str,
+                           box, CU_TENSOR_MAP_SWIZZLE_128B);
+}
+
+struct Launch {
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[2];
+  Launch(unsigned grid, int threads, size_t smem, int cluster, cudaStream_t st) {
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = (unsigned)cluster;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
+  }
+};
+
+template <int NT>
+int launch_gemm(const LinearArgs& a, int splits, int sms, int dev, cudaStream_t st) {
+  using G = Geo<NT>;
+  static std::mutex mu;
+  static bool set[kMaxDevices] = {};
+  {
+    std::lock_guard<std::mutex> lock(mu);
+    if (!set[dev]) {
+      MOE_CUDA_TRY(cudaFuncSetAttribute(linear_gemm_kernel<NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)G::smem));
+      set[dev] = true;
+    }
+  }
+  int box = 8;  // rows of the token box: the batch's, rounded up
+  while (box < BM && box < a.T) box *= 2;
+  TileArgs t = {};
+  t.nb = (a.K + BK - 1) / BK;
+  t.mt = (a.T + BM - 1) / BM;
+  t.tiles = t.mt * ((a.N + NT - 1) / NT);
+  t.splits = splits;
+  t.a_bytes = (uint32_t)box * BK * 2;
+  CUtensorMap mx, mw;
+  int rc;
+  if ((rc = row_map(&mx, a.x, false, a.K, a.T, a.ldx, box)) != MOE_OK) return rc;
+  if ((rc = row_map(&mw, a.w, false, a.K, a.N, a.K, NT)) != MOE_OK) return rc;
+  const Launch l((unsigned)(splits > 1 ? t.tiles * splits : std::min(t.tiles, sms)), G::threads, G::smem, splits, st);
+  const cudaError_t e = cudaLaunchKernelEx(&l.cfg, linear_gemm_kernel<NT>, mx, mw, a, t);
+  if (e != cudaSuccess) return fail(MOE_ERR_CUDA, "moe_linear launch: %s", cudaGetErrorString(e));
+  return MOE_OK;
+}
+
+template <typename Y>
+int launch_pair(const LinearArgs& a, int sms, int dev, cudaStream_t st) {
+  static std::mutex mu;
+  static bool set[kMaxDevices] = {};
+  {
+    std::lock_guard<std::mutex> lock(mu);
+    if (!set[dev]) {
+      MOE_CUDA_TRY(cudaFuncSetAttribute(linear_pair_kernel<Y>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                        (int)Pair::smem));
+      set[dev] = true;
+    }
+  }
+  constexpr bool f32 = sizeof(Y) == 4;
+  TileArgs t = {};
+  t.nb = (a.K + BK - 1) / BK;
+  t.mt = (a.T + 255) / 256;
+  t.tiles = t.mt * ((a.N + 255) / 256);
+  t.splits = 1;
+  t.y_tma = a.ldy * (long long)sizeof(Y) % 16 == 0;
+  t.r_tma = a.residual && a.ldr * (long long)sizeof(Y) % 16 == 0;
+  CUtensorMap mx, mw, my, mr;
+  int rc;
+  if ((rc = row_map(&mx, a.x, false, a.K, a.T, a.ldx, BM)) != MOE_OK) return rc;
+  if ((rc = row_map(&mw, a.w, false, a.K, a.N, a.K, 128)) != MOE_OK) return rc;
+  my = mr = mx;
+  if (t.y_tma && (rc = row_map(&my, a.y, f32, a.N, a.T, a.ldy, 32)) != MOE_OK) return rc;
+  if (t.r_tma && (rc = row_map(&mr, a.residual, f32, a.N, a.T, a.ldr, 32)) != MOE_OK) return rc;
+  const Launch l((unsigned)(2 * std::min(t.tiles, sms / 2)), Pair::threads, Pair::smem, 2, st);
+  const cudaError_t e = cudaLaunchKernelEx(&l.cfg, linear_pair_kernel<Y>, mx, mw, my, mr, a, t);
+  if (e != cudaSuccess) return fail(MOE_ERR_CUDA, "moe_linear launch: %s", cudaGetErrorString(e));
+  return MOE_OK;
+}
+
+int launch_plan(const LinearArgs& a, const LinearPlan& p, int sms, int dev, cudaStream_t st) {
+  switch (p.nt) {
+    case 0: return a.y32 ? launch_pair<float>(a, sms, dev, st) : launch_pair<__half>(a, sms, dev, st);
+    case 256: return launch_gemm<256>(a, p.splits, sms, dev, st);
+    case 128: return launch_gemm<128>(a, p.splits, sms, dev, st);
+    case 64: return launch_gemm<64>(a, p.splits, sms, dev, st);
+    default: return launch_gemm<32>(a, p.splits, sms, dev, st);
+  }
+}
+
+}  // namespace
+
+int linear_gemm(const LinearArgs& a, cudaStream_t st) {
+  int dev = 0, sms = 0;
+  const int rc = current_device_sms(&dev, &sms);
+  if (rc != MOE_OK) return rc;
+  return launch_plan(a, linear_plan(a.T, a.N, (a.K + BK - 1) / BK, sms), sms, dev, st);
+}
+
+}  // namespace moe
