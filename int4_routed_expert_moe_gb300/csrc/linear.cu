@@ -41,6 +41,7 @@ int moe_linear(const void* x, long long ldx, int T, int K, const void* w, int N,
   a.ldx = ldx;
   a.w = static_cast<const __half*>(w);
   a.bias = bias;
+  a.bias_vec = reinterpret_cast<uintptr_t>(bias) % 16 == 0;
   a.act = act;
   a.residual = residual;
   a.ldr = ldr;

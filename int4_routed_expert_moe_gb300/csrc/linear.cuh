@@ -17,6 +17,7 @@ struct LinearArgs {
   long long ldx;
   const __half* w;
   const float* bias;
+  bool bias_vec;  // on 16 bytes
   int act;
   const void* residual;  // of y's type
   long long ldr;
@@ -31,10 +32,21 @@ constexpr int kLinearStreamTokens = 16;  // up to here the weight stream, above 
 int linear_stream(const LinearArgs& a, cudaStream_t st);
 int linear_gemm(const LinearArgs& a, cudaStream_t st);
 
+// 1 / (1 + e^-v). FAST, for results that FP16 rounds: the special-function
+// unit's 2^x and 1/x (relative errors about 2^-22, and the exponent's rounding,
+// 2^-24 |v|); else expf and a division to 2 units in the last place. 0 where
+// 1 + e^-v is beyond 2^126, v < -87.
+template <bool FAST>
+__device__ __forceinline__ float sigmoid_times(float v, float m) {
+  if (!FAST) return __fdividef(m, 1.0f + expf(-v));
+  float e, r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(v * -1.4426950408889634f));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + e));
+  return m * r;
+}
 // The activations in FP32, of N values at a time. NaN gives NaN (relu: v > 0 ?
-// v : 0 v). silu and sigmoid divide by the special-function unit's reciprocal
-// (2 units in the last place; 0 where 1 + e^-v is beyond 2^126, v < -87).
-template <int N>
+// v : 0 v).
+template <bool FAST, int N>
 __device__ __forceinline__ void activate(int act, float (&v)[N]) {
   switch (act) {
     case MOE_ACT_RELU:
@@ -43,7 +55,7 @@ __device__ __forceinline__ void activate(int act, float (&v)[N]) {
       break;
     case MOE_ACT_SILU:
 #pragma unroll
-      for (int i = 0; i < N; ++i) v[i] = __fdividef(v[i], 1.0f + expf(-v[i]));
+      for (int i = 0; i < N; ++i) v[i] = sigmoid_times<FAST>(v[i], v[i]);
       break;
     case MOE_ACT_GELU:
 #pragma unroll
@@ -53,14 +65,32 @@ __device__ __forceinline__ void activate(int act, float (&v)[N]) {
 #pragma unroll
       for (int i = 0; i < N; ++i) {
         const float u = 0.79788456f * (v[i] + 0.044715f * v[i] * v[i] * v[i]);
-        v[i] = __fdividef(v[i], 1.0f + expf(-2.0f * u));
+        v[i] = sigmoid_times<FAST>(2.0f * u, v[i]);
       }
       break;
     case MOE_ACT_SIGMOID:
 #pragma unroll
-      for (int i = 0; i < N; ++i) v[i] = __fdividef(1.0f, 1.0f + expf(-v[i]));
+      for (int i = 0; i < N; ++i) v[i] = sigmoid_times<FAST>(v[i], 1.0f);
       break;
     default: break;
+  }
+}
+
+// The bias of columns n .. n + N - 1; every lane of a warp reads the same ones,
+// 16 bytes at a time: a load or a shuffle per column takes shared-memory
+// bandwidth from the MMAs' operands.
+template <int N>
+__device__ __forceinline__ void add_bias(const LinearArgs& a, int n, float (&v)[N]) {
+#pragma unroll
+  for (int i = 0; i < N; i += 4) {
+    if (a.bias_vec && n + i + 4 <= a.N) {
+      const float4 q = __ldg(reinterpret_cast<const float4*>(a.bias + n + i));
+      v[i] += q.x; v[i + 1] += q.y; v[i + 2] += q.z; v[i + 3] += q.w;
+    } else {
+#pragma unroll
+      for (int e = i; e < i + 4; ++e)
+        if (n + e < a.N) v[e] += __ldg(a.bias + n + e);
+    }
   }
 }
 
@@ -70,16 +100,12 @@ template <int N>
 __device__ __forceinline__ void finish(const LinearArgs& a, int t, int n, float (&v)[N]) {
   const int left = a.N - n;
   if (left <= 0) return;
-  if (a.bias) {
-#pragma unroll
-    for (int i = 0; i < N; ++i)
-      if (i < left) v[i] += a.bias[n + i];
-  }
-  activate(a.act, v);
+  if (a.bias) add_bias(a, n, v);
   const size_t at = (size_t)t * (size_t)a.ldy + n, ra = (size_t)t * (size_t)a.ldr + n;
   if (a.y32) {
     const float* r = static_cast<const float*>(a.residual) + ra;
     float* y = static_cast<float*>(a.y) + at;
+    activate<false>(a.act, v);
 #pragma unroll
     for (int i = 0; i < N; i += 4) {
       if (a.vec && i + 4 <= left) {
@@ -97,6 +123,7 @@ __device__ __forceinline__ void finish(const LinearArgs& a, int t, int n, float 
   } else {
     const __half* r = static_cast<const __half*>(a.residual) + ra;
     __half* y = static_cast<__half*>(a.y) + at;
+    activate<true>(a.act, v);
     if constexpr (N % 8 == 0) {
 #pragma unroll
       for (int i = 0; i < N; i += 8) {

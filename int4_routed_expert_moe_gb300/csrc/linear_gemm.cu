@@ -24,6 +24,11 @@ namespace {
 constexpr int BM = kLinearTokens;
 constexpr int BK = 64;
 constexpr uint32_t kABytes = BM * BK * 2;
+// FP32 results: an accumulator takes 8 steps (512 of K). The tensor cores cut
+// the running sum off every 16 terms, and the errors add up along K: a router's
+// logits over K = 2048 are 2.3e-6 off when one accumulator takes all of K.
+// Below the rounding of an FP16 result (2.1e-4) that does not show.
+constexpr int kSegment = 8;
 
 __device__ __forceinline__ uint32_t cluster_rank() {
   uint32_t r;
@@ -45,7 +50,9 @@ __device__ __forceinline__ float4 ld_cluster(uint32_t a, uint32_t rank) {
 
 struct TileArgs {
   int nb;            // steps along K
-  int mt, tiles;     // token tiles, tiles in all
+  int seg;           // steps that one accumulator takes
+  int mt, nt, tiles; // token tiles, tiles along N, in all
+  int group;         // pair kernel: token tiles walked together along N
   int splits;        // blocks of a cluster share one tile's steps
   uint32_t a_bytes;  // bytes of the token tile's box
   bool y_tma, r_tma; // pair kernel: rows of y / the residual that TMA can address
@@ -59,7 +66,7 @@ struct Geo {
   static constexpr int cols = NT / (epi / 4);  // per epilogue warp
   static constexpr int threads = 64 + 32 * epi;
   static constexpr uint32_t stage = kABytes + (uint32_t)NT * BK * 2;
-  static constexpr int stages = NT == 256 ? 4 : NT == 128 ? 6 : 8;
+  static constexpr int stages = NT == 128 ? 6 : 8;
   static constexpr uint32_t tmem_cols = 2 * NT;
   static constexpr uint32_t off_ctrl = (uint32_t)stages * stage;
   static constexpr size_t smem = (size_t)off_ctrl + 1024 + 1024;  // control block, alignment
@@ -106,7 +113,9 @@ __device__ __forceinline__ bool wait(const Bars& b, uint64_t* bar, uint32_t pari
   return __all_sync(0xffffffffu, ok);
 }
 
-template <int NT>
+// SEG: a tile's steps go into the accumulators in segments, whose sums the
+// epilogue warps add in registers.
+template <int NT, bool SEG>
 __global__ void __launch_bounds__(Geo<NT>::threads, 1)
     linear_gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_w,
                        const LinearArgs a, const TileArgs ta) {
@@ -166,10 +175,10 @@ __global__ void __launch_bounds__(Geo<NT>::threads, 1)
     constexpr uint32_t idesc = tc::idesc_f16(BM, NT);
     int g = 0, u = 0;
     bool ok = true;
-    for (int tile = first; tile < ta.tiles && ok; tile += stride, ++u) {
-      if (u >= 2 && !wait(b, &b.acc_empty[u & 1], ((u >> 1) - 1) & 1, a.flags)) break;
-      for (int kb = kb0; kb < kb1; ++kb, ++g) {
+    for (int tile = first; tile < ta.tiles && ok; tile += stride) {
+      for (int kb = kb0, e = 0; kb < kb1; ++kb, ++g) {  // e: step of the segment
         const int s = g % G::stages;
+        if (e == 0 && u >= 2 && !(ok = wait(b, &b.acc_empty[u & 1], ((u >> 1) - 1) & 1, a.flags))) break;
         if (!(ok = wait(b, &b.full[s], (g / G::stages) & 1, a.flags))) break;
         tc::tc_fence_after();
         const uint32_t base = tc::smem_addr(sm + (size_t)s * G::stage);
@@ -177,11 +186,15 @@ __global__ void __launch_bounds__(Geo<NT>::threads, 1)
         if (tc::elect_one()) {
 #pragma unroll
           for (int kk = 0; kk < BK / 16; ++kk)
-            tc::mma_f16(tmem + (uint32_t)((u & 1) * NT), ad + 2 * kk, bd + 2 * kk, idesc, kb > kb0 || kk > 0);
+            tc::mma_f16(tmem + (uint32_t)((u & 1) * NT), ad + 2 * kk, bd + 2 * kk, idesc, e > 0 || kk > 0);
           tc::mma_commit(&b.empty[s]);
-          if (kb == kb1 - 1) tc::mma_commit(&b.acc_full[u & 1]);
+          if (e == ta.seg - 1 || kb == kb1 - 1) tc::mma_commit(&b.acc_full[u & 1]);
         }
         __syncwarp();
+        if (++e == ta.seg || kb == kb1 - 1) {
+          e = 0;
+          ++u;
+        }
       }
     }
   } else {
@@ -191,24 +204,49 @@ __global__ void __launch_bounds__(Geo<NT>::threads, 1)
     for (int tile = first; tile < ta.tiles; tile += stride, ++u) {
       const int m0 = (tile % ta.mt) * BM, n0 = (tile / ta.mt) * NT;
       const int r = 32 * q4 + lane, row = m0 + r;
+      float sum[SEG ? G::cols : 1] = {};
+      if constexpr (SEG) {
+        bool ok = true;
+        for (int left = kb1 - kb0; left > ta.seg; left -= ta.seg, ++u) {
+          if (!(ok = wait(b, &b.acc_full[u & 1], (u >> 1) & 1, a.flags))) break;
+          tc::tc_fence_after();
+#pragma unroll
+          for (int c = 0; c < G::cols; c += 32) {
+            uint32_t d[32];
+            tc::tmem_ld32(tl + (uint32_t)((u & 1) * NT + c), d);
+            tc::tmem_ld32_wait(d);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) sum[c + i] += __uint_as_float(d[i]);
+          }
+          tc::tc_fence_before();
+          __syncwarp();
+          if (lane == 0) tc::bar_arrive(&b.acc_empty[u & 1]);
+        }
+        if (!ok) break;
+      }
       if (!wait(b, &b.acc_full[u & 1], (u >> 1) & 1, a.flags)) break;
       tc::tc_fence_after();
       if (S > 1) {  // partial tile to shared memory (every stage has been consumed)
         float* red = reinterpret_cast<float*>(sm) + (size_t)r * G::red_pitch + c0;
-#pragma unroll 1
+#pragma unroll
         for (int c = 0; c < G::cols; c += 32) {
           uint32_t d[32];
           __syncwarp();
-          tc::tmem_ld32(tl + (uint32_t)c, d);
+          tc::tmem_ld32(tl + (uint32_t)((u & 1) * NT + c), d);
           tc::tmem_ld32_wait(d);
           if (row < a.T) {
 #pragma unroll
-            for (int i = 0; i < 32; i += 4) *reinterpret_cast<uint4*>(red + c + i) = make_uint4(d[i], d[i + 1], d[i + 2], d[i + 3]);
+            for (int i = 0; i < 32; i += 4) {
+              float v[4];
+#pragma unroll
+              for (int e = 0; e < 4; ++e) v[e] = __uint_as_float(d[i + e]) + (SEG ? sum[SEG ? c + i + e : 0] : 0.0f);
+              *reinterpret_cast<float4*>(red + c + i) = make_float4(v[0], v[1], v[2], v[3]);
+            }
           }
         }
         break;
       }
-#pragma unroll 1
+#pragma unroll
       for (int c = 0; c < G::cols; c += 32) {
         uint32_t d[32];
         __syncwarp();
@@ -222,7 +260,7 @@ __global__ void __launch_bounds__(Geo<NT>::threads, 1)
         if (row < a.T) {
           float v[32];
 #pragma unroll
-          for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(d[i]);
+          for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(d[i]) + (SEG ? sum[SEG ? c + i : 0] : 0.0f);
           finish(a, row, n0 + c0 + c, v);
         }
       }
@@ -260,12 +298,13 @@ __global__ void __launch_bounds__(Geo<NT>::threads, 1)
 // 128 tokens (A) and half of the weight rows (B), and each accumulates its
 // tokens against all 256 rows. Warps: 0 TMA, 1 tensor memory and (in the
 // leading block) MMA issue, 4-11 epilogue (a lane quarter, 128 columns each).
+constexpr int kGroup = 16;
 struct Pair {
   static constexpr int epi = 8, threads = 384;
-  static constexpr int stages = 5;
+  static constexpr int stages = 6;
   static constexpr uint32_t stage = kABytes + 128 * BK * 2;
-  static constexpr uint32_t off_out = stages * stage;  // [epi][2][32 rows][128 bytes]
-  static constexpr uint32_t off_ctrl = off_out + epi * 8192;
+  static constexpr uint32_t off_out = stages * stage;  // [epi][32 rows][128 bytes]
+  static constexpr uint32_t off_ctrl = off_out + epi * 4096;
   static constexpr size_t smem = (size_t)off_ctrl + 1024 + 1024;
   static_assert(smem <= 232448, "shared memory of a block");
 };
@@ -279,13 +318,20 @@ __device__ __forceinline__ void mma_f16_pair(uint32_t d_tmem, uint64_t a_desc, u
       : "memory");
 }
 
-// An epilogue warp's 32 rows by 32 columns, chunk c of its staging area: rows
-// of 128 bytes in the 128-byte swizzle, 64 FP16 columns (two chunks) or 32
-// FP32 columns (one).
+// 16 bytes of an epilogue warp's staging area: 32 rows of 128 bytes in the
+// 128-byte swizzle, 64 FP16 columns (chunk c: 32 of them) or 32 FP32 columns.
 template <typename Y>
 __device__ __forceinline__ uint8_t* piece(uint8_t* out, int c, int lane, int i) {
-  if (sizeof(Y) == 2) return out + (c >> 1) * 4096 + tc::sw128_offset(lane, 4 * (c & 1) + i);
-  return out + c * 4096 + tc::sw128_offset(lane, i);
+  return out + tc::sw128_offset(lane, (sizeof(Y) == 2 ? 4 * c : 0) + i);
+}
+
+// Tile number to (token tile, tile along N): `group` token tiles go along N
+// together, so that the tiles in flight share few rows of both operands.
+__device__ __forceinline__ void place(const TileArgs& t, int tile, int& m, int& n) {
+  const int g = tile / (t.group * t.nt), r = tile - g * t.group * t.nt;
+  const int wide = min(t.group, t.mt - g * t.group);
+  m = g * t.group + r % wide;
+  n = r / wide;
 }
 
 template <typename Y>
@@ -327,12 +373,19 @@ __global__ void __launch_bounds__(Pair::threads, 1)
 
   const int nb = ta.nb;
   const int first = (int)blockIdx.x / 2, stride = (int)gridDim.x / 2;
+  // FP32 results: sums of segments in registers. 384 x 168 registers at launch
+  // = 128 x 72 + 256 x 216.
+  constexpr bool SEG = sizeof(Y) == 4;
+  if (SEG && warp < 4) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
   if (warp == 0) {
     // Both blocks' loads complete on the leading block's barrier.
     int g = 0;
     bool ok = true;
     for (int tile = first; tile < ta.tiles && ok; tile += stride) {
-      const int m0 = (tile % ta.mt) * 256 + rank * BM, n0 = (tile / ta.mt) * 256 + rank * 128;
+      int m0, n0;
+      place(ta, tile, m0, n0);
+      m0 = m0 * 256 + rank * BM;
+      n0 = n0 * 256 + rank * 128;
       for (int kb = 0; kb < nb; ++kb, ++g) {
         const int s = g % G::stages;
         if (g >= G::stages && !(ok = wait(b, &b.empty[s], ((g / G::stages) - 1) & 1, a.flags))) break;
@@ -358,10 +411,10 @@ __global__ void __launch_bounds__(Pair::threads, 1)
       constexpr uint32_t idesc = tc::idesc_f16(256, 256);
       int g = 0, u = 0;
       bool ok = true;
-      for (int tile = first; tile < ta.tiles && ok; tile += stride, ++u) {
-        if (u >= 2 && !wait(b, &b.acc_empty[u & 1], ((u >> 1) - 1) & 1, a.flags)) break;
-        for (int kb = 0; kb < nb; ++kb, ++g) {
+      for (int tile = first; tile < ta.tiles && ok; tile += stride) {
+        for (int kb = 0, e = 0; kb < nb; ++kb, ++g) {  // e: step of the segment
           const int s = g % G::stages;
+          if (e == 0 && u >= 2 && !(ok = wait(b, &b.acc_empty[u & 1], ((u >> 1) - 1) & 1, a.flags))) break;
           if (!(ok = wait(b, &b.full[s], (g / G::stages) & 1, a.flags))) break;
           tc::tc_fence_after();
           const uint32_t base = tc::smem_addr(sm + (size_t)s * G::stage);
@@ -369,40 +422,65 @@ __global__ void __launch_bounds__(Pair::threads, 1)
           if (tc::elect_one()) {
 #pragma unroll
             for (int kk = 0; kk < BK / 16; ++kk)
-              mma_f16_pair(tmem + (uint32_t)((u & 1) * 256), ad + 2 * kk, bd + 2 * kk, idesc, kb > 0 || kk > 0);
+              mma_f16_pair(tmem + (uint32_t)((u & 1) * 256), ad + 2 * kk, bd + 2 * kk, idesc, e > 0 || kk > 0);
             tc::mma_commit_pair(&b.empty[s]);
-            if (kb == nb - 1) tc::mma_commit_pair(&b.acc_full[u & 1]);
+            if (e == ta.seg - 1 || kb == nb - 1) tc::mma_commit_pair(&b.acc_full[u & 1]);
           }
           __syncwarp();
+          if (++e == ta.seg || kb == nb - 1) {
+            e = 0;
+            ++u;
+          }
         }
       }
     }
   } else if (warp >= 4) {
+    if constexpr (SEG) asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
     constexpr int kBox = 128 / (int)sizeof(Y);                  // columns per staged row
-    constexpr int kPass = 2 * kBox, kChunks = kPass / 32;       // columns and chunks per staging pass
+    constexpr int kPass = kBox, kChunks = kPass / 32;           // columns and chunks per staging pass
     const int q4 = warp & 3, e8 = warp - 4, j2 = e8 >> 2;
     const uint32_t tl = tmem + ((uint32_t)(32 * q4) << 16) + (uint32_t)(128 * j2);
     const uint32_t acc_empty0 = tc::map_rank(tc::smem_addr(&b.acc_empty[0]), 0);
-    uint8_t* out = sm + G::off_out + e8 * 8192;
+    uint8_t* out = sm + G::off_out + e8 * 4096;
     int u = 0, loads = 0;
     for (int tile = first; tile < ta.tiles; tile += stride, ++u) {
-      const int y0 = (tile % ta.mt) * 256 + rank * BM + 32 * q4, row = y0 + lane;
-      const int x0 = (tile / ta.mt) * 256 + 128 * j2;
+      int y0, x0;
+      place(ta, tile, y0, x0);
+      y0 = y0 * 256 + rank * BM + 32 * q4;
+      x0 = x0 * 256 + 128 * j2;
+      const int row = y0 + lane;
+      float sum[SEG ? 128 : 1] = {};
+      if constexpr (SEG) {
+        for (int left = nb; left > ta.seg; left -= ta.seg, ++u) {
+          wait(b, &b.acc_full[u & 1], (u >> 1) & 1, a.flags);  // given up: the stores below are left out
+          tc::tc_fence_after();
+#pragma unroll
+          for (int c = 0; c < 128; c += 32) {
+            uint32_t d[32];
+            tc::tmem_ld32(tl + (uint32_t)((u & 1) * 256 + c), d);
+            tc::tmem_ld32_wait(d);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) sum[c + i] += __uint_as_float(d[i]);
+          }
+          tc::tc_fence_before();
+          __syncwarp();
+          if (lane == 0) tc::bar_arrive_cluster(acc_empty0 + 8 * (u & 1));
+        }
+      }
       bool got = false;
-#pragma unroll 1
+#pragma unroll (SEG ? 128 / kPass : 1)
       for (int p = 0; p < 128 / kPass; ++p) {
         const int xp = x0 + p * kPass;
         // The stores of the last pass have read the staging area; the
         // residual's tile comes into it, and the results take its place.
-        if (lane < 2) tc::tma_store_wait_read();
+        if (lane == 0) tc::tma_store_wait_read();
         __syncwarp();
         const bool some = y0 < a.T && xp < a.N, load = some && ta.r_tma;
         if (load) {
           if (lane == 0) {
-            const int boxes = xp + kBox < a.N ? 2 : 1;
             tc::fence_async_smem();
-            tc::bar_expect_tx(&b.res[e8], 4096u * boxes);
-            for (int j = 0; j < boxes; ++j) tc::tma_load_2d(out + 4096 * j, &map_r, xp + kBox * j, y0, &b.res[e8]);
+            tc::bar_expect_tx(&b.res[e8], 4096u);
+            tc::tma_load_2d(out, &map_r, xp, y0, &b.res[e8]);
           }
           __syncwarp();
         }
@@ -410,7 +488,7 @@ __global__ void __launch_bounds__(Pair::threads, 1)
         tc::tc_fence_after();
         if (load && !wait(b, &b.res[e8], loads++ & 1, a.flags)) got = false;
         const bool last = p == 128 / kPass - 1;
-#pragma unroll 1
+#pragma unroll (SEG ? kChunks : 1)
         for (int c = 0; c < kChunks; ++c) {
           uint32_t d[32];
           __syncwarp();
@@ -424,13 +502,9 @@ __global__ void __launch_bounds__(Pair::threads, 1)
           const int n = xp + 32 * c;
           float v[32];
 #pragma unroll
-          for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(d[i]);
-          if (a.bias) {
-            const float bias = n + lane < a.N ? a.bias[n + lane] : 0.0f;
-#pragma unroll
-            for (int i = 0; i < 32; ++i) v[i] += __shfl_sync(0xffffffffu, bias, i);
-          }
-          activate(a.act, v);
+          for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(d[i]) + (SEG ? sum[SEG ? p * kPass + 32 * c + i : 0] : 0.0f);
+          if (a.bias) add_bias(a, n, v);
+          activate<sizeof(Y) == 2>(a.act, v);
           if (a.residual && !ta.r_tma && row < a.T) {
             const Y* r = static_cast<const Y*>(a.residual) + (size_t)row * (size_t)a.ldr + n;
 #pragma unroll
@@ -476,23 +550,22 @@ __global__ void __launch_bounds__(Pair::threads, 1)
         if (ta.y_tma) {
           tc::fence_async_smem();
           __syncwarp();
-          // A lane per store: one lane issuing both takes twice as long.
-          if (lane < 2 && some && xp + kBox * lane < a.N) tc::tma_store_2d(&map_y, xp + kBox * lane, y0, out + 4096 * lane);
+          if (lane == 0 && some) tc::tma_store_2d(&map_y, xp, y0, out);
         } else {
           // Rows that TMA cannot address (pitch no multiple of 16 bytes): one element per lane.
           __syncwarp();
           for (int rr = 0; rr < min(32, a.T - y0); ++rr)
 #pragma unroll
             for (int j = 0; j < kPass / 32; ++j) {
-              const int x = 32 * j + lane, box = x / kBox, col = (x % kBox) * (int)sizeof(Y);
-              const Y v = *reinterpret_cast<const Y*>(out + 4096 * box + tc::sw128_offset(rr, col >> 4) + (col & 15));
+              const int x = 32 * j + lane, col = x * (int)sizeof(Y);
+              const Y v = *reinterpret_cast<const Y*>(out + tc::sw128_offset(rr, col >> 4) + (col & 15));
               if (xp + x < a.N) static_cast<Y*>(a.y)[(size_t)(y0 + rr) * (size_t)a.ldy + xp + x] = v;
             }
           __syncwarp();
         }
       }
     }
-    if (lane < 2) tc::tma_store_wait_read();  // the grid's end waits for the writes
+    if (lane == 0) tc::tma_store_wait_read();  // the grid's end waits for the writes
   }
   tc::tc_fence_before();
   __syncwarp();
@@ -529,7 +602,7 @@ struct Launch {
   }
 };
 
-template <int NT>
+template <int NT, bool SEG>
 int launch_gemm(const LinearArgs& a, int splits, int sms, int dev, cudaStream_t st) {
   using G = Geo<NT>;
   static std::mutex mu;
@@ -537,7 +610,7 @@ int launch_gemm(const LinearArgs& a, int splits, int sms, int dev, cudaStream_t 
   {
     std::lock_guard<std::mutex> lock(mu);
     if (!set[dev]) {
-      MOE_CUDA_TRY(cudaFuncSetAttribute(linear_gemm_kernel<NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)G::smem));
+      MOE_CUDA_TRY(cudaFuncSetAttribute(linear_gemm_kernel<NT, SEG>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)G::smem));
       set[dev] = true;
     }
   }
@@ -545,6 +618,7 @@ int launch_gemm(const LinearArgs& a, int splits, int sms, int dev, cudaStream_t 
   while (box < BM && box < a.T) box *= 2;
   TileArgs t = {};
   t.nb = (a.K + BK - 1) / BK;
+  t.seg = SEG ? kSegment : t.nb;
   t.mt = (a.T + BM - 1) / BM;
   t.tiles = t.mt * ((a.N + NT - 1) / NT);
   t.splits = splits;
@@ -554,9 +628,14 @@ int launch_gemm(const LinearArgs& a, int splits, int sms, int dev, cudaStream_t 
   if ((rc = row_map(&mx, a.x, false, a.K, a.T, a.ldx, box)) != MOE_OK) return rc;
   if ((rc = row_map(&mw, a.w, false, a.K, a.N, a.K, NT)) != MOE_OK) return rc;
   const Launch l((unsigned)(splits > 1 ? t.tiles * splits : std::min(t.tiles, sms)), G::threads, G::smem, splits, st);
-  const cudaError_t e = cudaLaunchKernelEx(&l.cfg, linear_gemm_kernel<NT>, mx, mw, a, t);
+  const cudaError_t e = cudaLaunchKernelEx(&l.cfg, linear_gemm_kernel<NT, SEG>, mx, mw, a, t);
   if (e != cudaSuccess) return fail(MOE_ERR_CUDA, "moe_linear launch: %s", cudaGetErrorString(e));
   return MOE_OK;
+}
+
+template <int NT>
+int launch_gemm(const LinearArgs& a, int splits, int sms, int dev, cudaStream_t st) {
+  return a.y32 ? launch_gemm<NT, true>(a, splits, sms, dev, st) : launch_gemm<NT, false>(a, splits, sms, dev, st);
 }
 
 template <typename Y>
@@ -574,8 +653,11 @@ int launch_pair(const LinearArgs& a, int sms, int dev, cudaStream_t st) {
   constexpr bool f32 = sizeof(Y) == 4;
   TileArgs t = {};
   t.nb = (a.K + BK - 1) / BK;
+  t.seg = f32 ? kSegment : t.nb;
   t.mt = (a.T + 255) / 256;
-  t.tiles = t.mt * ((a.N + 255) / 256);
+  t.nt = (a.N + 255) / 256;
+  t.tiles = t.mt * t.nt;
+  t.group = kGroup;
   t.splits = 1;
   t.y_tma = a.ldy * (long long)sizeof(Y) % 16 == 0;
   t.r_tma = a.residual && a.ldr * (long long)sizeof(Y) % 16 == 0;
@@ -595,7 +677,6 @@ int launch_pair(const LinearArgs& a, int sms, int dev, cudaStream_t st) {
 int launch_plan(const LinearArgs& a, const LinearPlan& p, int sms, int dev, cudaStream_t st) {
   switch (p.nt) {
     case 0: return a.y32 ? launch_pair<float>(a, sms, dev, st) : launch_pair<__half>(a, sms, dev, st);
-    case 256: return launch_gemm<256>(a, p.splits, sms, dev, st);
     case 128: return launch_gemm<128>(a, p.splits, sms, dev, st);
     case 64: return launch_gemm<64>(a, p.splits, sms, dev, st);
     default: return launch_gemm<32>(a, p.splits, sms, dev, st);

@@ -23,7 +23,7 @@ inline LinearPlan linear_plan(int T, int N, int nb, int sms) {
   LinearPlan best = {0, 1};
   float t_best = 5.0f + (float)pair_waves * (0.38f * (float)nb + per_tile);
   const float a_bytes = 128.0f * (float)std::min(T, kLinearTokens);
-  for (int nt = 32; nt <= 256; nt *= 2) {
+  for (int nt = 32; nt <= 128; nt *= 2) {
     const int tiles = mt * ((N + nt - 1) / nt);
     const float step = std::max(0.2f, (128.0f * (float)nt + a_bytes) / 68000.0f);
     for (int s = 1; s <= kLinearMaxSplits && s <= nb; s *= 2) {

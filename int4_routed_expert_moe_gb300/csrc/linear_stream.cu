@@ -85,7 +85,7 @@ __global__ void __launch_bounds__(32 * kWarps, 2) linear_stream_kernel(const Lin
   for (int w = 0; w < kWarps; ++w) v[0] += red[w][t][n];
   if (n0 + n >= a.N) return;
   if (a.bias) v[0] += a.bias[n0 + n];
-  activate(a.act, v);
+  activate<false>(a.act, v);
   const size_t at = (size_t)t * (size_t)a.ldy + n0 + n, ra = (size_t)t * (size_t)a.ldr + n0 + n;
   if (a.y32) {
     if (a.residual) v[0] += static_cast<const float*>(a.residual)[ra];
