@@ -22,8 +22,14 @@
 namespace moe {
 namespace {
 
-constexpr int kMaxChunks = 152;  // one block per SM
-constexpr int kMinChunk = 32;    // tokens
+constexpr int kMinChunk = 32;  // tokens
+// Threads of a block by the values a lane holds, so that its registers suffice,
+// and chunks at most: what fills 152 SMs once.
+constexpr int threads_of(int nv) { return nv == 8 ? 1024 : nv == 16 ? 512 : 256; }
+constexpr int max_chunks(int E) { return E > 512 ? 304 : 152; }
+// Up to here the last block joins the chunks itself.
+constexpr int kFusedChunks = 16;
+constexpr int kFusedOutputs = 8192;
 
 struct BalanceArgs {
   const void* logits;
@@ -39,12 +45,13 @@ struct BalanceArgs {
   uint32_t* ticket;
   int32_t *counts, *tokens;
   float *mean, *loss;
+  bool fused;
   // backward
   const int32_t *bcounts, *btokens;
   const float* grad;
   float* dl;
   long long ldd;
-  bool accumulate, vec_out;
+  bool accumulate, vec_out;  // vec_out: four experts per store
 };
 
 __device__ __forceinline__ int offset_at(const BalanceArgs& a, int i) {
@@ -88,41 +95,51 @@ __device__ __forceinline__ void load_row(const BalanceArgs& a, int t, int l, flo
   }
 }
 
-// x: logits in, probabilities out (0 for every expert of a bad token); rest:
-// 1 - sigmoid(l). False for a bad token: NaN or +inf, or nothing above -inf.
+template <int L>
+__device__ __forceinline__ float group_max(float v, unsigned mask) {
+#pragma unroll
+  for (int o = 1; o < L; o <<= 1) v = fmaxf(v, __shfl_xor_sync(mask, v, o));
+  return v;
+}
+template <int L>
+__device__ __forceinline__ float group_sum(float v, unsigned mask) {
+#pragma unroll
+  for (int o = 1; o < L; o <<= 1) v += __shfl_xor_sync(mask, v, o);
+  return v;
+}
+
+// x: logits in, probabilities times their sum out; rest: 1 - sigmoid(l). The
+// sum's reciprocal, 0 for a bad token: NaN or +inf, or nothing above -inf (its
+// x may be anything).
 template <int L, int NV, bool REST>
-__device__ __forceinline__ bool probabilities(float (&x)[NV], float (&rest)[NV], bool sigmoid, unsigned mask) {
+__device__ __forceinline__ float probabilities(float (&x)[NV], float (&rest)[NV], bool sigmoid, unsigned mask) {
   float m = -INFINITY;
-  bool bad = false;
+  bool odd = false;
 #pragma unroll
   for (int v = 0; v < NV; ++v) {
-    bad |= !(x[v] < INFINITY);
+    odd |= !(x[v] < INFINITY);
     m = fmaxf(m, x[v]);
   }
-#pragma unroll
-  for (int o = 1; o < L; o <<= 1) m = fmaxf(m, __shfl_xor_sync(mask, m, o));
-  bad = __ballot_sync(mask, bad) & mask ? true : m == -INFINITY;
+  odd = (__ballot_sync(mask, odd) & mask) != 0;
   float s = 0.0f;
   if (!sigmoid) {
+    m = group_max<L>(m, mask);
 #pragma unroll
     for (int v = 0; v < NV; ++v) s += x[v] = expf(x[v] - m);
   } else {
     // With u = e^-|l|, sigmoid(l) = (l < 0 ? u : 1) / (1 + u). Where every logit
     // is negative, numerators e^(l - max l) keep the sum away from 0.
-    const bool low = m < 0.0f;
+    const bool low = (__ballot_sync(mask, m >= 0.0f) & mask) == 0;
+    m = low ? group_max<L>(m, mask) : 0.0f;
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
-      const float l = x[v], u = expf(-fabsf(l)), r = 1.0f / (1.0f + u);
+      const float l = x[v], u = expf(-fabsf(l)), r = __fdividef(1.0f, 1.0f + u);
       if (REST) rest[v] = l < 0.0f ? r : u * r;
       s += x[v] = (l < 0.0f ? (low ? expf(l - m) : u) : 1.0f) * r;
     }
   }
-#pragma unroll
-  for (int o = 1; o < L; o <<= 1) s += __shfl_xor_sync(mask, s, o);
-  const float inv = 1.0f / s;
-#pragma unroll
-  for (int v = 0; v < NV; ++v) x[v] = bad ? 0.0f : x[v] * inv;
-  return !bad;
+  s = group_sum<L>(s, mask);
+  return odd || m == -INFINITY ? 0.0f : 1.0f / s;
 }
 
 // The first sequence with tokens from t0 on that can hold t0: offsets at or
@@ -136,14 +153,66 @@ __device__ __forceinline__ int first_sequence(const BalanceArgs& a, int t0) {
   return max(n - 1, 0);
 }
 
+// A warp's 32 experts of sequence s from the sums over its chunks: the outputs,
+// and what they add to the loss (part i).
+__device__ __forceinline__ void finish_experts(const BalanceArgs& a, int s, int e, int i, float p, int c, int n,
+                                               int lane) {
+  const float mean = n ? p / (float)n : 0.0f;
+  if (e < a.E) {
+    a.counts[(size_t)s * a.E + e] = c;
+    if (a.mean) a.mean[(size_t)s * a.E + e] = mean;
+  }
+  if (e == 0) a.tokens[s] = n;
+  if (!a.loss) return;
+  const float f = e < a.E && n ? (float)c * ((float)a.E / ((float)a.k * (float)n)) * mean : 0.0f;
+  const float part = warp_sum(f);
+  if (lane == 0) a.lsum[i] = part;
+}
+
+// The losses' sum over coef and the sequences that count; whole block, in a
+// fixed order. parts: n of them.
+__device__ __forceinline__ void write_loss(const BalanceArgs& a, int n, double* sums, int* live) {
+  double v = 0.0;
+  int c = 0;
+  for (int i = threadIdx.x; i < n; i += blockDim.x) v += (double)__ldcg(a.lsum + i);
+  for (int i = threadIdx.x; i < a.S; i += blockDim.x) c += __ldcg(a.tokens + i) > 0;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  c = __reduce_add_sync(0xffffffffu, c);
+  if ((threadIdx.x & 31) == 0) {
+    sums[threadIdx.x >> 5] = v;
+    live[threadIdx.x >> 5] = c;
+  }
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    for (int i = 1; i < (int)blockDim.x / 32; ++i) {
+      v += sums[i];
+      c += live[i];
+    }
+    a.loss[0] = c ? (float)(v * (double)a.coef / (double)c) : 0.0f;
+  }
+}
+// Whole block: true in the last one of `total` to call; the others' writes are
+// then visible.
+__device__ __forceinline__ bool last_block(uint32_t* ticket, uint32_t total, int* flag) {
+  __threadfence();
+  __syncthreads();
+  if (threadIdx.x == 0) *flag = atomicInc(ticket, total - 1) == total - 1;  // back to 0 with the last
+  __syncthreads();
+  const bool last = *flag;
+  if (last) __threadfence();
+  return last;
+}
+
 template <int L, int NV, int VEC, bool F16>
-__global__ void __launch_bounds__(256) balance_partial_kernel(const BalanceArgs a) {
+__global__ void __launch_bounds__(threads_of(NV)) balance_partial_kernel(const BalanceArgs a) {
+  constexpr int kThreads = threads_of(NV), kWarps = kThreads / 32;
+  constexpr int G = 32 / L, kGroups = kWarps * G;  // groups per warp, per block
+  __shared__ float sums[kGroups][L * NV];
+  __shared__ int32_t cnt[L * NV];
+  __shared__ int32_t good[kWarps];
   griddep_wait();
   griddep_launch_dependents();
-  constexpr int G = 32 / L, kGroups = 8 * G;  // groups per warp, per block
-  __shared__ float sums[kGroups][L * NV];
-  __shared__ int32_t cnt[1024];
-  __shared__ int32_t good[8];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, l = lane & (L - 1), grp = warp * G + lane / L;
   const unsigned mask = L == 32 ? 0xffffffffu : ((1u << L) - 1u) << (lane & ~(L - 1));
   const int t0 = blockIdx.x * a.chunk, t1 = min(a.T, t0 + a.chunk);
@@ -151,20 +220,33 @@ __global__ void __launch_bounds__(256) balance_partial_kernel(const BalanceArgs 
     const int b0 = offset_at(a, s), lo = max(b0, t0), hi = min(offset_at(a, s + 1), t1);
     if (b0 >= t1) break;
     if (lo >= hi) continue;
-    for (int e = threadIdx.x; e < a.E; e += 256) cnt[e] = 0;
+    // The next token's logits are on their way while one is worked on (not
+    // with 32 values per lane: the registers are wanted for the values).
+    constexpr bool kAhead = NV <= 16;
+    float x[NV];
+    int t = lo + grp;
+    if (kAhead && t < hi) load_row<L, NV, VEC, F16>(a, t, l, x);
+    for (int e = threadIdx.x; e < a.E; e += kThreads) cnt[e] = 0;
     __syncthreads();
-    for (long long i = (long long)lo * a.k + threadIdx.x; i < (long long)hi * a.k; i += 256) {
+    for (long long i = (long long)lo * a.k + threadIdx.x; i < (long long)hi * a.k; i += kThreads) {
       const int e = a.ids[i];
       if (e >= 0 && e < a.E) atomicAdd(&cnt[e], 1);
     }
     float p[NV] = {};
     int n = 0;
-    for (int t = lo + grp; t < hi; t += kGroups) {
-      float x[NV], rest[NV];
-      load_row<L, NV, VEC, F16>(a, t, l, x);
-      n += probabilities<L, NV, false>(x, rest, a.sigmoid, mask);
+    for (; t < hi; t += kGroups) {
+      float next[NV], rest[NV];
+      if (!kAhead) load_row<L, NV, VEC, F16>(a, t, l, x);
+      if (kAhead && t + kGroups < hi) load_row<L, NV, VEC, F16>(a, t + kGroups, l, next);
+      const float inv = probabilities<L, NV, false>(x, rest, a.sigmoid, mask);
+      if (inv > 0.0f) {
+        ++n;
 #pragma unroll
-      for (int v = 0; v < NV; ++v) p[v] += x[v];
+        for (int v = 0; v < NV; ++v) p[v] = fmaf(x[v], inv, p[v]);
+      }
+      if (kAhead)
+#pragma unroll
+        for (int v = 0; v < NV; ++v) x[v] = next[v];
     }
 #pragma unroll
     for (int v = 0; v < NV; ++v) sums[grp][expert_of<L, NV, VEC>(l, v)] = p[v];
@@ -172,32 +254,63 @@ __global__ void __launch_bounds__(256) balance_partial_kernel(const BalanceArgs 
     if (lane == 0) good[warp] = n;
     __syncthreads();
     const size_t row = (size_t)blockIdx.x + s;
-    for (int e = threadIdx.x; e < a.E; e += 256) {
+    for (int e = threadIdx.x; e < a.E; e += kThreads) {
       float v = 0.0f;
-#pragma unroll
+#pragma unroll 8
       for (int g = 0; g < kGroups; ++g) v += sums[g][e];
       a.psum[row * a.E + e] = v;
       a.csum[row * a.E + e] = cnt[e];
     }
-    if (threadIdx.x == 0) {
-      int v = 0;
-#pragma unroll
-      for (int w = 0; w < 8; ++w) v += good[w];
-      a.nsum[row] = v;
+    if (warp == 0) {
+      const int v = __reduce_add_sync(0xffffffffu, lane < kWarps ? good[lane] : 0);
+      if (lane == 0) a.nsum[row] = v;
     }
     __syncthreads();
   }
+  if (!a.fused) return;
+  __shared__ int flag;
+  __shared__ double dsum[kWarps];
+  if (!last_block(a.ticket, gridDim.x, &flag)) return;
+  // The last block: a warp per sequence and 32 experts.
+  const int blocks = (a.E + 31) / 32;
+  for (int i = warp; i < blocks * a.S; i += kWarps) {
+    const int s = i / blocks, e = (i - s * blocks) * 32 + lane, b0 = offset_at(a, s), b1 = offset_at(a, s + 1);
+    const int c0 = b1 > b0 ? b0 / a.chunk : 0, c1 = b1 > b0 ? (b1 - 1) / a.chunk + 1 : 0;
+    float p = 0.0f;
+    int c = 0, n = 0;
+#pragma unroll 4
+    for (int r = c0; r < c1; ++r) {
+      const size_t row = (size_t)r + s;
+      n += __ldcg(a.nsum + row);
+      if (e < a.E) {
+        p += __ldcg(a.psum + row * a.E + e);
+        c += __ldcg(a.csum + row * a.E + e);
+      }
+    }
+    finish_experts(a, s, e, i, p, c, n, lane);
+  }
+  if (!a.loss) return;
+  __threadfence();
+  __syncthreads();
+  write_loss(a, blocks * a.S, dsum, good);
 }
 
-// Block (x, s): experts 32 x .. + 31 of sequence s; 8 warps share the partial rows.
-__global__ void __launch_bounds__(256) balance_join_kernel(const BalanceArgs a) {
+// Block (x, s): experts 32 x .. + 31 of sequence s; its warps share the partial rows.
+constexpr int kJoinWarps = 16;
+__global__ void __launch_bounds__(32 * kJoinWarps) balance_join_kernel(const BalanceArgs a) {
+  __shared__ float ps[kJoinWarps][32];
+  __shared__ int32_t cs[kJoinWarps][32], ns[kJoinWarps];
+  __shared__ double dsum[kJoinWarps];
+  __shared__ int flag;
   griddep_wait();
+  griddep_launch_dependents();
   const int s = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31, e = blockIdx.x * 32 + lane;
   const int lo = offset_at(a, s), hi = offset_at(a, s + 1);
   const int c0 = hi > lo ? lo / a.chunk : 0, c1 = hi > lo ? (hi - 1) / a.chunk + 1 : 0;
   float p = 0.0f;
   int c = 0, n = 0;
-  for (int r = c0 + warp; r < c1; r += 8) {
+#pragma unroll 4
+  for (int r = c0 + warp; r < c1; r += kJoinWarps) {
     const size_t row = (size_t)r + s;
     n += a.nsum[row];
     if (e < a.E) {
@@ -205,70 +318,36 @@ __global__ void __launch_bounds__(256) balance_join_kernel(const BalanceArgs a) 
       c += a.csum[row * a.E + e];
     }
   }
-  __shared__ float ps[8][32];
-  __shared__ int32_t cs[8][32], ns[8];
   ps[warp][lane] = p;
   cs[warp][lane] = c;
   if (lane == 0) ns[warp] = n;
   __syncthreads();
-  __shared__ bool last;
   if (warp == 0) {
     p = 0.0f;
     c = n = 0;
 #pragma unroll
-    for (int w = 0; w < 8; ++w) {
+    for (int w = 0; w < kJoinWarps; ++w) {
       p += ps[w][lane];
       c += cs[w][lane];
       n += ns[w];
     }
-    const float mean = n ? p / (float)n : 0.0f;
-    if (e < a.E) {
-      a.counts[(size_t)s * a.E + e] = c;
-      if (a.mean) a.mean[(size_t)s * a.E + e] = mean;
-    }
-    if (blockIdx.x == 0 && lane == 0) a.tokens[s] = n;
-    if (!a.loss) return;
-    const float f = e < a.E && n ? (float)c * ((float)a.E / ((float)a.k * (float)n)) * mean : 0.0f;
-    const float part = warp_sum(f);
-    if (lane == 0) {
-      a.lsum[(size_t)s * gridDim.x + blockIdx.x] = part;
-      __threadfence();
-      const uint32_t total = gridDim.x * gridDim.y;
-      last = atomicInc(a.ticket, total - 1) == total - 1;  // back to 0 with the last
-    }
+    finish_experts(a, s, e, s * (int)gridDim.x + (int)blockIdx.x, p, c, n, lane);
   }
-  if (!a.loss) return;
-  __syncthreads();
-  if (!last) return;
-  __threadfence();
-  double v = 0.0;
-  int live = 0;
-  for (int i = threadIdx.x; i < (int)(gridDim.x * a.S); i += 256) v += (double)__ldcg(a.lsum + i);
-  for (int i = threadIdx.x; i < a.S; i += 256) live += __ldcg(a.tokens + i) > 0;
-  __shared__ double vs[256];
-  vs[threadIdx.x] = v;
-  live = __syncthreads_count(0) + live;
-  __shared__ int lives;
-  if (threadIdx.x == 0) lives = 0;
-  __syncthreads();
-  if (live) atomicAdd(&lives, live);
-  __syncthreads();
-  if (threadIdx.x == 0) {
-    for (int i = 1; i < 256; ++i) v += vs[i];
-    a.loss[0] = lives ? (float)(v * (double)a.coef / (double)lives) : 0.0f;
-  }
+  if (!a.loss || !last_block(a.ticket, gridDim.x * gridDim.y, &flag)) return;
+  write_loss(a, (int)(gridDim.x * gridDim.y), dsum, ns);
 }
 
 template <int L, int NV, int VEC, bool F16>
-__global__ void __launch_bounds__(256) balance_back_kernel(const BalanceArgs a) {
+__global__ void __launch_bounds__(threads_of(NV)) balance_back_kernel(const BalanceArgs a) {
+  constexpr int kThreads = threads_of(NV);
+  constexpr int G = 32 / L, kGroups = kThreads / 32 * G;
   griddep_wait();
   griddep_launch_dependents();
-  constexpr int G = 32 / L, kGroups = 8 * G;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, l = lane & (L - 1), grp = warp * G + lane / L;
   const unsigned mask = L == 32 ? 0xffffffffu : ((1u << L) - 1u) << (lane & ~(L - 1));
   const int t0 = blockIdx.x * a.chunk, t1 = min(a.T, t0 + a.chunk);
   int live = 0;
-  for (int i = 0; i < a.S; i += 256) {
+  for (int i = 0; i < a.S; i += kThreads) {
     const int j = i + (int)threadIdx.x;
     live += __syncthreads_count(j < a.S && a.btokens[j] > 0);
   }
@@ -277,33 +356,58 @@ __global__ void __launch_bounds__(256) balance_back_kernel(const BalanceArgs a) 
     const int b0 = offset_at(a, s), lo = max(b0, t0), hi = min(offset_at(a, s + 1), t1);
     if (b0 >= t1) break;
     if (lo >= hi) continue;
+    constexpr bool kAhead = NV <= 16;
+    float x[NV], f[NV];
+    int t = lo + grp;
+    if (kAhead && t < hi) load_row<L, NV, VEC, F16>(a, t, l, x);
     const float n = (float)a.btokens[s];
     const float unit = n > 0.0f ? (float)a.E / ((float)a.k * n) : 0.0f;
     const float outer = n > 0.0f ? g / ((float)live * n) : 0.0f;
-    float f[NV];
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
       const int e = expert_of<L, NV, VEC>(l, v);
       f[v] = e < a.E ? (float)a.bcounts[(size_t)s * a.E + e] * unit : 0.0f;
     }
-    for (int t = lo + grp; t < hi; t += kGroups) {
-      float x[NV], rest[NV];
-      load_row<L, NV, VEC, F16>(a, t, l, x);
-      const bool ok = probabilities<L, NV, true>(x, rest, a.sigmoid, mask);
+    for (; t < hi; t += kGroups) {
+      float next[NV], rest[NV];
+      if (!kAhead) load_row<L, NV, VEC, F16>(a, t, l, x);
+      if (kAhead && t + kGroups < hi) load_row<L, NV, VEC, F16>(a, t + kGroups, l, next);
+      const float inv = probabilities<L, NV, true>(x, rest, a.sigmoid, mask);
       float dot = 0.0f;
 #pragma unroll
       for (int v = 0; v < NV; ++v) dot = fmaf(x[v], f[v], dot);
-#pragma unroll
-      for (int o = 1; o < L; o <<= 1) dot += __shfl_xor_sync(mask, dot, o);
-      float* out = a.dl + (size_t)t * (size_t)a.ldd;
+      dot = group_sum<L>(dot, mask) * inv;
+      const float c = outer * inv;
 #pragma unroll
       for (int v = 0; v < NV; ++v) {
-        const int e = expert_of<L, NV, VEC>(l, v);
-        float d = outer * x[v] * (f[v] - dot);
-        if (a.sigmoid) d *= rest[v];
-        if (!ok) d = 0.0f;
-        if (e < a.E) out[e] = a.accumulate ? out[e] + d : d;
+        x[v] = inv > 0.0f ? c * x[v] * (f[v] - dot) : 0.0f;
+        if (a.sigmoid && inv > 0.0f) x[v] *= rest[v];
       }
+      float* out = a.dl + (size_t)t * (size_t)a.ldd;
+      if (VEC == 4 && a.vec_out) {
+#pragma unroll
+        for (int j = 0; j < NV / 4; ++j) {
+          const int e = 4 * (l + L * j);
+          if (e < a.E) {
+            float4* o = reinterpret_cast<float4*>(out + e);
+            float4 d = make_float4(x[4 * j], x[4 * j + 1], x[4 * j + 2], x[4 * j + 3]);
+            if (a.accumulate) {
+              const float4 q = *o;
+              d.x += q.x; d.y += q.y; d.z += q.z; d.w += q.w;
+            }
+            *o = d;
+          }
+        }
+      } else {
+#pragma unroll
+        for (int v = 0; v < NV; ++v) {
+          const int e = expert_of<L, NV, VEC>(l, v);
+          if (e < a.E) out[e] = a.accumulate ? out[e] + x[v] : x[v];
+        }
+      }
+      if (kAhead)
+#pragma unroll
+        for (int v = 0; v < NV; ++v) x[v] = next[v];
     }
   }
 }
@@ -312,7 +416,7 @@ struct Ws {
   size_t psum, csum, nsum, lsum, total;
 };
 Ws ws_of(int T, int E, int S) {
-  const size_t rows = (size_t)std::min((T + kMinChunk - 1) / kMinChunk, kMaxChunks) + S;
+  const size_t rows = (size_t)std::min((T + kMinChunk - 1) / kMinChunk, max_chunks(E)) + S;
   auto up = [](size_t b) { return (b + 255) / 256 * 256; };
   Ws w;
   size_t o = kWorkspaceHeader;
@@ -325,7 +429,8 @@ Ws ws_of(int T, int E, int S) {
 }
 
 template <bool BACK, int L, int NV, int VEC, bool F16>
-cudaError_t launch_tokens(const cudaLaunchConfig_t& cfg, const BalanceArgs& a) {
+cudaError_t launch_tokens(cudaLaunchConfig_t cfg, const BalanceArgs& a) {
+  cfg.blockDim = dim3(threads_of(NV));
   if (BACK) return cudaLaunchKernelEx(&cfg, balance_back_kernel<L, NV, VEC, F16>, a);
   return cudaLaunchKernelEx(&cfg, balance_partial_kernel<L, NV, VEC, F16>, a);
 }
@@ -367,12 +472,18 @@ int check_balance(const char* who, const moe_balance_cfg* c, const void* logits,
   return MOE_OK;
 }
 
+void set_chunks(BalanceArgs& a) {
+  const int most = max_chunks(a.E);
+  a.chunk = std::max(kMinChunk, (a.T + most - 1) / most);
+  a.chunks = (a.T + a.chunk - 1) / a.chunk;
+}
+
 struct Launch {
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[1];
-  Launch(dim3 grid, cudaStream_t st) {
+  Launch(dim3 grid, int threads, cudaStream_t st) {
     cfg.gridDim = grid;
-    cfg.blockDim = dim3(256);
+    cfg.blockDim = dim3((unsigned)threads);
     cfg.stream = st;
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
@@ -412,8 +523,8 @@ int moe_balance_loss(const moe_balance_cfg* cfg, const void* logits, int logit_t
   a.logits = logits;
   a.ld = ld;
   a.T = T; a.E = E; a.k = k; a.S = S;
-  a.chunk = std::max(moe::kMinChunk, (T + moe::kMaxChunks - 1) / moe::kMaxChunks);
-  a.chunks = (T + a.chunk - 1) / a.chunk;
+  moe::set_chunks(a);
+  a.fused = T > 0 && a.chunks <= moe::kFusedChunks && (long long)S * E <= moe::kFusedOutputs;
   a.sigmoid = cfg->score == MOE_SCORE_SIGMOID;
   a.coef = cfg->coef;
   a.ids = ids;
@@ -430,11 +541,11 @@ int moe_balance_loss(const moe_balance_cfg* cfg, const void* logits, int logit_t
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   cudaError_t e = cudaSuccess;
   if (T > 0) {
-    const moe::Launch l(dim3((unsigned)a.chunks), st);
+    const moe::Launch l(dim3((unsigned)a.chunks), 0, st);
     e = moe::launch_tokens<false>(l.cfg, a, logit_type);
   }
-  if (e == cudaSuccess) {
-    const moe::Launch l(dim3((unsigned)((E + 31) / 32), (unsigned)S), st);
+  if (e == cudaSuccess && !a.fused) {
+    const moe::Launch l(dim3((unsigned)((E + 31) / 32), (unsigned)S), 32 * moe::kJoinWarps, st);
     e = cudaLaunchKernelEx(&l.cfg, moe::balance_join_kernel, a);
   }
   if (e != cudaSuccess) return moe::fail(MOE_ERR_CUDA, "%s launch: %s", who, cudaGetErrorString(e));
@@ -460,8 +571,8 @@ int moe_balance_loss_backward(const moe_balance_cfg* cfg, const void* logits, in
   a.logits = logits;
   a.ld = ld;
   a.T = T; a.E = E; a.k = k; a.S = S;
-  a.chunk = moe::kMinChunk;
-  a.chunks = (T + a.chunk - 1) / a.chunk;
+  moe::set_chunks(a);
+  a.vec_out = reinterpret_cast<uintptr_t>(dlogits) % 16 == 0 && ldd % 4 == 0;
   a.sigmoid = cfg->score == MOE_SCORE_SIGMOID;
   a.coef = cfg->coef;
   a.offsets = offsets;
@@ -471,7 +582,7 @@ int moe_balance_loss_backward(const moe_balance_cfg* cfg, const void* logits, in
   a.dl = dlogits;
   a.ldd = ldd;
   a.accumulate = accumulate != 0;
-  const moe::Launch l(dim3((unsigned)a.chunks), static_cast<cudaStream_t>(stream));
+  const moe::Launch l(dim3((unsigned)a.chunks), 0, static_cast<cudaStream_t>(stream));
   const cudaError_t e = moe::launch_tokens<true>(l.cfg, a, logit_type);
   if (e != cudaSuccess) return moe::fail(MOE_ERR_CUDA, "%s launch: %s", who, cudaGetErrorString(e));
   return MOE_OK;

@@ -659,7 +659,9 @@ int launch_pair(const LinearArgs& a, int sms, int dev, cudaStream_t st) {
   t.tiles = t.mt * t.nt;
   t.group = kGroup;
   t.splits = 1;
-  t.y_tma = a.ldy * (long long)sizeof(Y) % 16 == 0;
+  // A store is cut off at N in steps of 16 bytes: what it wrote past N would
+  // not be left as it was.
+  t.y_tma = a.ldy * (long long)sizeof(Y) % 16 == 0 && a.N * sizeof(Y) % 16 == 0;
   t.r_tma = a.residual && a.ldr * (long long)sizeof(Y) % 16 == 0;
   CUtensorMap mx, mw, my, mr;
   int rc;
