@@ -5,14 +5,17 @@
 //
 // A token's logits stay in the registers of a group of lanes: 8, 16 or 32
 // lanes with 8 values each for up to 256 experts, then 32 lanes with 16 or 32.
-// Forward, launch 1: chunks of consecutive tokens, one per block; each lane
-// adds its experts' probabilities over the group's tokens, the block adds its
-// groups in order and writes a partial row per sequence that the chunk meets,
-// row chunk + sequence: (chunk, sequence) pairs along the tokens never share
-// that sum, since each next pair raises one of the two. Launch 2: a block per
-// sequence and 32 experts adds the partial rows in order; the last block to
-// finish adds the losses in order. No floating-point atomics, so the same
-// inputs give the same bits. Backward: one pass, the probabilities recomputed.
+// Forward: chunks of consecutive tokens, one per block; each lane adds its
+// experts' probabilities over the group's tokens, the block adds its groups in
+// order. A sequence inside one chunk is finished there; of one that several
+// chunks share, each writes a partial row, and the last of them to arrive (a
+// ticket per sequence) adds the rows in order. The last block of all adds the
+// sequences' losses in order. Rows are numbered chunk + sequence: (chunk,
+// sequence) pairs along the tokens never share that sum, since each next pair
+// raises one of the two. Many experts' rows are too much for one block, so
+// above 2^15 + 2^13 of them (chunks times experts) a second launch joins all.
+// No floating-point atomics: the same inputs give the same bits. Backward: one
+// pass, the probabilities recomputed.
 #include <algorithm>
 
 #include "common.h"
@@ -26,10 +29,12 @@ constexpr int kMinChunk = 32;  // tokens
 // Threads of a block by the values a lane holds, so that its registers suffice,
 // and chunks at most: what fills 152 SMs once.
 constexpr int threads_of(int nv) { return nv == 8 ? 1024 : nv == 16 ? 512 : 256; }
-constexpr int max_chunks(int E) { return E > 512 ? 304 : 152; }
-// Up to here the last block joins the chunks itself.
-constexpr int kFusedChunks = 16;
-constexpr int kFusedOutputs = 8192;
+constexpr int max_chunks(int E) { return E > 512 ? 304 : 152; }  // not decreasing in E
+// A batch of up to 8 rounds of a block's tokens and 16 sequences is one chunk,
+// and so one block: 256 tokens of 64 experts 6.0 us, in eight chunks 11.9.
+constexpr int kAloneRounds = 8;
+constexpr int kAloneSequences = 16;
+constexpr int kFusedRows = 40960;  // chunks times experts that one launch joins
 
 struct BalanceArgs {
   const void* logits;
@@ -42,7 +47,8 @@ struct BalanceArgs {
   int32_t* csum;    // counts,
   int32_t* nsum;    // [chunks + S]: good tokens
   float* lsum;      // [S][ceil(E / 32)]
-  uint32_t* ticket;
+  uint32_t* ticket;  // of all blocks
+  uint32_t* tickets; // of the sequence that goes on past a chunk, by its first chunk
   int32_t *counts, *tokens;
   float *mean, *loss;
   bool fused;
@@ -108,38 +114,55 @@ __device__ __forceinline__ float group_sum(float v, unsigned mask) {
   return v;
 }
 
+// e^v and 1/v of the special-function unit: relative errors about 2^-22, and
+// for e^v the exponent's rounding, 2^-24 |v|.
+__device__ __forceinline__ float exp_unit(float v) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v * 1.4426950408889634f));
+  return r;
+}
+__device__ __forceinline__ float rcp_unit(float v) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+  return r;
+}
+
 // x: logits in, probabilities times their sum out; rest: 1 - sigmoid(l). The
 // sum's reciprocal, 0 for a bad token: NaN or +inf, or nothing above -inf (its
-// x may be anything).
+// x may be anything). Those are where the sum is NaN: exponents +-inf - +-inf,
+// or any - NaN; a sigmoid's +inf is looked for.
 template <int L, int NV, bool REST>
 __device__ __forceinline__ float probabilities(float (&x)[NV], float (&rest)[NV], bool sigmoid, unsigned mask) {
-  float m = -INFINITY;
-  bool odd = false;
+  float m = x[0];
 #pragma unroll
-  for (int v = 0; v < NV; ++v) {
-    odd |= !(x[v] < INFINITY);
-    m = fmaxf(m, x[v]);
-  }
-  odd = (__ballot_sync(mask, odd) & mask) != 0;
+  for (int v = 1; v < NV; ++v) m = fmaxf(m, x[v]);
   float s = 0.0f;
   if (!sigmoid) {
     m = group_max<L>(m, mask);
 #pragma unroll
-    for (int v = 0; v < NV; ++v) s += x[v] = expf(x[v] - m);
-  } else {
-    // With u = e^-|l|, sigmoid(l) = (l < 0 ? u : 1) / (1 + u). Where every logit
-    // is negative, numerators e^(l - max l) keep the sum away from 0.
-    const bool low = (__ballot_sync(mask, m >= 0.0f) & mask) == 0;
-    m = low ? group_max<L>(m, mask) : 0.0f;
+    for (int v = 0; v < NV; ++v) s += x[v] = exp_unit(x[v] - m);
+  } else if (__ballot_sync(mask, m >= 0.0f) & mask) {
+    if (__ballot_sync(mask, m == INFINITY) & mask) s = NAN;
+    // u = e^-l is infinite below l = -88, and sigmoid(l) 0.
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
-      const float l = x[v], u = expf(-fabsf(l)), r = __fdividef(1.0f, 1.0f + u);
-      if (REST) rest[v] = l < 0.0f ? r : u * r;
-      s += x[v] = (l < 0.0f ? (low ? expf(l - m) : u) : 1.0f) * r;
+      const float l = x[v], u = exp_unit(-l);
+      s += x[v] = rcp_unit(1.0f + u);
+      if (REST) rest[v] = l < 0.0f ? 1.0f - x[v] : u * x[v];
+    }
+  } else {
+    // Every logit is negative: e^(l - max l) / (1 + e^l), so that the sum stays
+    // away from 0.
+    m = group_max<L>(m, mask);
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      const float r = rcp_unit(1.0f + exp_unit(x[v]));
+      if (REST) rest[v] = r;
+      s += x[v] = exp_unit(x[v] - m) * r;
     }
   }
   s = group_sum<L>(s, mask);
-  return odd || m == -INFINITY ? 0.0f : 1.0f / s;
+  return s > 0.0f ? 1.0f / s : 0.0f;
 }
 
 // The first sequence with tokens from t0 on that can hold t0: offsets at or
@@ -154,19 +177,15 @@ __device__ __forceinline__ int first_sequence(const BalanceArgs& a, int t0) {
 }
 
 // A warp's 32 experts of sequence s from the sums over its chunks: the outputs,
-// and what they add to the loss (part i).
-__device__ __forceinline__ void finish_experts(const BalanceArgs& a, int s, int e, int i, float p, int c, int n,
-                                               int lane) {
+// and, returned, what they add to the loss.
+__device__ __forceinline__ float finish_experts(const BalanceArgs& a, int s, int e, float p, int c, int n) {
   const float mean = n ? p / (float)n : 0.0f;
   if (e < a.E) {
     a.counts[(size_t)s * a.E + e] = c;
     if (a.mean) a.mean[(size_t)s * a.E + e] = mean;
   }
   if (e == 0) a.tokens[s] = n;
-  if (!a.loss) return;
-  const float f = e < a.E && n ? (float)c * ((float)a.E / ((float)a.k * (float)n)) * mean : 0.0f;
-  const float part = warp_sum(f);
-  if (lane == 0) a.lsum[i] = part;
+  return warp_sum(e < a.E && n ? (float)c * ((float)a.E / ((float)a.k * (float)n)) * mean : 0.0f);
 }
 
 // The losses' sum over coef and the sequences that count; whole block, in a
@@ -204,32 +223,51 @@ __device__ __forceinline__ bool last_block(uint32_t* ticket, uint32_t total, int
   return last;
 }
 
+// The sequence to go on with after the empty sequence s at token t: past all
+// empty ones there. Whole block.
+__device__ __forceinline__ int next_sequence(const BalanceArgs& a, int s, int t) {
+  return max(s + 1, first_sequence(a, t));
+}
+
 template <int L, int NV, int VEC, bool F16>
 __global__ void __launch_bounds__(threads_of(NV)) balance_partial_kernel(const BalanceArgs a) {
   constexpr int kThreads = threads_of(NV), kWarps = kThreads / 32;
   constexpr int G = 32 / L, kGroups = kWarps * G;  // groups per warp, per block
-  __shared__ float sums[kGroups][L * NV];
+  __shared__ float sums[kWarps][L * NV];
   __shared__ int32_t cnt[L * NV];
   __shared__ int32_t good[kWarps];
   griddep_wait();
   griddep_launch_dependents();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, l = lane & (L - 1), grp = warp * G + lane / L;
   const unsigned mask = L == 32 ? 0xffffffffu : ((1u << L) - 1u) << (lane & ~(L - 1));
-  const int t0 = blockIdx.x * a.chunk, t1 = min(a.T, t0 + a.chunk);
-  for (int s = first_sequence(a, t0); s < a.S; ++s) {
-    const int b0 = offset_at(a, s), lo = max(b0, t0), hi = min(offset_at(a, s + 1), t1);
+  const int t0 = blockIdx.x * a.chunk, t1 = min(a.T, t0 + a.chunk), blocks = (a.E + 31) / 32;
+  const bool alone = gridDim.x == 1;
+  __shared__ float parts[32];
+  __shared__ int flag;
+  double loss = 0.0;
+  int live = 0;
+  for (int s = first_sequence(a, t0); s < a.S;) {
+    const int b0 = offset_at(a, s), b1 = offset_at(a, s + 1), lo = max(b0, t0), hi = min(b1, t1);
     if (b0 >= t1) break;
-    if (lo >= hi) continue;
+    if (lo >= hi) {
+      s = next_sequence(a, s, lo);
+      continue;
+    }
     // The next token's logits are on their way while one is worked on (not
     // with 32 values per lane: the registers are wanted for the values).
     constexpr bool kAhead = NV <= 16;
     float x[NV];
     int t = lo + grp;
     if (kAhead && t < hi) load_row<L, NV, VEC, F16>(a, t, l, x);
+    long long i = (long long)lo * a.k + threadIdx.x;
+    const long long end = (long long)hi * a.k;
+    int id = i < end ? a.ids[i] : -1;
     for (int e = threadIdx.x; e < a.E; e += kThreads) cnt[e] = 0;
     __syncthreads();
-    for (long long i = (long long)lo * a.k + threadIdx.x; i < (long long)hi * a.k; i += kThreads) {
-      const int e = a.ids[i];
+    while (i < end) {
+      const int e = id;
+      i += kThreads;
+      id = i < end ? a.ids[i] : -1;
       if (e >= 0 && e < a.E) atomicAdd(&cnt[e], 1);
     }
     float p[NV] = {};
@@ -249,50 +287,104 @@ __global__ void __launch_bounds__(threads_of(NV)) balance_partial_kernel(const B
         for (int v = 0; v < NV; ++v) x[v] = next[v];
     }
 #pragma unroll
-    for (int v = 0; v < NV; ++v) sums[grp][expert_of<L, NV, VEC>(l, v)] = p[v];
+    for (int v = 0; v < NV; ++v) {
+#pragma unroll
+      for (int o = L; o < 32; o <<= 1) p[v] += __shfl_xor_sync(0xffffffffu, p[v], o);
+      if (lane < L) sums[warp][expert_of<L, NV, VEC>(l, v)] = p[v];
+    }
     n = __reduce_add_sync(0xffffffffu, l == 0 ? n : 0);
     if (lane == 0) good[warp] = n;
     __syncthreads();
+    n = __reduce_add_sync(0xffffffffu, lane < kWarps ? good[lane] : 0);
+    const bool whole = a.fused && lo == b0 && hi == b1;
     const size_t row = (size_t)blockIdx.x + s;
-    for (int e = threadIdx.x; e < a.E; e += kThreads) {
+    for (int i = warp; i < blocks; i += kWarps) {
+      const int e = i * 32 + lane;
       float v = 0.0f;
+      if (e < a.E)
 #pragma unroll 8
-      for (int g = 0; g < kGroups; ++g) v += sums[g][e];
-      a.psum[row * a.E + e] = v;
-      a.csum[row * a.E + e] = cnt[e];
-    }
-    if (warp == 0) {
-      const int v = __reduce_add_sync(0xffffffffu, lane < kWarps ? good[lane] : 0);
-      if (lane == 0) a.nsum[row] = v;
-    }
-    __syncthreads();
-  }
-  if (!a.fused) return;
-  __shared__ int flag;
-  __shared__ double dsum[kWarps];
-  if (!last_block(a.ticket, gridDim.x, &flag)) return;
-  // The last block: a warp per sequence and 32 experts.
-  const int blocks = (a.E + 31) / 32;
-  for (int i = warp; i < blocks * a.S; i += kWarps) {
-    const int s = i / blocks, e = (i - s * blocks) * 32 + lane, b0 = offset_at(a, s), b1 = offset_at(a, s + 1);
-    const int c0 = b1 > b0 ? b0 / a.chunk : 0, c1 = b1 > b0 ? (b1 - 1) / a.chunk + 1 : 0;
-    float p = 0.0f;
-    int c = 0, n = 0;
-#pragma unroll 4
-    for (int r = c0; r < c1; ++r) {
-      const size_t row = (size_t)r + s;
-      n += __ldcg(a.nsum + row);
-      if (e < a.E) {
-        p += __ldcg(a.psum + row * a.E + e);
-        c += __ldcg(a.csum + row * a.E + e);
+        for (int w = 0; w < kWarps; ++w) v += sums[w][e];
+      if (whole) {
+        const float part = finish_experts(a, s, e, v, e < a.E ? cnt[e] : 0, n);
+        if (lane == 0) parts[i] = part;
+        if (lane == 0 && !alone) a.lsum[(size_t)s * blocks + i] = part;
+      } else if (e < a.E) {
+        a.psum[row * a.E + e] = v;
+        a.csum[row * a.E + e] = cnt[e];
       }
     }
-    finish_experts(a, s, e, i, p, c, n, lane);
+    if (!whole && threadIdx.x == 0) a.nsum[row] = n;
+    if (a.fused && !whole) {
+      // The last chunk of the sequence to arrive adds the rows: a warp per 32
+      // experts, or several that share the rows.
+      const int c0 = b0 / a.chunk, c1 = (b1 - 1) / a.chunk + 1;
+      if (last_block(a.tickets + c0, (uint32_t)(c1 - c0), &flag)) {
+        const int slices = max(1, kWarps / blocks);
+        for (int i = warp; i < blocks * slices; i += kWarps) {
+          const int e = (i % blocks) * 32 + lane, slice = i / blocks;
+          float q = 0.0f;
+          int c = 0;
+          n = 0;
+#pragma unroll 4
+          for (int r = c0 + slice; r < c1; r += slices) {
+            const size_t at = (size_t)r + s;
+            n += __ldcg(a.nsum + at);
+            if (e < a.E) {
+              q += __ldcg(a.psum + at * a.E + e);
+              c += __ldcg(a.csum + at * a.E + e);
+            }
+          }
+          if (e < a.E) {
+            sums[slice][e] = q;
+            if (slice == 0) cnt[e] = 0;
+          }
+          if (i % blocks == 0 && lane == 0) good[slice] = n;
+          __syncwarp();
+          id = c;  // added below, once every slice 0 has cleared its counts
+          if (slices == 1 && e < a.E) cnt[e] = c;
+        }
+        __syncthreads();
+        if (slices > 1 && warp < blocks * slices) {
+          const int e = (warp % blocks) * 32 + lane;
+          if (e < a.E) atomicAdd(&cnt[e], id);
+        }
+        n = __reduce_add_sync(0xffffffffu, lane < slices ? good[lane] : 0);
+        __syncthreads();
+        for (int i = warp; i < blocks; i += kWarps) {
+          const int e = i * 32 + lane;
+          float v = 0.0f;
+          if (e < a.E)
+            for (int w = 0; w < slices; ++w) v += sums[w][e];
+          const float part = finish_experts(a, s, e, v, e < a.E ? cnt[e] : 0, n);
+          if (lane == 0) a.lsum[(size_t)s * blocks + i] = part;
+        }
+      }
+    }
+    __syncthreads();
+    if (alone && threadIdx.x == 0) {  // the next sequence's parts come after its own barriers
+      for (int i = 0; i < blocks; ++i) loss += parts[i];
+      live += n > 0;
+    }
+    ++s;
   }
-  if (!a.loss) return;
-  __threadfence();
-  __syncthreads();
-  write_loss(a, blocks * a.S, dsum, good);
+  if (!a.fused) return;
+  // The sequences without tokens, a warp for each.
+  for (int s = (int)blockIdx.x * kWarps + warp; s < a.S; s += (int)gridDim.x * kWarps) {
+    if (offset_at(a, s) < offset_at(a, s + 1)) continue;
+    for (int i = 0; i < blocks; ++i) {
+      finish_experts(a, s, i * 32 + lane, 0.0f, 0, 0);
+      if (lane == 0 && !alone) a.lsum[(size_t)s * blocks + i] = 0.0f;
+    }
+  }
+  if (alone) {
+    if (threadIdx.x == 0 && a.loss) a.loss[0] = live ? (float)(loss * (double)a.coef / (double)live) : 0.0f;
+    return;
+  }
+  if (!last_block(a.ticket, gridDim.x, &flag)) return;
+  __shared__ double dsum[kWarps];
+  // Tickets are back at 0 by themselves, unless offsets decreased.
+  for (int c = threadIdx.x; c < a.chunks; c += kThreads) a.tickets[c] = 0;
+  if (a.loss) write_loss(a, blocks * a.S, dsum, good);
 }
 
 // Block (x, s): experts 32 x .. + 31 of sequence s; its warps share the partial rows.
@@ -331,7 +423,8 @@ __global__ void __launch_bounds__(32 * kJoinWarps) balance_join_kernel(const Bal
       c += cs[w][lane];
       n += ns[w];
     }
-    finish_experts(a, s, e, s * (int)gridDim.x + (int)blockIdx.x, p, c, n, lane);
+    const float part = finish_experts(a, s, e, p, c, n);
+    if (lane == 0 && a.loss) a.lsum[s * (int)gridDim.x + (int)blockIdx.x] = part;
   }
   if (!a.loss || !last_block(a.ticket, gridDim.x * gridDim.y, &flag)) return;
   write_loss(a, (int)(gridDim.x * gridDim.y), dsum, ns);
@@ -352,10 +445,13 @@ __global__ void __launch_bounds__(threads_of(NV)) balance_back_kernel(const Bala
     live += __syncthreads_count(j < a.S && a.btokens[j] > 0);
   }
   const float g = a.coef * (a.grad ? *a.grad : 1.0f);
-  for (int s = first_sequence(a, t0); s < a.S; ++s) {
+  for (int s = first_sequence(a, t0); s < a.S;) {
     const int b0 = offset_at(a, s), lo = max(b0, t0), hi = min(offset_at(a, s + 1), t1);
     if (b0 >= t1) break;
-    if (lo >= hi) continue;
+    if (lo >= hi) {
+      s = next_sequence(a, s, lo);
+      continue;
+    }
     constexpr bool kAhead = NV <= 16;
     float x[NV], f[NV];
     int t = lo + grp;
@@ -409,17 +505,20 @@ __global__ void __launch_bounds__(threads_of(NV)) balance_back_kernel(const Bala
 #pragma unroll
         for (int v = 0; v < NV; ++v) x[v] = next[v];
     }
+    ++s;
   }
 }
 
 struct Ws {
-  size_t psum, csum, nsum, lsum, total;
+  size_t psum, csum, nsum, lsum, tickets, total;
 };
 Ws ws_of(int T, int E, int S) {
   const size_t rows = (size_t)std::min((T + kMinChunk - 1) / kMinChunk, max_chunks(E)) + S;
   auto up = [](size_t b) { return (b + 255) / 256 * 256; };
   Ws w;
   size_t o = kWorkspaceHeader;
+  // In the same place for every T, E and S: they have to stay zero between calls.
+  w.tickets = o; o += up(max_chunks(1024) * 4);
   w.psum = o; o += up(rows * E * 4);
   w.csum = o; o += up(rows * E * 4);
   w.nsum = o; o += up(rows * 4);
@@ -472,10 +571,15 @@ int check_balance(const char* who, const moe_balance_cfg* c, const void* logits,
   return MOE_OK;
 }
 
-void set_chunks(BalanceArgs& a) {
+void set_chunks(BalanceArgs& a, bool back) {
   const int most = max_chunks(a.E);
   a.chunk = std::max(kMinChunk, (a.T + most - 1) / most);
-  a.chunks = (a.T + a.chunk - 1) / a.chunk;
+  if (!back && a.S <= kAloneSequences) {
+    const int groups = threads_of(a.E <= 256 ? 8 : a.E <= 512 ? 16 : 32) / (a.E <= 64 ? 8 : a.E <= 128 ? 16 : 32);
+    if (a.T <= kAloneRounds * groups) a.chunk = kAloneRounds * groups;
+  }
+  a.chunks = std::max(1, (a.T + a.chunk - 1) / a.chunk);
+  a.fused = a.chunks * a.E <= kFusedRows;
 }
 
 struct Launch {
@@ -523,8 +627,7 @@ int moe_balance_loss(const moe_balance_cfg* cfg, const void* logits, int logit_t
   a.logits = logits;
   a.ld = ld;
   a.T = T; a.E = E; a.k = k; a.S = S;
-  moe::set_chunks(a);
-  a.fused = T > 0 && a.chunks <= moe::kFusedChunks && (long long)S * E <= moe::kFusedOutputs;
+  moe::set_chunks(a, false);
   a.sigmoid = cfg->score == MOE_SCORE_SIGMOID;
   a.coef = cfg->coef;
   a.ids = ids;
@@ -534,13 +637,14 @@ int moe_balance_loss(const moe_balance_cfg* cfg, const void* logits, int logit_t
   a.nsum = reinterpret_cast<int32_t*>(w8 + w.nsum);
   a.lsum = reinterpret_cast<float*>(w8 + w.lsum);
   a.ticket = reinterpret_cast<uint32_t*>(w8) + 1;
+  a.tickets = reinterpret_cast<uint32_t*>(w8 + w.tickets);
   a.counts = counts;
   a.tokens = tokens;
   a.mean = mean;
   a.loss = loss;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   cudaError_t e = cudaSuccess;
-  if (T > 0) {
+  {
     const moe::Launch l(dim3((unsigned)a.chunks), 0, st);
     e = moe::launch_tokens<false>(l.cfg, a, logit_type);
   }
@@ -571,7 +675,7 @@ int moe_balance_loss_backward(const moe_balance_cfg* cfg, const void* logits, in
   a.logits = logits;
   a.ld = ld;
   a.T = T; a.E = E; a.k = k; a.S = S;
-  moe::set_chunks(a);
+  moe::set_chunks(a, true);
   a.vec_out = reinterpret_cast<uintptr_t>(dlogits) % 16 == 0 && ldd % 4 == 0;
   a.sigmoid = cfg->score == MOE_SCORE_SIGMOID;
   a.coef = cfg->coef;

@@ -314,3 +314,24 @@ def test_refusals():
         moe.moe_balance_loss_backward(cfg, lg, k, None, b.counts, b.tokens, None, torch.zeros((T, E + 1), device="cuda"))
     with pytest.raises(moe.MoeError):
         moe.moe_balance_loss_backward(cfg, lg, 17, None, b.counts, b.tokens, None, torch.zeros((T, E), device="cuda"))
+
+
+@pytest.mark.parametrize("T,E,k,S", [(3000, 8, 2, 4), (9000, 64, 4, 40), (6000, 130, 4, 3), (20000, 256, 8, 1), (20000, 256, 2, 500),
+                                     (3000, 300, 3, 2), (2500, 1000, 2, 6)])
+def test_sequences_over_many_chunks_and_one_workspace_for_all(T, E, k, S):
+    # Long sequences that many blocks share, short ones within a block; the workspace serves calls of other
+    # sizes in between, whose layout differs.
+    l, ids, off = _inputs(T, E, k, S)
+    cfg, b = moe.moe_balance_config("sigmoid", 0.01), Buffers(20000, 1024, 500)
+    other = Buffers(1, 1024, 500)
+    other.work = b.work
+    small = _inputs(300, 1024, 2, 500, seed=1)
+    b.counts, b.tokens, b.mean = b.counts[:S, :E].contiguous(), b.tokens[:S], b.mean[:S, :E].contiguous()
+    args = _cuda(l), _cuda(ids), _cuda(off)
+    b.forward(cfg, *args)
+    _check_forward(b, l, ids, off, k, "sigmoid", 0.01)
+    want = [t.clone() for t in (b.counts, b.tokens, b.mean, b.loss)]
+    other.forward(cfg, *[_cuda(v) for v in small])
+    _check_forward(other, *small, 2, "sigmoid", 0.01)
+    b.forward(cfg, *args)
+    assert all(torch.equal(x, y) for x, y in zip((b.counts, b.tokens, b.mean, b.loss), want))
