@@ -30,9 +30,10 @@ constexpr int kMinChunk = 32;  // tokens
 // and chunks at most: what fills 152 SMs once.
 constexpr int threads_of(int nv) { return nv == 8 ? 1024 : nv == 16 ? 512 : 256; }
 constexpr int max_chunks(int E) { return E > 512 ? 304 : 152; }  // not decreasing in E
-// A batch of up to 8 rounds of a block's tokens and 16 sequences is one chunk,
-// and so one block: 256 tokens of 64 experts 6.0 us, in eight chunks 11.9.
-constexpr int kAloneRounds = 8;
+// A batch of up to 3 rounds of a block's tokens and 16 sequences is one chunk,
+// and so one block: 256 tokens of 64 experts 6.1 us, in eight chunks 11.9; eight
+// rounds (256 of 256 experts) take about what the chunks take.
+constexpr int kAloneRounds = 3;
 constexpr int kAloneSequences = 16;
 constexpr int kFusedRows = 40960;  // chunks times experts that one launch joins
 
@@ -40,10 +41,11 @@ struct BalanceArgs {
   const void* logits;
   long long ld;
   int T, E, k, S, chunk, chunks;
+  int pitch;  // of the partial rows: E rounded up to 4
   bool sigmoid;
   float coef;
   const int32_t *ids, *offsets;
-  float* psum;      // partial rows [chunks + S][E]: probabilities,
+  float* psum;      // partial rows [chunks + S][pitch]: probabilities,
   int32_t* csum;    // counts,
   int32_t* nsum;    // [chunks + S]: good tokens
   float* lsum;      // [S][ceil(E / 32)]
@@ -64,6 +66,21 @@ __device__ __forceinline__ int offset_at(const BalanceArgs& a, int i) {
   if (!a.offsets) return i ? a.T : 0;
   return min(max(a.offsets[i], 0), a.T);
 }
+// The offsets, in shared memory where they fit: they are looked at some five
+// times, and a load from memory takes 0.6 us each time. Whole block, before the
+// first look.
+constexpr int kLocalOffsets = 1024;
+struct Offsets {
+  const BalanceArgs& a;
+  const int32_t* local;
+  __device__ __forceinline__ Offsets(const BalanceArgs& a, int32_t* sm) : a(a), local(a.S < kLocalOffsets ? sm : nullptr) {
+    if (local) {
+      for (int i = threadIdx.x; i <= a.S; i += blockDim.x) sm[i] = offset_at(a, i);
+      __syncthreads();
+    }
+  }
+  __device__ __forceinline__ int operator()(int i) const { return local ? local[i] : offset_at(a, i); }
+};
 
 // Lane l of a group of L holds NV experts: VEC = 4: 4 (l + L j) + i, VEC = 1: l + L j.
 template <int L, int NV, int VEC>
@@ -167,11 +184,11 @@ __device__ __forceinline__ float probabilities(float (&x)[NV], float (&rest)[NV]
 
 // The first sequence with tokens from t0 on that can hold t0: offsets at or
 // below t0, less one. Whole block.
-__device__ __forceinline__ int first_sequence(const BalanceArgs& a, int t0) {
+__device__ __forceinline__ int first_sequence(const BalanceArgs& a, const Offsets& off, int t0) {
   int n = 0;
   for (int i = 0; i <= a.S; i += blockDim.x) {
     const int j = i + (int)threadIdx.x;
-    n += __syncthreads_count(j <= a.S && offset_at(a, j) <= t0);
+    n += __syncthreads_count(j <= a.S && off(j) <= t0);
   }
   return max(n - 1, 0);
 }
@@ -188,203 +205,322 @@ __device__ __forceinline__ float finish_experts(const BalanceArgs& a, int s, int
   return warp_sum(e < a.E && n ? (float)c * ((float)a.E / ((float)a.k * (float)n)) * mean : 0.0f);
 }
 
-// The losses' sum over coef and the sequences that count; whole block, in a
-// fixed order. parts: n of them.
-__device__ __forceinline__ void write_loss(const BalanceArgs& a, int n, double* sums, int* live) {
-  double v = 0.0;
+// The mean of n sequences' losses from their parts; whole block, in a fixed
+// order. FP32: all terms are positive, and one FP64 division alone takes longer
+// than the sum (3 us with FP64 sums).
+__device__ __forceinline__ void write_loss(const BalanceArgs& a, int n, float* sums, int* live) {
+  float v = 0.0f;
   int c = 0;
-  for (int i = threadIdx.x; i < n; i += blockDim.x) v += (double)__ldcg(a.lsum + i);
+  for (int i = threadIdx.x; i < n; i += blockDim.x) v += __ldcg(a.lsum + i);
   for (int i = threadIdx.x; i < a.S; i += blockDim.x) c += __ldcg(a.tokens + i) > 0;
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  v = warp_sum(v);
   c = __reduce_add_sync(0xffffffffu, c);
-  if ((threadIdx.x & 31) == 0) {
+  const int lane = threadIdx.x & 31, warps = blockDim.x / 32;
+  if (lane == 0) {
     sums[threadIdx.x >> 5] = v;
     live[threadIdx.x >> 5] = c;
   }
   __syncthreads();
-  if (threadIdx.x == 0) {
-    for (int i = 1; i < (int)blockDim.x / 32; ++i) {
-      v += sums[i];
-      c += live[i];
-    }
-    a.loss[0] = c ? (float)(v * (double)a.coef / (double)c) : 0.0f;
+  if (threadIdx.x < 32) {
+    v = warp_sum(lane < warps ? sums[lane] : 0.0f);
+    c = __reduce_add_sync(0xffffffffu, lane < warps ? live[lane] : 0);
+    if (lane == 0) a.loss[0] = c ? v * a.coef / (float)c : 0.0f;
   }
 }
 // Whole block: true in the last one of `total` to call; the others' writes are
 // then visible.
 __device__ __forceinline__ bool last_block(uint32_t* ticket, uint32_t total, int* flag) {
-  __threadfence();
   __syncthreads();
-  if (threadIdx.x == 0) *flag = atomicInc(ticket, total - 1) == total - 1;  // back to 0 with the last
+  if (threadIdx.x == 0) {  // its fences stand for the block's: the barriers order the others' accesses with them
+    __threadfence();
+    *flag = atomicInc(ticket, total - 1) == total - 1;  // back to 0 with the last
+    __threadfence();
+  }
   __syncthreads();
-  const bool last = *flag;
-  if (last) __threadfence();
-  return last;
+  return *flag;
 }
 
 // The sequence to go on with after the empty sequence s at token t: past all
 // empty ones there. Whole block.
-__device__ __forceinline__ int next_sequence(const BalanceArgs& a, int s, int t) {
-  return max(s + 1, first_sequence(a, t));
+__device__ __forceinline__ int next_sequence(const BalanceArgs& a, const Offsets& off, int s, int t) {
+  return max(s + 1, first_sequence(a, off, t));
+}
+
+// The partial rows of sequence s, all of them written, added in order and
+// finished. A thread takes four experts of every slices-th row, four rows' loads
+// in flight (one after the other they took 1 us each). Whole block; sums (of
+// 8 * kThreads values at least), good: scratch.
+template <int kThreads, int kGroups>
+__device__ __forceinline__ void join_rows(const BalanceArgs& a, const Offsets& off, int s, int blocks, float* sums,
+                                          int32_t* good) {
+  const int quads = a.pitch / 4, slices = min(kThreads / quads, kGroups);
+  const int slice = (int)threadIdx.x / quads, e0 = 4 * ((int)threadIdx.x - slice * quads);
+  const int c0 = off(s) / a.chunk, c1 = (off(s + 1) - 1) / a.chunk + 1;
+  int32_t* counts = reinterpret_cast<int32_t*>(sums + 4 * kThreads);
+  if (slice < slices) {
+    float4 p = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    int4 c = make_int4(0, 0, 0, 0);
+    int n = 0;
+    for (int r = c0 + slice; r < c1; r += 4 * slices) {
+      float4 q[4];
+      int4 d[4];
+      int k[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const size_t row = (size_t)(r + u * slices) + s;
+        q[u] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        d[u] = make_int4(0, 0, 0, 0);
+        k[u] = 0;
+        if (r + u * slices < c1) {
+          q[u] = __ldcg(reinterpret_cast<const float4*>(a.psum + row * a.pitch + e0));
+          d[u] = __ldcg(reinterpret_cast<const int4*>(a.csum + row * a.pitch + e0));
+          if (e0 == 0) k[u] = __ldcg(a.nsum + row);
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        p.x += q[u].x; p.y += q[u].y; p.z += q[u].z; p.w += q[u].w;
+        c.x += d[u].x; c.y += d[u].y; c.z += d[u].z; c.w += d[u].w;
+        n += k[u];
+      }
+    }
+    *reinterpret_cast<float4*>(sums + slice * a.pitch + e0) = p;
+    *reinterpret_cast<int4*>(counts + slice * a.pitch + e0) = c;
+    if (e0 == 0) good[slice] = n;
+  }
+  __syncthreads();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  int n = 0;
+  for (int w = lane; w < slices; w += 32) n += good[w];
+  n = __reduce_add_sync(0xffffffffu, n);
+  for (int i = warp; i < blocks; i += kThreads / 32) {
+    const int e = i * 32 + lane;
+    float v = 0.0f;
+    int c = 0;
+    if (e < a.E)
+#pragma unroll 8
+      for (int w = 0; w < slices; ++w) {
+        v += sums[w * a.pitch + e];
+        c += counts[w * a.pitch + e];
+      }
+    const float part = finish_experts(a, s, e, v, c, n);
+    if (lane == 0) a.lsum[(size_t)s * blocks + i] = part;
+  }
+  __syncthreads();
+}
+
+// A pass of a block: up to M sequences that follow one another in its chunk.
+template <int M>
+struct Pass {
+  int seq[M], lo[M], hi[M];  // and their tokens within the chunk
+  int m;                     // how many
+  int next;                  // sequence to go on with, S at the chunk's end
+};
+// From sequence s on, those with tokens below t1. Warp 0. Offsets that decrease
+// are taken as their running maximum, so that the sequences of a pass always
+// follow one another.
+template <int M>
+__device__ __forceinline__ void find_pass(const BalanceArgs& a, const Offsets& off, int s, int t0, int t1, Pass<M>& pass) {
+  const unsigned full = 0xffffffffu;
+  const int lane = threadIdx.x & 31;
+  int m = 0, next = a.S, start = max(off(s), t0);
+  for (; s < a.S; s += 32) {
+    int hi = off(min(s + lane + 1, a.S));
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(full, hi, o);
+      if (lane >= o) hi = max(hi, v);
+    }
+    hi = max(hi, start);
+    const int before = __shfl_up_sync(full, hi, 1), lo = lane ? before : start;
+    const bool in = s + lane < a.S && lo < min(hi, t1);
+    const unsigned some = __ballot_sync(full, in);
+    const int at = m + __popc(some & ((1u << lane) - 1u));
+    if (in && at < M) {
+      pass.seq[at] = s + lane;
+      pass.lo[at] = lo;
+      pass.hi[at] = min(hi, t1);
+    }
+    const unsigned over = __ballot_sync(full, in && at == M);  // the first that does not fit
+    if (over) {
+      m = M;
+      next = s + __ffs(over) - 1;
+      break;
+    }
+    m += __popc(some);
+    start = __shfl_sync(full, hi, 31);
+    if (start >= t1) break;
+    if (m && !some) {  // a run of empty sequences: the next pass jumps over it
+      next = s + 32;
+      break;
+    }
+  }
+  if (lane == 0) {
+    pass.m = m;
+    pass.next = min(next, a.S);
+  }
 }
 
 template <int L, int NV, int VEC, bool F16>
 __global__ void __launch_bounds__(threads_of(NV)) balance_partial_kernel(const BalanceArgs a) {
   constexpr int kThreads = threads_of(NV), kWarps = kThreads / 32;
-  constexpr int G = 32 / L, kGroups = kWarps * G;  // groups per warp, per block
-  __shared__ float sums[kWarps][L * NV];
-  __shared__ int32_t cnt[L * NV];
-  __shared__ int32_t good[kWarps];
+  constexpr int kGroups = kWarps * (32 / L);  // in a block
+  constexpr int kE = L * NV, M = 1024 / kE;   // experts at most, sequences of a pass
+  // Rows group + sequence, as the partial rows in memory.
+  __shared__ __align__(16) float sums[(kGroups + M) * kE];
+  static_assert((kGroups + M) * kE >= 8 * kThreads, "scratch of the joining");
+  __shared__ int32_t good[kGroups + M], cnt[M * kE];
+  __shared__ float parts[32];
+  __shared__ int32_t count[M], flags[2];
+  __shared__ Pass<M> pass;
+  __shared__ int32_t offs[kLocalOffsets];
   griddep_wait();
   griddep_launch_dependents();
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, l = lane & (L - 1), grp = warp * G + lane / L;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, l = lane & (L - 1), grp = (int)threadIdx.x / L;
   const unsigned mask = L == 32 ? 0xffffffffu : ((1u << L) - 1u) << (lane & ~(L - 1));
   const int t0 = blockIdx.x * a.chunk, t1 = min(a.T, t0 + a.chunk), blocks = (a.E + 31) / 32;
   const bool alone = gridDim.x == 1;
-  __shared__ float parts[32];
-  __shared__ int flag;
-  double loss = 0.0;
+  const Offsets off(a, offs);
+  float loss = 0.0f;
   int live = 0;
-  for (int s = first_sequence(a, t0); s < a.S;) {
-    const int b0 = offset_at(a, s), b1 = offset_at(a, s + 1), lo = max(b0, t0), hi = min(b1, t1);
-    if (b0 >= t1) break;
-    if (lo >= hi) {
-      s = next_sequence(a, s, lo);
-      continue;
-    }
-    // The next token's logits are on their way while one is worked on (not
-    // with 32 values per lane: the registers are wanted for the values).
+  for (int s0 = t0 < t1 ? first_sequence(a, off, t0) : a.S; s0 < a.S;) {
+    if (warp == 0) find_pass<M>(a, off, s0, t0, t1, pass);
+    for (int e = threadIdx.x; e < M * kE; e += kThreads) cnt[e] = 0;
+    __syncthreads();
+    const int m = pass.m;
+    if (m == 0) break;
+    const int p0 = pass.lo[0], p1 = pass.hi[m - 1];
+    // Group g takes tokens from p0 + g per on; the next token's logits and
+    // first picks are on their way while one is worked on (not with 32 values
+    // per lane: the registers are wanted for the values).
+    const int per = (p1 - p0 + kGroups - 1) / kGroups;
+    int t = p0 + grp * per;
+    const int end = min(p1, t + per);
     constexpr bool kAhead = NV <= 16;
-    float x[NV];
-    int t = lo + grp;
-    if (kAhead && t < hi) load_row<L, NV, VEC, F16>(a, t, l, x);
-    long long i = (long long)lo * a.k + threadIdx.x;
-    const long long end = (long long)hi * a.k;
-    int id = i < end ? a.ids[i] : -1;
-    for (int e = threadIdx.x; e < a.E; e += kThreads) cnt[e] = 0;
-    __syncthreads();
-    while (i < end) {
-      const int e = id;
-      i += kThreads;
-      id = i < end ? a.ids[i] : -1;
-      if (e >= 0 && e < a.E) atomicAdd(&cnt[e], 1);
-    }
-    float p[NV] = {};
-    int n = 0;
-    for (; t < hi; t += kGroups) {
-      float next[NV], rest[NV];
-      if (!kAhead) load_row<L, NV, VEC, F16>(a, t, l, x);
-      if (kAhead && t + kGroups < hi) load_row<L, NV, VEC, F16>(a, t + kGroups, l, next);
-      const float inv = probabilities<L, NV, false>(x, rest, a.sigmoid, mask);
-      if (inv > 0.0f) {
-        ++n;
-#pragma unroll
-        for (int v = 0; v < NV; ++v) p[v] = fmaf(x[v], inv, p[v]);
+    float x[NV], p[NV] = {};
+    int id = -1, n = 0, j = 0;
+    if (t < end) {
+      if (kAhead) {
+        load_row<L, NV, VEC, F16>(a, t, l, x);
+        if (l < a.k) id = a.ids[(size_t)t * a.k + l];
       }
-      if (kAhead)
+      while (t >= pass.hi[j]) ++j;
+      for (;;) {
+        float next[NV], rest[NV];
+        int next_id = -1;
+        if (!kAhead) {
+          load_row<L, NV, VEC, F16>(a, t, l, x);
+          if (l < a.k) id = a.ids[(size_t)t * a.k + l];
+        } else if (t + 1 < end) {
+          load_row<L, NV, VEC, F16>(a, t + 1, l, next);
+          if (l < a.k) next_id = a.ids[(size_t)(t + 1) * a.k + l];
+        }
+        const float inv = probabilities<L, NV, false>(x, rest, a.sigmoid, mask);
+        if (inv > 0.0f) {
+          ++n;
 #pragma unroll
-        for (int v = 0; v < NV; ++v) x[v] = next[v];
+          for (int v = 0; v < NV; ++v) p[v] = fmaf(x[v], inv, p[v]);
+        }
+        if (id >= 0 && id < a.E) atomicAdd(&cnt[j * kE + id], 1);
+        for (int q = l + L; q < a.k; q += L) {
+          id = a.ids[(size_t)t * a.k + q];
+          if (id >= 0 && id < a.E) atomicAdd(&cnt[j * kE + id], 1);
+        }
+        ++t;
+        if (t == end || t == pass.hi[j]) {
+#pragma unroll
+          for (int v = 0; v < NV; ++v) {
+            sums[(grp + j) * kE + expert_of<L, NV, VEC>(l, v)] = p[v];
+            p[v] = 0.0f;
+          }
+          if (l == 0) good[grp + j] = n;
+          n = 0;
+          ++j;
+          if (t == end) break;
+        }
+        if (kAhead) {
+#pragma unroll
+          for (int v = 0; v < NV; ++v) x[v] = next[v];
+          id = next_id;
+        }
+      }
     }
-#pragma unroll
-    for (int v = 0; v < NV; ++v) {
-#pragma unroll
-      for (int o = L; o < 32; o <<= 1) p[v] += __shfl_xor_sync(0xffffffffu, p[v], o);
-      if (lane < L) sums[warp][expert_of<L, NV, VEC>(l, v)] = p[v];
-    }
-    n = __reduce_add_sync(0xffffffffu, l == 0 ? n : 0);
-    if (lane == 0) good[warp] = n;
     __syncthreads();
-    n = __reduce_add_sync(0xffffffffu, lane < kWarps ? good[lane] : 0);
-    const bool whole = a.fused && lo == b0 && hi == b1;
-    const size_t row = (size_t)blockIdx.x + s;
-    for (int i = warp; i < blocks; i += kWarps) {
-      const int e = i * 32 + lane;
+    // A warp per sequence and 32 experts.
+    for (int i = warp; i < m * blocks; i += kWarps) {
+      const int q = i / blocks, e = (i - q * blocks) * 32 + lane, s = pass.seq[q], lo = pass.lo[q], hi = pass.hi[q];
+      const int g0 = (lo - p0) / per, g1 = (hi - 1 - p0) / per;
+      int c = 0;
+      for (int g = g0 + lane; g <= g1; g += 32) c += good[g + q];
+      c = __reduce_add_sync(0xffffffffu, c);
       float v = 0.0f;
       if (e < a.E)
 #pragma unroll 8
-        for (int w = 0; w < kWarps; ++w) v += sums[w][e];
-      if (whole) {
-        const float part = finish_experts(a, s, e, v, e < a.E ? cnt[e] : 0, n);
-        if (lane == 0) parts[i] = part;
-        if (lane == 0 && !alone) a.lsum[(size_t)s * blocks + i] = part;
+        for (int g = g0; g <= g1; ++g) v += sums[(g + q) * kE + e];
+      const size_t row = (size_t)blockIdx.x + s;
+      if (a.fused && lo == off(s) && hi == off(s + 1)) {
+        const float part = finish_experts(a, s, e, v, e < a.E ? cnt[q * kE + e] : 0, c);
+        if (lane == 0) {
+          parts[i] = part;
+          if (!alone) a.lsum[(size_t)s * blocks + (i - q * blocks)] = part;
+        }
       } else if (e < a.E) {
-        a.psum[row * a.E + e] = v;
-        a.csum[row * a.E + e] = cnt[e];
+        a.psum[row * a.pitch + e] = v;
+        a.csum[row * a.pitch + e] = cnt[q * kE + e];
+        if (e == 0) a.nsum[row] = c;
       }
+      if (e == 0) count[q] = c;
     }
-    if (!whole && threadIdx.x == 0) a.nsum[row] = n;
-    if (a.fused && !whole) {
-      // The last chunk of the sequence to arrive adds the rows: a warp per 32
-      // experts, or several that share the rows.
-      const int c0 = b0 / a.chunk, c1 = (b1 - 1) / a.chunk + 1;
-      if (last_block(a.tickets + c0, (uint32_t)(c1 - c0), &flag)) {
-        const int slices = max(1, kWarps / blocks);
-        for (int i = warp; i < blocks * slices; i += kWarps) {
-          const int e = (i % blocks) * 32 + lane, slice = i / blocks;
-          float q = 0.0f;
-          int c = 0;
-          n = 0;
-#pragma unroll 4
-          for (int r = c0 + slice; r < c1; r += slices) {
-            const size_t at = (size_t)r + s;
-            n += __ldcg(a.nsum + at);
-            if (e < a.E) {
-              q += __ldcg(a.psum + at * a.E + e);
-              c += __ldcg(a.csum + at * a.E + e);
-            }
-          }
-          if (e < a.E) {
-            sums[slice][e] = q;
-            if (slice == 0) cnt[e] = 0;
-          }
-          if (i % blocks == 0 && lane == 0) good[slice] = n;
-          __syncwarp();
-          id = c;  // added below, once every slice 0 has cleared its counts
-          if (slices == 1 && e < a.E) cnt[e] = c;
+    if (alone) {
+      __syncthreads();
+      if (warp == 0) {
+        loss += warp_sum(lane < m * blocks ? parts[lane] : 0.0f);
+        live += __reduce_add_sync(0xffffffffu, lane < m && count[lane < m ? lane : 0] > 0 ? 1 : 0);
+      }
+    } else if (a.fused) {
+      // Sequences that other chunks share are the pass's first or last. The
+      // last chunk of a sequence to arrive adds its rows.
+      int c0 = 0, c1 = 0;
+      bool shared = false;
+      if (threadIdx.x < 2 && (threadIdx.x == 0 || m > 1)) {
+        const int q = threadIdx.x == 0 ? 0 : m - 1, s = pass.seq[q], b0 = off(s), b1 = off(s + 1);
+        shared = pass.lo[q] != b0 || pass.hi[q] != b1;
+        c0 = b0 / a.chunk;
+        c1 = (b1 - 1) / a.chunk + 1;
+      }
+      if (__syncthreads_or(shared)) {
+        if (threadIdx.x < 2) {
+          const uint32_t total = (uint32_t)(c1 - c0);
+          __threadfence();
+          flags[threadIdx.x] = shared && atomicInc(a.tickets + c0, total - 1) == total - 1;  // back to 0 with the last
+          __threadfence();
         }
         __syncthreads();
-        if (slices > 1 && warp < blocks * slices) {
-          const int e = (warp % blocks) * 32 + lane;
-          if (e < a.E) atomicAdd(&cnt[e], id);
-        }
-        n = __reduce_add_sync(0xffffffffu, lane < slices ? good[lane] : 0);
-        __syncthreads();
-        for (int i = warp; i < blocks; i += kWarps) {
-          const int e = i * 32 + lane;
-          float v = 0.0f;
-          if (e < a.E)
-            for (int w = 0; w < slices; ++w) v += sums[w][e];
-          const float part = finish_experts(a, s, e, v, e < a.E ? cnt[e] : 0, n);
-          if (lane == 0) a.lsum[(size_t)s * blocks + i] = part;
-        }
+        for (int w = 0; w < 2; ++w)
+          if (flags[w]) join_rows<kThreads, kGroups>(a, off, pass.seq[w ? m - 1 : 0], blocks, sums, good);
       }
     }
+    const int from = pass.next;
+    s0 = m == M || from == a.S ? from : max(from, first_sequence(a, off, p1));
     __syncthreads();
-    if (alone && threadIdx.x == 0) {  // the next sequence's parts come after its own barriers
-      for (int i = 0; i < blocks; ++i) loss += parts[i];
-      live += n > 0;
-    }
-    ++s;
   }
   if (!a.fused) return;
   // The sequences without tokens, a warp for each.
   for (int s = (int)blockIdx.x * kWarps + warp; s < a.S; s += (int)gridDim.x * kWarps) {
-    if (offset_at(a, s) < offset_at(a, s + 1)) continue;
+    if (off(s) < off(s + 1)) continue;
     for (int i = 0; i < blocks; ++i) {
       finish_experts(a, s, i * 32 + lane, 0.0f, 0, 0);
       if (lane == 0 && !alone) a.lsum[(size_t)s * blocks + i] = 0.0f;
     }
   }
   if (alone) {
-    if (threadIdx.x == 0 && a.loss) a.loss[0] = live ? (float)(loss * (double)a.coef / (double)live) : 0.0f;
+    if (threadIdx.x == 0 && a.loss) a.loss[0] = live ? loss * a.coef / (float)live : 0.0f;
     return;
   }
-  if (!last_block(a.ticket, gridDim.x, &flag)) return;
-  __shared__ double dsum[kWarps];
+  if (!last_block(a.ticket, gridDim.x, &flags[0])) return;
   // Tickets are back at 0 by themselves, unless offsets decreased.
   for (int c = threadIdx.x; c < a.chunks; c += kThreads) a.tickets[c] = 0;
-  if (a.loss) write_loss(a, blocks * a.S, dsum, good);
+  if (a.loss) write_loss(a, blocks * a.S, parts, good);
 }
 
 // Block (x, s): experts 32 x .. + 31 of sequence s; its warps share the partial rows.
@@ -392,7 +528,7 @@ constexpr int kJoinWarps = 16;
 __global__ void __launch_bounds__(32 * kJoinWarps) balance_join_kernel(const BalanceArgs a) {
   __shared__ float ps[kJoinWarps][32];
   __shared__ int32_t cs[kJoinWarps][32], ns[kJoinWarps];
-  __shared__ double dsum[kJoinWarps];
+  __shared__ float dsum[kJoinWarps];
   __shared__ int flag;
   griddep_wait();
   griddep_launch_dependents();
@@ -401,13 +537,22 @@ __global__ void __launch_bounds__(32 * kJoinWarps) balance_join_kernel(const Bal
   const int c0 = hi > lo ? lo / a.chunk : 0, c1 = hi > lo ? (hi - 1) / a.chunk + 1 : 0;
   float p = 0.0f;
   int c = 0, n = 0;
-#pragma unroll 4
-  for (int r = c0 + warp; r < c1; r += kJoinWarps) {
-    const size_t row = (size_t)r + s;
-    n += a.nsum[row];
-    if (e < a.E) {
-      p += a.psum[row * a.E + e];
-      c += a.csum[row * a.E + e];
+  for (int r = c0 + warp; r < c1; r += 8 * kJoinWarps) {
+    float q[8];
+    int d[8], k[8];
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+      const size_t row = (size_t)(r + u * kJoinWarps) + s;
+      const bool in = r + u * kJoinWarps < c1;
+      q[u] = in && e < a.E ? a.psum[row * a.pitch + e] : 0.0f;
+      d[u] = in && e < a.E ? a.csum[row * a.pitch + e] : 0;
+      k[u] = in ? a.nsum[row] : 0;
+    }
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+      p += q[u];
+      c += d[u];
+      n += k[u];
     }
   }
   ps[warp][lane] = p;
@@ -434,8 +579,10 @@ template <int L, int NV, int VEC, bool F16>
 __global__ void __launch_bounds__(threads_of(NV)) balance_back_kernel(const BalanceArgs a) {
   constexpr int kThreads = threads_of(NV);
   constexpr int G = 32 / L, kGroups = kThreads / 32 * G;
+  __shared__ int32_t offs[kLocalOffsets];
   griddep_wait();
   griddep_launch_dependents();
+  const Offsets off(a, offs);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, l = lane & (L - 1), grp = warp * G + lane / L;
   const unsigned mask = L == 32 ? 0xffffffffu : ((1u << L) - 1u) << (lane & ~(L - 1));
   const int t0 = blockIdx.x * a.chunk, t1 = min(a.T, t0 + a.chunk);
@@ -445,11 +592,11 @@ __global__ void __launch_bounds__(threads_of(NV)) balance_back_kernel(const Bala
     live += __syncthreads_count(j < a.S && a.btokens[j] > 0);
   }
   const float g = a.coef * (a.grad ? *a.grad : 1.0f);
-  for (int s = first_sequence(a, t0); s < a.S;) {
-    const int b0 = offset_at(a, s), lo = max(b0, t0), hi = min(offset_at(a, s + 1), t1);
+  for (int s = first_sequence(a, off, t0); s < a.S;) {
+    const int b0 = off(s), lo = max(b0, t0), hi = min(off(s + 1), t1);
     if (b0 >= t1) break;
     if (lo >= hi) {
-      s = next_sequence(a, s, lo);
+      s = next_sequence(a, off, s, lo);
       continue;
     }
     constexpr bool kAhead = NV <= 16;
@@ -519,8 +666,9 @@ Ws ws_of(int T, int E, int S) {
   size_t o = kWorkspaceHeader;
   // In the same place for every T, E and S: they have to stay zero between calls.
   w.tickets = o; o += up(max_chunks(1024) * 4);
-  w.psum = o; o += up(rows * E * 4);
-  w.csum = o; o += up(rows * E * 4);
+  const size_t pitch = (size_t)(E + 3) / 4 * 4;
+  w.psum = o; o += up(rows * pitch * 4);
+  w.csum = o; o += up(rows * pitch * 4);
   w.nsum = o; o += up(rows * 4);
   w.lsum = o; o += up((size_t)S * ((E + 31) / 32) * 4);
   w.total = o;
@@ -627,6 +775,7 @@ int moe_balance_loss(const moe_balance_cfg* cfg, const void* logits, int logit_t
   a.logits = logits;
   a.ld = ld;
   a.T = T; a.E = E; a.k = k; a.S = S;
+  a.pitch = (E + 3) / 4 * 4;
   moe::set_chunks(a, false);
   a.sigmoid = cfg->score == MOE_SCORE_SIGMOID;
   a.coef = cfg->coef;
