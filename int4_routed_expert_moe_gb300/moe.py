@@ -573,20 +573,14 @@ def moe_norm_config(kind: str = "rms", eps: float = 1e-6, weight_offset: float =
     return moe_norm_cfg(_NORMS[kind], float(eps), float(weight_offset))
 
 
-def _stream_rows(x, name: str) -> tuple:
-    """(pointer, type, T, H) of a residual stream: float16 or float32 [T][H]."""
-    if not isinstance(x, torch.Tensor):
+def _stream_type(t, name: str) -> int:
+    """MOE_F16 or MOE_F32 of a residual stream."""
+    if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a CUDA tensor")
-    kind = _LOGIT_TYPES.get(x.dtype)
+    kind = _LOGIT_TYPES.get(t.dtype)
     if kind is None:
-        raise TypeError(f"{name} must be float32 or float16, got {x.dtype}")
-    T, H = x.shape
-    return _dev(x, x.dtype, name), kind, T, H
-
-
-def _norm_outputs(y, q, scales, n: int, nb: int) -> tuple:
-    return (None if y is None else _dev(y, _F16, "y", n), None if q is None else _dev(q, _FP8, "q", n),
-            None if scales is None else _dev(scales, _F32, "scales", nb))
+        raise TypeError(f"{name} must be float32 or float16, got {t.dtype}")
+    return kind
 
 
 def moe_norm(cfg: moe_norm_cfg, x: torch.Tensor, w: torch.Tensor, b: torch.Tensor | None = None,
@@ -594,10 +588,13 @@ def moe_norm(cfg: moe_norm_cfg, x: torch.Tensor, w: torch.Tensor, b: torch.Tenso
              stream=None) -> None:
     """norm(x) of x [T][H] (float16 or float32) as float16 y, as float8_e4m3fn codes q with scales
     [T][ceil(H / 128)], or both."""
-    ptr, kind, T, H = _stream_rows(x, "x")
-    py, pq, ps = _norm_outputs(y, q, scales, T * H, T * _nb(H))
-    status = _lib.moe_norm(cfg, ptr, kind, T, H, _dev(w, _F16, "w", H), None if b is None else _dev(b, _F16, "b", H),
-                           py, pq, ps, _stream(stream))
+    kind = _stream_type(x, "x")
+    T, H = x.shape
+    n = T * H
+    status = _lib.moe_norm(cfg, _dev(x, x.dtype, "x"), kind, T, H, _dev(w, _F16, "w", H),
+                           None if b is None else _dev(b, _F16, "b", H), None if y is None else _dev(y, _F16, "y", n),
+                           None if q is None else _dev(q, _FP8, "q", n),
+                           None if scales is None else _dev(scales, _F32, "scales", T * _nb(H)), _stream(stream))
     if status:
         _check(status, "moe_norm")
 
@@ -623,26 +620,25 @@ def moe_norm_residual(cfg: moe_norm_cfg, branch: torch.Tensor, residual: torch.T
                       q: torch.Tensor | None = None, scales: torch.Tensor | None = None, stream=None) -> None:
     """h = residual_scale * residual + scale * gate * (branch or its norm with post_w); then, with y or q, the
     norm of h with w as moe_norm gives it. residual and h: float16 or float32 [T][H], of one type."""
-    T, H = branch.shape
+    shape = branch.shape
+    T, H = shape
     n = T * H
-    typ = _F16
+    typ, kind = _F16, MOE_F16
     for name, t in (("residual", residual), ("h", h)):
         if t is not None:
-            if not isinstance(t, torch.Tensor):
-                raise TypeError(f"{name} must be a CUDA tensor")
-            if t.shape != (T, H):
+            kind = _stream_type(t, name)
+            if t.shape != shape:
                 raise ValueError(f"{name} must be [{T}][{H}], got {list(t.shape)}")
             typ = t.dtype
-    if typ not in _LOGIT_TYPES:
-        raise TypeError(f"residual and h must be float32 or float16, got {typ}")
-    py, pq, ps = _norm_outputs(y, q, scales, n, T * _nb(H))
-    pg, kind = (None, MOE_GATE_NONE) if gate is None else _gate(gate, T, H)
+    pg, gk = (None, MOE_GATE_NONE) if gate is None else _gate(gate, T, H)
     status = _lib.moe_norm_residual(
-        cfg, _dev(branch, _F16, "branch"), None if residual is None else _dev(residual, typ, "residual"),
-        _LOGIT_TYPES[typ], T, H, None if post_w is None else _dev(post_w, _F16, "post_w", H),
-        None if post_b is None else _dev(post_b, _F16, "post_b", H), pg, kind, scale, residual_scale,
+        cfg, _dev(branch, _F16, "branch"), None if residual is None else _dev(residual, typ, "residual"), kind, T, H,
+        None if post_w is None else _dev(post_w, _F16, "post_w", H),
+        None if post_b is None else _dev(post_b, _F16, "post_b", H), pg, gk, scale, residual_scale,
         None if h is None else _dev(h, typ, "h"), None if w is None else _dev(w, _F16, "w", H),
-        None if b is None else _dev(b, _F16, "b", H), py, pq, ps, _stream(stream))
+        None if b is None else _dev(b, _F16, "b", H), None if y is None else _dev(y, _F16, "y", n),
+        None if q is None else _dev(q, _FP8, "q", n),
+        None if scales is None else _dev(scales, _F32, "scales", T * _nb(H)), _stream(stream))
     if status:
         _check(status, "moe_norm_residual")
 
@@ -654,6 +650,11 @@ _ACTS = {"none": MOE_ACT_NONE, "relu": MOE_ACT_RELU, "silu": MOE_ACT_SILU, "gelu
 
 def _rows(t, name: str, shape: tuple, dtypes) -> tuple:
     """(pointer, row stride) of a [rows][columns] tensor whose rows may be strided."""
+    try:  # the usual case in few steps
+        if t.is_cuda and t.dtype in dtypes and t.is_contiguous() and t.shape == shape:
+            return t.data_ptr(), shape[1]
+    except AttributeError:
+        pass
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
     if t.dtype not in dtypes:
@@ -667,6 +668,9 @@ def _rows(t, name: str, shape: tuple, dtypes) -> tuple:
     return t.data_ptr(), ld if rows > 1 else cols
 
 
+_HALF, _HALF_OR_FLOAT = (_F16,), (_F16, _F32)
+
+
 def moe_linear_workspace_bytes(T: int, N: int, K: int) -> int:
     return _lib.moe_linear_workspace_bytes(T, N, K)
 
@@ -675,12 +679,13 @@ def moe_linear(x: torch.Tensor, w: torch.Tensor, bias: torch.Tensor | None, y: t
                act: str = "none", residual: torch.Tensor | None = None, stream=None) -> None:
     """y [T][N] (float16 or float32) = act(x W^T + bias) + residual, x [T][K] and w [N][K] float16, bias
     float32 [N], residual of y's type. Rows of x, y and residual may be strided."""
-    T, K = x.shape
+    shape = x.shape
+    T, K = shape
     N, Kw = w.shape
     if Kw != K:
         raise ValueError(f"x has {K} columns, w {Kw}")
-    px, ldx = _rows(x, "x", (T, K), (_F16,))
-    py, ldy = _rows(y, "y", (T, N), (_F16, _F32))
+    px, ldx = _rows(x, "x", shape, _HALF)
+    py, ldy = _rows(y, "y", (T, N), _HALF_OR_FLOAT)
     pr, ldr = (None, 0) if residual is None else _rows(residual, "residual", (T, N), (y.dtype,))
     status = _lib.moe_linear(px, ldx, T, K, _dev(w, _F16, "w"), N, None if bias is None else _dev(bias, _F32, "bias", N),
                              _ACTS[act], pr, ldr, py, _LOGIT_TYPES[y.dtype], ldy, _dev(workspace, _U8, "workspace"),
