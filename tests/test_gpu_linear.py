@@ -217,3 +217,9 @@ def test_refusals():
     with pytest.raises(KeyError):
         moe.moe_linear(x, w, b, y, ws, "tanh")
     moe.moe_linear(x[:0], w, b, y[:0], ws)
+
+
+@pytest.mark.parametrize("T,N,K", [(8, 2500, 520), (11, 2432, 4104), (16, 100, 6000), (10, 2433, 4096), (9, 7290, 136), (16, 7301, 80)])
+def test_every_variant_of_the_weight_stream(T, N, K):
+    _run(T, N, K, "none", True, True, True)
+    _run(T, N, K, "silu", False, False, False, seed=3)
