@@ -7,7 +7,9 @@
 // read once, stays in registers between the sums and the outputs, and each
 // output is written once. A row is shared by whole warps, eight consecutive
 // elements per lane and step; a 1 x 128 scale block is then sixteen lanes of a
-// warp.
+// warp. Measured: 8192 x 4096, FP32 stream, channel gate, FP16 and codes out
+// 68 us, 6.4 TB/s, 95 % of the measured copy rate; 8192 x 4096 FP16 x alone 23 us
+// (partly in L2); one token of 2048 1.8 us.
 #include <algorithm>
 
 #include "common.h"
@@ -213,11 +215,22 @@ cudaError_t launch(const cudaLaunchConfig_t& cfg, const NormArgs& a, bool layer,
 int run_norm(const char* who, NormArgs a, bool f32, bool layer, cudaStream_t st) {
   a.inv_h = 1.0f / (float)a.H;
   a.nb = (a.H + fp8::kBlock - 1) / fp8::kBlock;
+  // A small batch is over soonest with eight elements per lane (one token of
+  // 4096: 1.8 us, with sixteen 2.0, with 32 2.4). From 4 M elements on, where
+  // bytes count, fewer warps with more loads each: x alone takes 32 elements
+  // per lane (8192 x 4096: 23.1 us, with eight 32.6), with a branch and its norm
+  // or long rows sixteen (8192 x 4096: 61 and 59 us, with eight 72 and 60, with
+  // 32 96 and 84: too few warps fit).
   const int units = (a.H / 8 + 31) / 32;  // warps, with eight elements per lane
-  a.warps = std::min(units, kMaxThreads / 32);
   int vec = 1;
-  while (vec * a.warps < units) vec *= 2;
-  a.rows = a.warps >= 4 ? 1 : 4 / a.warps;
+  if ((long long)a.T * a.H >= (1 << 22)) {
+    if (!a.branch) vec = units >= 4 ? 4 : units;
+    else if (units >= (a.pw ? 8 : 16)) vec = 2;
+    if (vec == 3) vec = 2;
+  }
+  while (vec * (kMaxThreads / 32) < units) vec *= 2;
+  a.warps = (units + vec - 1) / vec;
+  a.rows = a.warps == 1 ? 8 : a.warps == 2 ? 2 : 1;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(((long long)a.T + a.rows - 1) / a.rows));
   cfg.blockDim = dim3(32u * (unsigned)a.warps, (unsigned)a.rows);

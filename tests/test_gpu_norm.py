@@ -272,3 +272,32 @@ def test_refusals():
     with pytest.raises(ValueError, match="gate"):
         moe.moe_norm_residual(cfg, c["branch"], c["residual"], y, gate=c["w"][:4])
     moe.moe_norm(cfg, c["residual"][:0], c["w"], None, y[:0])  # no tokens
+
+
+@pytest.mark.parametrize("T,H", [(70_001, 64), (16_400, 264), (8300, 520), (8200, 776), (4200, 1032), (2101, 2008), (1100, 4104),
+                                 (600, 8192), (300, 16384)])
+@pytest.mark.parametrize("f32", [False, True])
+def test_large_batches(T, H, f32):
+    # Above 4 M elements the rows are shared otherwise: the same values as row by row in small batches.
+    g = torch.Generator(device="cuda").manual_seed(T)
+    br = torch.randn((T, H), generator=g, device="cuda").half()
+    res = torch.randn((T, H), generator=g, device="cuda").to(torch.float32 if f32 else torch.float16)
+    w, pw, gate = (torch.rand(H, generator=g, device="cuda").half() for _ in range(3))
+    cfg = moe.moe_norm_config()
+    for post in (None, pw):
+        h, y = torch.full_like(res, 7.0), torch.full_like(br, 7.0)
+        moe.moe_norm_residual(cfg, br, res, h, post, None, gate, 1.0, 1.0, w, None, y)
+        a = br.double()
+        if post is not None:
+            a = a / torch.sqrt((a * a).mean(1, keepdim=True) + 1e-6) * pw.double()
+        want = res.double() + gate.double() * a
+        m = res.double().abs() + (gate.double() * a).abs()
+        e = 2.0 ** -18 * m
+        assert ((h.double() - want).abs() <= e + (2.0 ** -24 if f32 else 2.0 ** -11) * want.abs() + 2.0 ** -25).all()
+        r = 1 / torch.sqrt((want * want).mean(1, keepdim=True) + 1e-6)
+        n = want * r * w.double()
+        e = r * w.double() * e + 2.0 ** -17 * n.abs()  # r's error from h's too
+        assert ((y.double() - n).abs() <= e + 2.0 ** -11 * n.abs() + 2.0 ** -25).all()
+    moe.moe_norm(cfg, res, w, None, y)
+    want = res.double() / torch.sqrt((res.double() ** 2).mean(1, keepdim=True) + 1e-6) * w.double()
+    assert ((y.double() - want).abs() <= (2.0 ** -11 + 2.0 ** -18) * want.abs() + 2.0 ** -25).all()
