@@ -44,7 +44,7 @@ inline LinearPlan linear_plan(int T, int N, int nb, int sms) {
       const float step = std::max(least, std::max(bytes / 113000.0f, blocks * bytes / 14.4e6f));
       const float t = 4.05f + (float)(waves * steps) * step + 0.44f * (float)(waves - 1) +
                       (s > 1 ? 0.5f + 0.076f * (float)s + 0.018f * (float)nt * full : 0.0f) +
-                      (s == 1 && N % 8 ? (float)waves * 0.11f * (float)nt * full : 0.0f);
+                      (s == 1 && N % 8 ? (float)waves * 0.11f * (float)std::min(nt, N) * full : 0.0f);
       if (t < t_best) {
         t_best = t;
         best = {nt, s};
