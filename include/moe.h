@@ -538,6 +538,51 @@ int moe_balance_loss_backward(const moe_balance_cfg* cfg, const void* logits, in
                               const int32_t* counts, const int32_t* tokens, const float* grad_loss,
                               float* dlogits, long long ldd, int accumulate, void* stream);
 
+/* ---- a whole MoE block -----------------------------------------------------
+ * What lies between two residual sums, in one call ("02 / A solução": the
+ * router picks the experts of each token, the rest of the model gets their
+ * result): with the calls above, in this order and on `stream`,
+ *   n      = moe_norm(h)                          (fp16)
+ *   logits = moe_linear(n, gate_w, gate_b)        (fp32)
+ *   y      = moe_layer_forward_scored(n, logits)  (+ moe_shared_forward(n))
+ *   h      = moe_norm_residual(y, h): residual_scale * h + scale * y, or the
+ *            norm of y with post_w, post_b if post_w is not NULL
+ * h        device [T][H] of stream_type (MOE_F16 or MOE_F32), updated in place
+ * ids, weights  device out [T][top_k], the routing used
+ * logits   device fp32 [T][experts] out, or NULL (kept in the workspace): what
+ *          moe_balance_loss takes with ids
+ * Members of moe_block: norm_w, norm_b, post_w, post_b device fp16 [H]; gate_w
+ * device fp16 [experts][H]; gate_b, route_bias device fp32 [experts] or NULL
+ * (route_bias: moe_route_scored's bias); pool, slot_of, n_slots as
+ * moe_expert_forward; shared_g, shared_u device fp16 [shared_inter][H] and
+ * shared_d [H][shared_inter], all NULL with shared_inter 0: no shared path.
+ * workspace >= moe_block_workspace_bytes(b, T) for every T it serves,
+ *          256-aligned, zero-filled before its first use; its first 4 bytes are
+ *          the sticky error word that collects those of the parts
+ *          (moe_expert_forward's and moe_linear's bits).
+ * Limits: those of the parts; T * top_k <= 65536. All arguments are checked
+ * before anything is enqueued.
+ */
+typedef struct {
+  moe_expert_shape shape;
+  int32_t experts, top_k, n_slots;
+  int32_t shared_inter;
+  moe_norm_cfg norm; /* of both norms */
+  moe_route_cfg route;
+  float scale, residual_scale;
+  const void *norm_w, *norm_b;
+  const void* gate_w;
+  const float *gate_b, *route_bias;
+  const void* pool;
+  const int32_t* slot_of;
+  const void *shared_g, *shared_u, *shared_d;
+  const void *post_w, *post_b;
+} moe_block;
+size_t moe_block_workspace_bytes(const moe_block* b, int T);
+int moe_block_forward(const moe_block* b, void* h, int stream_type, int T, int32_t* ids,
+                      float* weights, float* logits, void* workspace, size_t workspace_bytes,
+                      void* stream);
+
 /* ---- residency manager ----------------------------------------------------
  * Per-layer GPU slot pools fed from a complete, immutable host source
  * ("03 / Arquitetura", ADR 0009). One decode step of one layer:

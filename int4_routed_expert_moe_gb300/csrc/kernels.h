@@ -100,6 +100,15 @@ int check_route_cfg(const char* who, const moe_route_cfg* c, const void* logits,
 int launch_quantize_fp8(const __half* x, int rows, int cols, int block_rows, uint8_t* q, float* scales,
                         cudaStream_t st);
 
+// The norms of a whole block (see moe_block_forward): moe_norm that also sets the
+// error word `clear` to 0 (or NULL), and moe_norm_residual in place on h, that
+// also moves the error words of `from` (or NULL) into `into`.
+int block_norm_in(const moe_norm_cfg* cfg, const void* x, int type, int T, int H, const void* w, const void* b,
+                  void* y, int32_t* clear, cudaStream_t st);
+int block_norm_out(const moe_norm_cfg* cfg, const void* branch, void* h, int type, int T, int H, const void* post_w,
+                   const void* post_b, float scale, float residual_scale, int32_t* into, int32_t* from0,
+                   int32_t* from1, cudaStream_t st);
+
 // Slot-table updates of one residency step, passed to the publish kernel by
 // value (so no host buffer has to outlive the launch).
 constexpr int kMaxSlotUpdates = 128;

@@ -36,6 +36,7 @@ struct NormArgs {
   uint8_t* q;
   float* scales;
   int nb;
+  int32_t *clear, *into, *from[2];  // error words of a whole block's workspace
 };
 
 __device__ __forceinline__ void widen(const uint4& v, float (&f)[8]) {
@@ -133,6 +134,16 @@ __global__ void __launch_bounds__(kMaxThreads) norm_kernel(const NormArgs a) {
   __shared__ float red[kMaxThreads / 32];
   griddep_wait();
   griddep_launch_dependents();
+  if (a.clear || a.into) {
+    if (blockIdx.x == 0 && threadIdx.x == 0 && threadIdx.y == 0) {
+      if (a.clear) *a.clear = 0;
+      for (int i = 0; a.into && i < 2; ++i)
+        if (a.from[i] && *a.from[i]) {
+          *a.into |= *a.from[i];
+          *a.from[i] = 0;
+        }
+    }
+  }
   const long long t = (long long)blockIdx.x * a.rows + threadIdx.y;
   const bool live = t < a.T;
   const size_t row = (size_t)(live ? t : 0) * a.H;
@@ -263,6 +274,38 @@ int check_norm(const char* who, const moe_norm_cfg* cfg, int type, int T, int H,
 }
 
 }  // namespace
+
+int block_norm_in(const moe_norm_cfg* cfg, const void* x, int type, int T, int H, const void* w, const void* b,
+                  void* y, int32_t* clear, cudaStream_t st) {
+  NormArgs a = {};
+  a.T = T; a.H = H;
+  a.eps = cfg->eps; a.off = cfg->weight_offset;
+  a.res = x;
+  a.w = static_cast<const __half*>(w);
+  a.b = static_cast<const __half*>(b);
+  a.y = static_cast<__half*>(y);
+  a.clear = clear;
+  return run_norm("moe_block_forward", a, type == MOE_F32, cfg->kind == MOE_NORM_LAYER, st);
+}
+
+int block_norm_out(const moe_norm_cfg* cfg, const void* branch, void* h, int type, int T, int H, const void* post_w,
+                   const void* post_b, float scale, float residual_scale, int32_t* into, int32_t* from0,
+                   int32_t* from1, cudaStream_t st) {
+  NormArgs a = {};
+  a.T = T; a.H = H;
+  a.eps = cfg->eps; a.off = cfg->weight_offset;
+  a.scale = scale; a.rscale = residual_scale;
+  a.branch = static_cast<const __half*>(branch);
+  a.res = h;
+  a.h = h;
+  a.pw = static_cast<const __half*>(post_w);
+  a.pb = static_cast<const __half*>(post_b);
+  a.into = into;
+  a.from[0] = from0;
+  a.from[1] = from1;
+  return run_norm("moe_block_forward", a, type == MOE_F32, cfg->kind == MOE_NORM_LAYER, st);
+}
+
 }  // namespace moe
 
 extern "C" {

@@ -70,6 +70,15 @@ class moe_balance_cfg(ctypes.Structure):
     _fields_ = [("score", ctypes.c_int32), ("coef", ctypes.c_float)]
 
 
+class moe_block(ctypes.Structure):
+    _fields_ = [("shape", moe_expert_shape)] + [
+        (n, ctypes.c_int32) for n in ("experts", "top_k", "n_slots", "shared_inter")] + [
+        ("norm", moe_norm_cfg), ("route", moe_route_cfg), ("scale", ctypes.c_float),
+        ("residual_scale", ctypes.c_float)] + [
+        (n, ctypes.c_void_p) for n in ("norm_w", "norm_b", "gate_w", "gate_b", "route_bias", "pool", "slot_of",
+                                       "shared_g", "shared_u", "shared_d", "post_w", "post_b")]
+
+
 MOE_POLICY_DECAY, MOE_POLICY_LRU, MOE_POLICY_PINNED = 0, 1, 2
 
 
@@ -115,6 +124,7 @@ _SHAPE = ctypes.POINTER(moe_expert_shape)
 _CFG = ctypes.POINTER(moe_route_cfg)
 _NORM = ctypes.POINTER(moe_norm_cfg)
 _BAL = ctypes.POINTER(moe_balance_cfg)
+_BLOCK = ctypes.POINTER(moe_block)
 _LL = ctypes.c_longlong
 _F = ctypes.c_float
 
@@ -153,6 +163,8 @@ _SIGS = {
     "moe_balance_workspace_bytes": (_SZ, [_I, _I, _I]),
     "moe_balance_loss": (_I, [_BAL, _P, _I, _LL, _I, _I, _P, _I, _P, _I, _P, _P, _P, _P, _P, _SZ, _P]),
     "moe_balance_loss_backward": (_I, [_BAL, _P, _I, _LL, _I, _I, _I, _P, _I, _P, _P, _P, _P, _LL, _I, _P]),
+    "moe_block_workspace_bytes": (_SZ, [_BLOCK, _I]),
+    "moe_block_forward": (_I, [_BLOCK, _P, _I, _I, _P, _P, _P, _P, _SZ, _P]),
     "moe_residency_create": (_I, [ctypes.POINTER(moe_residency_cfg), _P, _P, _P, _P, _P,
                                   ctypes.POINTER(_P)]),
     "moe_residency_prepare": (_I, [_P, _I, _P, _I]),
@@ -744,6 +756,56 @@ def moe_balance_loss_backward(cfg: moe_balance_cfg, logits: torch.Tensor, k: int
         _stream(stream))
     if status:
         _check(status, "moe_balance_loss_backward")
+
+
+# ---- a whole MoE block -------------------------------------------------------------
+def moe_block_config(shape, k: int, norm: moe_norm_cfg, norm_w: torch.Tensor, gate_w: torch.Tensor,
+                     route: moe_route_cfg, pool: torch.Tensor, slot_of: torch.Tensor, n_slots: int,
+                     norm_b: torch.Tensor | None = None, gate_b: torch.Tensor | None = None,
+                     route_bias: torch.Tensor | None = None, shared: tuple | None = None,
+                     post_w: torch.Tensor | None = None, post_b: torch.Tensor | None = None, scale: float = 1.0,
+                     residual_scale: float = 1.0) -> moe_block:
+    """An MoE block's weights and settings (made once, passed to every call; it keeps the tensors). gate_w
+    float16 [E][H]; shared: (wg, wu [Is][H], wd [H][Is]) float16 or None."""
+    H, E = int(shape[0]), gate_w.shape[0]
+    if gate_w.shape != (E, H):
+        raise ValueError(f"gate_w must be [E][{H}], got {list(gate_w.shape)}")
+    Is = 0
+    if shared is not None:
+        Is = shared[0].shape[0]
+        for name, t, want in zip(("wg", "wu", "wd"), shared, ((Is, H), (Is, H), (H, Is))):
+            if t.shape != want:
+                raise ValueError(f"{name} must be {list(want)}, got {list(t.shape)}")
+    vec = lambda t, name: None if t is None else _dev(t, _F16, name, H)
+    per = lambda t, name: None if t is None else _dev(t, _F32, name, E)
+    sg, su, sd = (None,) * 3 if shared is None else (_dev(t, _F16, n) for t, n in zip(shared, ("wg", "wu", "wd")))
+    b = moe_block(_shape(shape), E, int(k), int(n_slots), Is, norm, route, float(scale), float(residual_scale),
+                  _dev(norm_w, _F16, "norm_w", H), vec(norm_b, "norm_b"), _dev(gate_w, _F16, "gate_w"),
+                  per(gate_b, "gate_b"), per(route_bias, "route_bias"),
+                  _dev(pool, _U8, "pool", int(n_slots) * moe_expert_block_bytes(shape)), _dev(slot_of, _I32, "slot_of", E),
+                  sg, su, sd, vec(post_w, "post_w"), vec(post_b, "post_b"))
+    b.tensors = (norm_w, norm_b, gate_w, gate_b, route_bias, pool, slot_of, shared, post_w, post_b)
+    return b
+
+
+def moe_block_workspace_bytes(block: moe_block, T: int) -> int:
+    return _lib.moe_block_workspace_bytes(block, T)
+
+
+def moe_block_forward(block: moe_block, h: torch.Tensor, ids: torch.Tensor, weights: torch.Tensor,
+                      workspace: torch.Tensor, logits: torch.Tensor | None = None, stream=None) -> None:
+    """h [T][H] (float16 or float32) through norm, router, experts (and shared FFN) and residual sum, in place."""
+    kind = _stream_type(h, "h")
+    T, H = h.shape
+    if H != block.shape.hidden:
+        raise ValueError(f"h must be [T][{block.shape.hidden}], got {list(h.shape)}")
+    n = T * block.top_k
+    status = _lib.moe_block_forward(
+        block, _dev(h, h.dtype, "h"), kind, T, _dev(ids, _I32, "ids", n), _dev(weights, _F32, "weights", n),
+        None if logits is None else _dev(logits, _F32, "logits", T * block.experts), _dev(workspace, _U8, "workspace"),
+        workspace.numel(), _stream(stream))
+    if status:
+        _check(status, "moe_block_forward")
 
 
 # ---- residency manager -----------------------------------------------------

@@ -124,3 +124,37 @@ def test_shapes_in_the_binding():
             moe._rows(t, "x", (2, 64), (torch.float16,))
     with pytest.raises(TypeError, match="CUDA"):
         moe.moe_balance_loss(moe.moe_balance_config(), f(2, 8), None, None, None, None, None, None, None)
+
+
+def test_block_arguments():
+    P = 4096
+
+    def block(**kw):
+        f = dict(shape=moe.moe_expert_shape(256, 128, 64), experts=16, top_k=4, n_slots=16, shared_inter=0,
+                 norm=moe.moe_norm_config(), route=moe.moe_route_config(), scale=1.0, residual_scale=1.0, norm_w=P, norm_b=None,
+                 gate_w=P, gate_b=None, route_bias=None, pool=P, slot_of=P, shared_g=None, shared_u=None, shared_d=None,
+                 post_w=None, post_b=None)
+        return moe.moe_block(*{**f, **kw}.values())
+
+    def f(b=None, h=P, typ=0, T=2, ids=P, w=P, lg=None, ws=P, nb=1 << 30, **kw):
+        return lib.moe_block_forward(block(**kw) if b is None else b, h, typ, T, ids, w, lg, ws, nb, None)
+    assert f(T=0) == moe.MOE_OK
+    assert lib.moe_block_forward(None, P, 0, 0, P, P, None, P, 0, None) == moe.MOE_ERR_ARG
+    layer, S = moe.moe_norm_config("layer"), dict(shared_inter=128, shared_g=P, shared_u=P, shared_d=P)
+    assert f(T=0, norm=layer, norm_b=P, post_w=P, post_b=P, **S) == moe.MOE_OK
+    assert f(T=0, shape=moe.moe_expert_shape(100, 128, 64)) == moe.MOE_ERR_SHAPE
+    for kw in (dict(T=-1), dict(T=16385), dict(typ=2), dict(experts=0), dict(top_k=0), dict(top_k=17), dict(n_slots=0),
+               dict(shared_inter=100, shared_g=P, shared_u=P, shared_d=P), dict(shared_inter=-64), dict(shared_g=P),
+               {**S, "shared_d": None}, dict(norm_w=None), dict(gate_w=None), dict(pool=None), dict(slot_of=None),
+               dict(norm_b=P), dict(post_b=P), dict(norm=layer, post_b=P), dict(scale=float("nan")),
+               dict(residual_scale=float("inf")), dict(norm=moe.moe_norm_config(eps=-1.0)),
+               dict(route=moe.moe_route_config(n_groups=3)), dict(norm_w=P + 8), dict(gate_w=P + 2), dict(pool=P + 16),
+               dict(slot_of=P + 2), dict(gate_b=P + 2), dict(route_bias=P + 1), {**S, "shared_u": P + 8},
+               dict(h=None), dict(ids=None), dict(w=None), dict(ws=None), dict(h=P + 8), dict(lg=P + 4), dict(ids=P + 2),
+               dict(ws=P + 64)):
+        assert f(**kw) == moe.MOE_ERR_ARG, kw
+    assert f(nb=4096) == moe.MOE_ERR_CAPACITY
+    b = block(**S)
+    assert moe.moe_block_workspace_bytes(b, -1) == 0
+    assert moe.moe_block_workspace_bytes(block(shape=moe.moe_expert_shape(100, 128, 64)), 4) == 0
+    assert moe.moe_block_workspace_bytes(b, 4) > moe.moe_block_workspace_bytes(block(), 4) > 4 * (256 * 4 + 16 * 4)
