@@ -422,7 +422,7 @@ int moe_shared_forward_fp8(const void* x, int T, int H, int Is, const void* wg, 
  *   layer:  norm(v) = (v - mean(v)) / sqrt(mean((v - mean(v))^2) + eps) * (w + weight_offset) + b
  * moe_norm (before a block): y = norm(x), as FP16 (y), as E4M3 codes with a
  * scale per 1 x 128 block (q, scales: as moe_quantize_fp8, from the FP32
- * values), or both.
+ * values; a block with amax < 448 * 2^-126 as one of zeros), or both.
  * moe_norm_residual (after a block, with what comes before the next one):
  *   a = branch, or norm(branch) with post_w, post_b if post_w is not NULL;
  *   h = residual_scale * residual + scale * gate * a;

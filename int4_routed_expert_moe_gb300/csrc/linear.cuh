@@ -44,14 +44,13 @@ __device__ __forceinline__ float sigmoid_times(float v, float m) {
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + e));
   return m * r;
 }
-// The activations in FP32, of N values at a time. NaN gives NaN (relu: v > 0 ?
-// v : 0 v).
+// The activations in FP32, of N values at a time. NaN gives NaN.
 template <bool FAST, int N>
 __device__ __forceinline__ void activate(int act, float (&v)[N]) {
   switch (act) {
     case MOE_ACT_RELU:
 #pragma unroll
-      for (int i = 0; i < N; ++i) v[i] = v[i] > 0.0f ? v[i] : 0.0f * v[i];
+      for (int i = 0; i < N; ++i) asm("max.NaN.f32 %0, %0, 0f00000000;" : "+f"(v[i]));
       break;
     case MOE_ACT_SILU:
 #pragma unroll

@@ -123,6 +123,9 @@ def test_odd_values(T, act):
     if act in ("none", "relu"):
         pos = w[:, 7] > 0
         assert (y[2][pos] == float("inf")).all()
+        assert (y[2][w[:, 7] < 0] == (float("-inf") if act == "none" else 0.0)).all()
+    if act == "sigmoid":
+        assert (y[2] == (w[:, 7] > 0).float()).all()
 
 
 def test_fp16_overflow_and_fp32_range():
