@@ -1,13 +1,16 @@
 // y = act(x W^T + bias) + residual on the tensor cores, more than 16 tokens.
 //
 // Tokens are the MMA's M, rows of W its N. Both operands come by TMA in the
-// 128-byte-swizzled K-major layout, 64 columns (128 bytes) per pipeline step,
-// and a tile's sums stay in tensor memory until its last step; a second
-// accumulator takes the next tile meanwhile.
+// 128-byte-swizzled K-major layout, in steps of 64 columns (128 bytes), and a
+// tile's sums stay in tensor memory until its last step; a second accumulator
+// takes the next tile meanwhile. A pipeline stage holds one, two or four steps:
+// waiting, handing over and committing cost some 0.2 us each time, more than
+// the MMAs of a step of a narrow tile (64 tokens, 2048 x 2048 in tiles of 64
+// columns, us: one step per stage 12.0, two 8.3, four 7.9).
 //
 // linear_gemm_kernel: a block and 128 tokens by NT columns, the K steps of a
 // tile split over a cluster where the tiles are few. linear_pair_kernel: two
-// blocks and 256 x 256. linear_plan picks.
+// blocks and 256 x 256 or 256 x 128. linear_plan picks.
 #include <algorithm>
 #include <mutex>
 
@@ -65,8 +68,10 @@ struct Geo {
   static constexpr int epi = NT >= 128 ? 8 : 4;
   static constexpr int cols = NT / (epi / 4);  // per epilogue warp
   static constexpr int threads = 64 + 32 * epi;
-  static constexpr uint32_t stage = kABytes + (uint32_t)NT * BK * 2;
-  static constexpr int stages = NT == 128 ? 6 : 8;
+  static constexpr int kb = NT == 128 ? 2 : 4;  // steps per stage
+  static_assert(kSegment % kb == 0, "a segment is whole stages");
+  static constexpr uint32_t step = kABytes + (uint32_t)NT * BK * 2, stage = kb * step;
+  static constexpr int stages = NT == 128 ? 3 : 2;
   static constexpr uint32_t tmem_cols = 2 * NT;
   static constexpr uint32_t off_ctrl = (uint32_t)stages * stage;
   static constexpr size_t smem = (size_t)off_ctrl + 1024 + 1024;  // control block, alignment
@@ -156,14 +161,16 @@ __global__ void __launch_bounds__(Geo<NT>::threads, 1)
     bool ok = true;
     for (int tile = first; tile < ta.tiles && ok; tile += stride) {
       const int m0 = (tile % ta.mt) * BM, n0 = (tile / ta.mt) * NT;
-      for (int kb = kb0; kb < kb1; ++kb, ++g) {
-        const int s = g % G::stages;
+      for (int kb = kb0; kb < kb1; kb += G::kb, ++g) {
+        const int s = g % G::stages, n = min(G::kb, kb1 - kb);
         if (g >= G::stages && !(ok = wait(b, &b.empty[s], ((g / G::stages) - 1) & 1, a.flags))) break;
         if (tc::elect_one()) {
           uint8_t* st = sm + (size_t)s * G::stage;
-          tc::bar_expect_tx(&b.full[s], ta.a_bytes + NT * BK * 2);
-          tc::tma_load_2d(st, &map_x, kb * BK, m0, &b.full[s]);
-          tc::tma_load_2d(st + kABytes, &map_w, kb * BK, n0, &b.full[s]);
+          tc::bar_expect_tx(&b.full[s], (uint32_t)n * (ta.a_bytes + NT * BK * 2));
+          for (int i = 0; i < n; ++i) {
+            tc::tma_load_2d(st + i * G::step, &map_x, (kb + i) * BK, m0, &b.full[s]);
+            tc::tma_load_2d(st + i * G::step + kABytes, &map_w, (kb + i) * BK, n0, &b.full[s]);
+          }
         }
         __syncwarp();
       }
@@ -176,22 +183,28 @@ __global__ void __launch_bounds__(Geo<NT>::threads, 1)
     int g = 0, u = 0;
     bool ok = true;
     for (int tile = first; tile < ta.tiles && ok; tile += stride) {
-      for (int kb = kb0, e = 0; kb < kb1; ++kb, ++g) {  // e: step of the segment
-        const int s = g % G::stages;
+      for (int kb = kb0, e = 0; kb < kb1; kb += G::kb, ++g) {  // e: step of the segment
+        const int s = g % G::stages, n = min(G::kb, kb1 - kb);
         if (e == 0 && u >= 2 && !(ok = wait(b, &b.acc_empty[u & 1], ((u >> 1) - 1) & 1, a.flags))) break;
         if (!(ok = wait(b, &b.full[s], (g / G::stages) & 1, a.flags))) break;
         tc::tc_fence_after();
         const uint32_t base = tc::smem_addr(sm + (size_t)s * G::stage);
         const uint64_t ad = tc::sw128_desc(base), bd = tc::sw128_desc(base + kABytes);
+        const bool end = e + n >= ta.seg || kb + n >= kb1;
         if (tc::elect_one()) {
 #pragma unroll
-          for (int kk = 0; kk < BK / 16; ++kk)
-            tc::mma_f16(tmem + (uint32_t)((u & 1) * NT), ad + 2 * kk, bd + 2 * kk, idesc, e > 0 || kk > 0);
+          for (int i = 0; i < G::kb; ++i)
+            if (i < n)
+#pragma unroll
+              for (int kk = 0; kk < BK / 16; ++kk)
+                tc::mma_f16(tmem + (uint32_t)((u & 1) * NT), ad + i * (G::step >> 4) + 2 * kk,
+                            bd + i * (G::step >> 4) + 2 * kk, idesc, e > 0 || i > 0 || kk > 0);
           tc::mma_commit(&b.empty[s]);
-          if (e == ta.seg - 1 || kb == kb1 - 1) tc::mma_commit(&b.acc_full[u & 1]);
+          if (end) tc::mma_commit(&b.acc_full[u & 1]);
         }
         __syncwarp();
-        if (++e == ta.seg || kb == kb1 - 1) {
+        e += n;
+        if (end) {
           e = 0;
           ++u;
         }
@@ -293,16 +306,30 @@ __global__ void __launch_bounds__(Geo<NT>::threads, 1)
   tc::gemm_teardown(tmem, G::tmem_cols);
 }
 
-// ---- SM pairs: 256 tokens by 256 rows of W ----------------------------------
+// ---- SM pairs: 256 tokens by 256 or 128 rows of W ----------------------------
 // Two blocks of a cluster run one tile with cta_group::2 MMAs: each holds its
 // 128 tokens (A) and half of the weight rows (B), and each accumulates its
-// tokens against all 256 rows. Warps: 0 TMA, 1 tensor memory and (in the
-// leading block) MMA issue, 4-11 epilogue (a lane quarter, 128 columns each).
+// tokens against all rows. Warps: 0 TMA, 1 tensor memory and (in the leading
+// block) MMA issue, 4-11 epilogue (a lane quarter, half of the columns each).
+//
+// Measured: 8192 x 8192 x 4096, FP16 out, 292 us (1.88 PFLOP/s, 98 % of the
+// measured BF16 rate; the tensor pipe is active 96 % of the SMs' time); with
+// bias, SiLU and residual 311 us, 92 %: the epilogue's passes through shared
+// memory take bandwidth from the MMAs' operands, which need all of it. Under
+// sustained load the power limit takes them to 335 and 360 us (cuBLAS without
+// epilogue 285 and 328). FP32 out 318 us: 268 MB more to write. 16 tiles of
+// tokens go along N together (kGroup), us: 4 318, 8 308, 16 303, 32 (all) 324:
+// the tiles in flight then read 43 MB, which stays in L2.
 constexpr int kGroup = 16;
+template <int NT>
 struct Pair {
   static constexpr int epi = 8, threads = 384;
-  static constexpr int stages = 6;
-  static constexpr uint32_t stage = kABytes + 128 * BK * 2;
+  static constexpr int cols = NT / 2;  // per epilogue warp
+  static constexpr int kb = NT == 256 ? 1 : 2;  // steps per stage (256: two 3 % slower, 128: one 17 % slower)
+  static_assert(kSegment % kb == 0, "a segment is whole stages");
+  static constexpr uint32_t step = kABytes + (uint32_t)(NT / 2) * BK * 2, stage = kb * step;
+  static constexpr int stages = NT == 256 ? 6 : 4;
+  static constexpr uint32_t tmem_cols = 2 * NT;
   static constexpr uint32_t off_out = stages * stage;  // [epi][32 rows][128 bytes]
   static constexpr uint32_t off_ctrl = off_out + epi * 4096;
   static constexpr size_t smem = (size_t)off_ctrl + 1024 + 1024;
@@ -334,12 +361,12 @@ __device__ __forceinline__ void place(const TileArgs& t, int tile, int& m, int& 
   n = r / wide;
 }
 
-template <typename Y>
-__global__ void __launch_bounds__(Pair::threads, 1)
+template <typename Y, int NT>
+__global__ void __launch_bounds__(Pair<NT>::threads, 1)
     linear_pair_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_w,
                        const __grid_constant__ CUtensorMap map_y, const __grid_constant__ CUtensorMap map_r,
                        const LinearArgs a, const TileArgs ta) {
-  using G = Pair;
+  using G = Pair<NT>;
   extern __shared__ uint8_t smraw[];
   uint8_t* sm = tc::align1024(smraw);
   const Bars b = bars_at(sm + G::off_ctrl, G::stages);
@@ -362,7 +389,7 @@ __global__ void __launch_bounds__(Pair::threads, 1)
     *b.abort = 0;
     tc::bar_init_fence();
   }
-  if (warp == 1) tc::tmem_alloc2(b.tmem_slot, 512);
+  if (warp == 1) tc::tmem_alloc2(b.tmem_slot, G::tmem_cols);
   tc::tc_fence_before();
   __syncthreads();
   cluster_sync();
@@ -373,10 +400,10 @@ __global__ void __launch_bounds__(Pair::threads, 1)
 
   const int nb = ta.nb;
   const int first = (int)blockIdx.x / 2, stride = (int)gridDim.x / 2;
-  // FP32 results: sums of segments in registers. 384 x 168 registers at launch
-  // = 128 x 72 + 256 x 216.
-  constexpr bool SEG = sizeof(Y) == 4;
-  if (SEG && warp < 4) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+  // FP32 results: sums of segments in registers, 128 of them with 256 columns.
+  // 384 x 168 registers at launch = 128 x 72 + 256 x 216.
+  constexpr bool SEG = sizeof(Y) == 4, kSplitRegs = SEG && NT == 256;
+  if (kSplitRegs && warp < 4) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
   if (warp == 0) {
     // Both blocks' loads complete on the leading block's barrier.
     int g = 0;
@@ -385,16 +412,18 @@ __global__ void __launch_bounds__(Pair::threads, 1)
       int m0, n0;
       place(ta, tile, m0, n0);
       m0 = m0 * 256 + rank * BM;
-      n0 = n0 * 256 + rank * 128;
-      for (int kb = 0; kb < nb; ++kb, ++g) {
-        const int s = g % G::stages;
+      n0 = n0 * NT + rank * (NT / 2);
+      for (int kb = 0; kb < nb; kb += G::kb, ++g) {
+        const int s = g % G::stages, n = min(G::kb, nb - kb);
         if (g >= G::stages && !(ok = wait(b, &b.empty[s], ((g / G::stages) - 1) & 1, a.flags))) break;
         if (tc::elect_one()) {
           uint8_t* st = sm + (size_t)s * G::stage;
           const uint32_t full = tc::map_rank(tc::smem_addr(&b.full[s]), 0);
-          if (rank == 0) tc::bar_expect_tx(&b.full[s], 2 * G::stage);
-          tc::tma_load_2d_pair(st, &map_x, kb * BK, m0, full);
-          tc::tma_load_2d_pair(st + kABytes, &map_w, kb * BK, n0, full);
+          if (rank == 0) tc::bar_expect_tx(&b.full[s], (uint32_t)n * 2 * G::step);
+          for (int i = 0; i < n; ++i) {
+            tc::tma_load_2d_pair(st + i * G::step, &map_x, (kb + i) * BK, m0, full);
+            tc::tma_load_2d_pair(st + i * G::step + kABytes, &map_w, (kb + i) * BK, n0, full);
+          }
         }
         __syncwarp();
       }
@@ -408,26 +437,32 @@ __global__ void __launch_bounds__(Pair::threads, 1)
     }
   } else if (warp == 1) {
     if (rank == 0) {
-      constexpr uint32_t idesc = tc::idesc_f16(256, 256);
+      constexpr uint32_t idesc = tc::idesc_f16(256, NT);
       int g = 0, u = 0;
       bool ok = true;
       for (int tile = first; tile < ta.tiles && ok; tile += stride) {
-        for (int kb = 0, e = 0; kb < nb; ++kb, ++g) {  // e: step of the segment
-          const int s = g % G::stages;
+        for (int kb = 0, e = 0; kb < nb; kb += G::kb, ++g) {  // e: step of the segment
+          const int s = g % G::stages, n = min(G::kb, nb - kb);
           if (e == 0 && u >= 2 && !(ok = wait(b, &b.acc_empty[u & 1], ((u >> 1) - 1) & 1, a.flags))) break;
           if (!(ok = wait(b, &b.full[s], (g / G::stages) & 1, a.flags))) break;
           tc::tc_fence_after();
           const uint32_t base = tc::smem_addr(sm + (size_t)s * G::stage);
           const uint64_t ad = tc::sw128_desc(base), bd = tc::sw128_desc(base + kABytes);
+          const bool end = e + n >= ta.seg || kb + n >= nb;
           if (tc::elect_one()) {
 #pragma unroll
-            for (int kk = 0; kk < BK / 16; ++kk)
-              mma_f16_pair(tmem + (uint32_t)((u & 1) * 256), ad + 2 * kk, bd + 2 * kk, idesc, e > 0 || kk > 0);
+            for (int i = 0; i < G::kb; ++i)
+              if (i < n)
+#pragma unroll
+                for (int kk = 0; kk < BK / 16; ++kk)
+                  mma_f16_pair(tmem + (uint32_t)((u & 1) * NT), ad + i * (G::step >> 4) + 2 * kk,
+                               bd + i * (G::step >> 4) + 2 * kk, idesc, e > 0 || i > 0 || kk > 0);
             tc::mma_commit_pair(&b.empty[s]);
-            if (e == ta.seg - 1 || kb == nb - 1) tc::mma_commit_pair(&b.acc_full[u & 1]);
+            if (end) tc::mma_commit_pair(&b.acc_full[u & 1]);
           }
           __syncwarp();
-          if (++e == ta.seg || kb == nb - 1) {
+          e += n;
+          if (end) {
             e = 0;
             ++u;
           }
@@ -435,11 +470,11 @@ __global__ void __launch_bounds__(Pair::threads, 1)
       }
     }
   } else if (warp >= 4) {
-    if constexpr (SEG) asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
+    if constexpr (kSplitRegs) asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
     constexpr int kBox = 128 / (int)sizeof(Y);                  // columns per staged row
     constexpr int kPass = kBox, kChunks = kPass / 32;           // columns and chunks per staging pass
     const int q4 = warp & 3, e8 = warp - 4, j2 = e8 >> 2;
-    const uint32_t tl = tmem + ((uint32_t)(32 * q4) << 16) + (uint32_t)(128 * j2);
+    const uint32_t tl = tmem + ((uint32_t)(32 * q4) << 16) + (uint32_t)(G::cols * j2);
     const uint32_t acc_empty0 = tc::map_rank(tc::smem_addr(&b.acc_empty[0]), 0);
     uint8_t* out = sm + G::off_out + e8 * 4096;
     int u = 0, loads = 0;
@@ -447,17 +482,17 @@ __global__ void __launch_bounds__(Pair::threads, 1)
       int y0, x0;
       place(ta, tile, y0, x0);
       y0 = y0 * 256 + rank * BM + 32 * q4;
-      x0 = x0 * 256 + 128 * j2;
+      x0 = x0 * NT + G::cols * j2;
       const int row = y0 + lane;
-      float sum[SEG ? 128 : 1] = {};
+      float sum[SEG ? G::cols : 1] = {};
       if constexpr (SEG) {
         for (int left = nb; left > ta.seg; left -= ta.seg, ++u) {
           wait(b, &b.acc_full[u & 1], (u >> 1) & 1, a.flags);  // given up: the stores below are left out
           tc::tc_fence_after();
 #pragma unroll
-          for (int c = 0; c < 128; c += 32) {
+          for (int c = 0; c < G::cols; c += 32) {
             uint32_t d[32];
-            tc::tmem_ld32(tl + (uint32_t)((u & 1) * 256 + c), d);
+            tc::tmem_ld32(tl + (uint32_t)((u & 1) * NT + c), d);
             tc::tmem_ld32_wait(d);
 #pragma unroll
             for (int i = 0; i < 32; ++i) sum[c + i] += __uint_as_float(d[i]);
@@ -468,8 +503,8 @@ __global__ void __launch_bounds__(Pair::threads, 1)
         }
       }
       bool got = false;
-#pragma unroll (SEG ? 128 / kPass : 1)
-      for (int p = 0; p < 128 / kPass; ++p) {
+#pragma unroll (SEG ? G::cols / kPass : 1)
+      for (int p = 0; p < G::cols / kPass; ++p) {
         const int xp = x0 + p * kPass;
         // The stores of the last pass have read the staging area; the
         // residual's tile comes into it, and the results take its place.
@@ -487,12 +522,12 @@ __global__ void __launch_bounds__(Pair::threads, 1)
         if (!got) got = wait(b, &b.acc_full[u & 1], (u >> 1) & 1, a.flags);
         tc::tc_fence_after();
         if (load && !wait(b, &b.res[e8], loads++ & 1, a.flags)) got = false;
-        const bool last = p == 128 / kPass - 1;
+        const bool last = p == G::cols / kPass - 1;
 #pragma unroll (SEG ? kChunks : 1)
         for (int c = 0; c < kChunks; ++c) {
           uint32_t d[32];
           __syncwarp();
-          tc::tmem_ld32(tl + (uint32_t)((u & 1) * 256 + p * kPass + 32 * c), d);
+          tc::tmem_ld32(tl + (uint32_t)((u & 1) * NT + p * kPass + 32 * c), d);
           tc::tmem_ld32_wait(d);
           if (last && c == kChunks - 1) {
             tc::tc_fence_before();
@@ -571,7 +606,7 @@ __global__ void __launch_bounds__(Pair::threads, 1)
   __syncwarp();
   cluster_sync();  // neither block leaves while the other's MMAs, loads or arrivals can reach it
   tc::tc_fence_after();
-  if (warp == 1) tc::tmem_dealloc2(tmem, 512);
+  if (warp == 1) tc::tmem_dealloc2(tmem, G::tmem_cols);
 }
 
 // A row-major matrix [rows][cols], rows ld elements apart, in boxes of 128-byte rows.
@@ -638,15 +673,15 @@ int launch_gemm(const LinearArgs& a, int splits, int sms, int dev, cudaStream_t 
   return a.y32 ? launch_gemm<NT, true>(a, splits, sms, dev, st) : launch_gemm<NT, false>(a, splits, sms, dev, st);
 }
 
-template <typename Y>
+template <typename Y, int NT>
 int launch_pair(const LinearArgs& a, int sms, int dev, cudaStream_t st) {
   static std::mutex mu;
   static bool set[kMaxDevices] = {};
   {
     std::lock_guard<std::mutex> lock(mu);
     if (!set[dev]) {
-      MOE_CUDA_TRY(cudaFuncSetAttribute(linear_pair_kernel<Y>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                        (int)Pair::smem));
+      MOE_CUDA_TRY(cudaFuncSetAttribute(linear_pair_kernel<Y, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                        (int)Pair<NT>::smem));
       set[dev] = true;
     }
   }
@@ -655,7 +690,7 @@ int launch_pair(const LinearArgs& a, int sms, int dev, cudaStream_t st) {
   t.nb = (a.K + BK - 1) / BK;
   t.seg = f32 ? kSegment : t.nb;
   t.mt = (a.T + 255) / 256;
-  t.nt = (a.N + 255) / 256;
+  t.nt = (a.N + NT - 1) / NT;
   t.tiles = t.mt * t.nt;
   t.group = kGroup;
   t.splits = 1;
@@ -666,19 +701,21 @@ int launch_pair(const LinearArgs& a, int sms, int dev, cudaStream_t st) {
   CUtensorMap mx, mw, my, mr;
   int rc;
   if ((rc = row_map(&mx, a.x, false, a.K, a.T, a.ldx, BM)) != MOE_OK) return rc;
-  if ((rc = row_map(&mw, a.w, false, a.K, a.N, a.K, 128)) != MOE_OK) return rc;
+  if ((rc = row_map(&mw, a.w, false, a.K, a.N, a.K, NT / 2)) != MOE_OK) return rc;
   my = mr = mx;
   if (t.y_tma && (rc = row_map(&my, a.y, f32, a.N, a.T, a.ldy, 32)) != MOE_OK) return rc;
   if (t.r_tma && (rc = row_map(&mr, a.residual, f32, a.N, a.T, a.ldr, 32)) != MOE_OK) return rc;
-  const Launch l((unsigned)(2 * std::min(t.tiles, sms / 2)), Pair::threads, Pair::smem, 2, st);
-  const cudaError_t e = cudaLaunchKernelEx(&l.cfg, linear_pair_kernel<Y>, mx, mw, my, mr, a, t);
+  const Launch l((unsigned)(2 * std::min(t.tiles, sms / 2)), Pair<NT>::threads, Pair<NT>::smem, 2, st);
+  const cudaError_t e = cudaLaunchKernelEx(&l.cfg, linear_pair_kernel<Y, NT>, mx, mw, my, mr, a, t);
   if (e != cudaSuccess) return fail(MOE_ERR_CUDA, "moe_linear launch: %s", cudaGetErrorString(e));
   return MOE_OK;
 }
 
 int launch_plan(const LinearArgs& a, const LinearPlan& p, int sms, int dev, cudaStream_t st) {
+  if (p.pair && p.nt == 256)
+    return a.y32 ? launch_pair<float, 256>(a, sms, dev, st) : launch_pair<__half, 256>(a, sms, dev, st);
+  if (p.pair) return a.y32 ? launch_pair<float, 128>(a, sms, dev, st) : launch_pair<__half, 128>(a, sms, dev, st);
   switch (p.nt) {
-    case 0: return a.y32 ? launch_pair<float>(a, sms, dev, st) : launch_pair<__half>(a, sms, dev, st);
     case 128: return launch_gemm<128>(a, p.splits, sms, dev, st);
     case 64: return launch_gemm<64>(a, p.splits, sms, dev, st);
     default: return launch_gemm<32>(a, p.splits, sms, dev, st);

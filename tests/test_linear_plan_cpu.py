@@ -16,7 +16,7 @@ SHIM = """
 extern "C" void plans(int n, const int* tnk, int sms, int* out) {
   for (int i = 0; i < n; ++i) {
     const moe::LinearPlan p = moe::linear_plan(tnk[3 * i], tnk[3 * i + 1], (tnk[3 * i + 2] + 63) / 64, sms);
-    out[2 * i] = p.nt;
+    out[2 * i] = p.pair ? -p.nt : p.nt;
     out[2 * i + 1] = p.splits;
   }
 }
@@ -58,4 +58,10 @@ def test_splits_never_exceed_the_steps_or_a_wave(plans):
     sizes = np.stack([rng.integers(17, 3000, 20000), rng.integers(1, 9000, 20000), rng.integers(1, 600, 20000) * 8], 1)
     for (T, N, K), (nt, s) in zip(sizes, plans(sizes)):
         if s > 1:
-            assert nt and s <= -(-K // 64) and -(-T // 128) * -(-N // nt) * s <= SMS
+            assert nt > 0 and s <= -(-K // 64) and -(-T // 128) * -(-N // nt) * s <= SMS
+
+
+def test_strided_sizes_run_on_the_pair_kernels(plans):
+    from tests.test_gpu_linear_plans import STRIDED
+    for plan, sizes in STRIDED.items():
+        assert plans(sizes) == [plan] * len(sizes), plan

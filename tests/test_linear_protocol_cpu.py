@@ -2,12 +2,13 @@
 
 A model of the roles of one block (linear_gemm_kernel) or of a pair of blocks
 (linear_pair_kernel) runs random interleavings:
-  producer   per step: wait empty (reuse); issue the block's loads, which land
-             later and count on the leading block's `full`, where the leader's
-             producer also announces the bytes (the peer's may land first);
-  MMA issuer (leading block) wait acc_empty at a segment's first step (reuse)
+  producer   per stage of one or two steps: wait empty (reuse); issue the
+             block's loads, which land later and count on the leading block's
+             `full`, where the leader's producer also announces the bytes (the
+             peer's may land first);
+  MMA issuer (leading block) wait acc_empty at a segment's first stage (reuse)
              and full, issue; the MMAs run in order, later, and their commits
-             arrive on `empty`, and after a segment's last step on `acc_full`,
+             arrive on `empty`, and after a segment's last stage on `acc_full`,
              of every block;
   epilogue   per segment: wait acc_full, read the accumulator, arrive on the
              leader's acc_empty. Pair, after a tile's last segment, in passes:
@@ -23,7 +24,8 @@ import random
 
 import pytest
 
-STAGES = {1: 6, 2: 6}  # single blocks (128-column tiles), pairs
+STAGES = {1: 3, 2: 4}  # single blocks, pairs (of 128 columns)
+PER_STAGE = 2          # steps of 64 columns that a stage holds
 EPI = 8                # epilogue warps per block
 PASSES = 2             # staging passes per tile
 
@@ -54,12 +56,13 @@ class Bar:
 def run(blocks, tiles, steps, seg, seed, drop=None):
     rnd = random.Random(seed)
     stages = STAGES[blocks]
-    # Step g: its tile's step kb, segment number, whether it ends the segment.
+    # Stage g: whether it begins its segment, the segment's number, whether it ends it, its loads.
     plan, n_seg = [], 0
     for _ in range(tiles):
-        for kb in range(steps):
-            last = (kb + 1) % seg == 0 or kb == steps - 1
-            plan.append((kb % seg == 0, n_seg, last))
+        for kb in range(0, steps, PER_STAGE):
+            n = min(PER_STAGE, steps - kb)
+            last = (kb + n) % seg == 0 or kb + n == steps
+            plan.append((kb % seg == 0, n_seg, last, n))
             n_seg += last
     per_tile = n_seg // tiles
     total = len(plan)
@@ -67,7 +70,7 @@ def run(blocks, tiles, steps, seg, seed, drop=None):
     acc_empty = [Bar(EPI * blocks) for _ in range(2)]
     empty = [[Bar(1) for _ in range(stages)] for _ in range(blocks)]
     acc_full = [[Bar(1) for _ in range(2)] for _ in range(blocks)]
-    stage = [[-1] * stages for _ in range(blocks)]  # step whose operands it holds
+    stage = [[{} for _ in range(stages)] for _ in range(blocks)]  # by step: whose operands it holds
     acc = [(-1, 0)] * 2                             # segment, complete
     reads = [0] * n_seg                             # epilogue warps that have read a segment
     mma_done = [0]
@@ -87,13 +90,14 @@ def run(blocks, tiles, steps, seg, seed, drop=None):
             if g >= stages:
                 yield from wait(empty[b][s], g // stages - 1, "empty")
             if b == 0:
-                full[s].arrive(tx=blocks)
+                full[s].arrive(tx=blocks * plan[g][3])
                 yield
-            landing.append((b, s, g))
-            yield
+            for i in range(plan[g][3]):
+                landing.append((b, s, g, i))
+                yield
 
     def issuer():
-        for g, (first, u, _) in enumerate(plan):
+        for g, (first, u, _, _) in enumerate(plan):
             if first and u >= 2:
                 yield from wait(acc_empty[u & 1], (u >> 1) - 1, "acc_empty")
             yield from wait(full[g % stages], g // stages, "full")
@@ -141,16 +145,16 @@ def run(blocks, tiles, steps, seg, seed, drop=None):
             return False
         kind = rnd.choice(kinds)
         if kind == "load":
-            b, s, g = landing.pop(rnd.randrange(len(landing)))
+            b, s, g, i = landing.pop(rnd.randrange(len(landing)))
             if g >= stages and mma_done[0] <= g - stages:
-                raise Hazard(f"load of step {g} lands while step {g - stages} is still to be multiplied")
-            stage[b][s] = g
+                raise Hazard(f"load of stage {g} lands while stage {g - stages} is still to be multiplied")
+            stage[b][s][i] = g
             full[s].land()
         elif kind == "mma":
             g = mmas.pop(0)
-            first, u, last = plan[g]
-            if any(stage[b][g % stages] != g for b in range(blocks)):
-                raise Hazard(f"step {g} multiplies {[stage[b][g % stages] for b in range(blocks)]}")
+            first, u, last, n = plan[g]
+            if any(stage[b][g % stages].get(i) != g for b in range(blocks) for i in range(n)):
+                raise Hazard(f"stage {g} multiplies {[stage[b][g % stages] for b in range(blocks)]}")
             if first:
                 if u >= 2 and reads[u - 2] != EPI * blocks:
                     raise Hazard(f"segment {u} overwrites sums of segment {u - 2} still being read")
@@ -197,7 +201,7 @@ def run(blocks, tiles, steps, seg, seed, drop=None):
 
 
 @pytest.mark.parametrize("blocks", [1, 2])
-@pytest.mark.parametrize("tiles,steps,seg", [(1, 1, 8), (1, 3, 8), (3, 5, 5), (2, 16, 8), (2, 17, 8), (3, 9, 4), (5, 2, 8)])
+@pytest.mark.parametrize("tiles,steps,seg", [(1, 1, 8), (1, 3, 8), (3, 5, 6), (2, 16, 8), (2, 17, 8), (3, 9, 4), (5, 2, 8)])
 def test_no_hazard_and_no_deadlock(blocks, tiles, steps, seg):
     for seed in range(8):
         run(blocks, tiles, steps, seg, seed)
@@ -209,7 +213,7 @@ def test_each_wait_is_needed(blocks, drop):
     failed = 0
     for seed in range(20):
         try:
-            run(blocks, 4, 9, 4, seed, drop)
+            run(blocks, 4, 13, 4, seed, drop)
         except AssertionError:
             failed += 1
     assert failed, f"dropping {drop} went unnoticed"
