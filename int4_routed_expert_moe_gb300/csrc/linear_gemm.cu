@@ -6,7 +6,7 @@
 // takes the next tile meanwhile. A pipeline stage holds one, two or four steps:
 // waiting, handing over and committing cost some 0.2 us each time, more than
 // the MMAs of a step of a narrow tile (64 tokens, 2048 x 2048 in tiles of 64
-// columns, us: one step per stage 12.0, two 8.3, four 7.9).
+// columns, us: one step per stage 12.0, two 9.5, four 8.3).
 //
 // linear_gemm_kernel: a block and 128 tokens by NT columns, the K steps of a
 // tile split over a cluster where the tiles are few. linear_pair_kernel: two

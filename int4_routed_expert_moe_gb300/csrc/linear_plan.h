@@ -18,7 +18,7 @@ struct LinearPlan {
 // The cheapest by a model of the time (us); nb: steps of 64 along K. Fitted to
 // runs of every choice at 13 batch sizes from 17 to 8192 against 12 matrices
 // from 64 x 2048 to 8192 x 8192 (us measured by choice, e.g. 64 tokens, 2048 x
-// 2048: 64/4 6.5, 32/1 8.0, 128/4 7.3, pairs 13.7 and 9.1; 8192 tokens, 256 x
+// 2048: 64/4 6.6, 32/1 7.2, 128/4 7.5, pairs 13.8 and 8.6; 8192 tokens, 256 x
 // 2048: pairs of 128 columns 10.4, 128/1 12.6, 64/1 16.0, pairs of 256 16.0); over
 // them its choice is 0.5 % slower than the best:
 //   single blocks: 3.75 to start and end; a step takes its barriers and MMAs
