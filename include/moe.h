@@ -472,7 +472,7 @@ int moe_norm_residual(const moe_norm_cfg* cfg, const void* branch, const void* r
  * residual device, of y's type, row t at residual + t * ldr (ldr >= N), or
  *          NULL; may be y itself with ldr = ldy
  * y        device, y_type MOE_F16 or MOE_F32, row t at y + t * ldy (ldy >= N);
- *          columns past N are left as they were
+ *          columns past N are left as they were; overlaps neither x nor w
  * Products and sums in FP32, bias, activation and residual too; one rounding.
  * NaN in x W^T gives NaN for every activation.
  * workspace >= moe_linear_workspace_bytes(T, N, K), 256-aligned, zero-filled
@@ -559,7 +559,8 @@ int moe_balance_loss_backward(const moe_balance_cfg* cfg, const void* logits, in
  * workspace >= moe_block_workspace_bytes(b, T) for every T it serves,
  *          256-aligned, zero-filled before its first use; its first 4 bytes are
  *          the sticky error word that collects those of the parts
- *          (moe_expert_forward's and moe_linear's bits).
+ *          (moe_expert_forward's and moe_linear's bits; after bit 2, zero the
+ *          workspace again).
  * Limits: those of the parts; T * top_k <= 65536. All arguments are checked
  * before anything is enqueued.
  */

@@ -682,6 +682,11 @@ int launch_pair(const LinearArgs& a, int sms, int dev, cudaStream_t st) {
     if (!set[dev]) {
       MOE_CUDA_TRY(cudaFuncSetAttribute(linear_pair_kernel<Y, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                         (int)Pair<NT>::smem));
+      // The register split must not ask for more than the block is launched with: it would wait forever.
+      cudaFuncAttributes fa;
+      MOE_CUDA_TRY(cudaFuncGetAttributes(&fa, linear_pair_kernel<Y, NT>));
+      if (sizeof(Y) == 4 && NT == 256 && fa.numRegs * Pair<NT>::threads < 128 * 72 + 256 * 216)
+        return fail(MOE_ERR_UNSUPPORTED, "moe_linear: the pair kernel was built with %d registers per thread", fa.numRegs);
       set[dev] = true;
     }
   }

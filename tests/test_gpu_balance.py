@@ -335,3 +335,37 @@ def test_sequences_over_many_chunks_and_one_workspace_for_all(T, E, k, S):
     _check_forward(other, *small, 2, "sigmoid", 0.01)
     b.forward(cfg, *args)
     assert all(torch.equal(x, y) for x, y in zip((b.counts, b.tokens, b.mean, b.loss), want))
+
+
+@pytest.mark.parametrize("T,E,k,S", [(5000, 1, 1, 2), (9001, 3, 2, 5), (4000, 5, 3, 1023), (4000, 64, 3, 1024), (3 * 128, 64, 2, 16),
+                                     (3 * 128 + 1, 64, 2, 16), (384, 60, 2, 17), (96, 256, 4, 3), (97, 255, 4, 3), (24, 700, 2, 2),
+                                     (25, 700, 2, 2), (41 * 32, 1000, 2, 3), (40 * 32, 1000, 2, 3)])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_borders_between_the_ways_of_joining(T, E, k, S, score):
+    # One block, one launch, two; offsets in shared memory or not; fewest experts.
+    l, ids, off = _inputs(T, E, k, S, masked=True)
+    cfg, b = moe.moe_balance_config(score, 0.5), Buffers(T, E, S)
+    lg, ig, o = _cuda(l), _cuda(ids), _cuda(off)
+    for _ in range(2):  # the workspace is left as it has to be
+        for t in (b.counts, b.tokens, b.mean, b.loss):
+            t.fill_(-7)
+        b.forward(cfg, lg, ig, o)
+        c, n, L = _check_forward(b, l, ids, off, k, score, 0.5)
+    d = torch.full((T, E), 3.0, device="cuda")
+    moe.moe_balance_loss_backward(cfg, lg, k, o, b.counts, b.tokens, None, d)
+    _check_backward(d.double().cpu().numpy(), (0.0, 3.0), l, off, k, c, n, score, 0.5, 1.0, L)
+
+
+def test_runs_of_empty_sequences():
+    # Hundreds of empty sequences at the front, between two tokens and at the end.
+    T, E, k = 300, 20, 2
+    l, ids, _ = _inputs(T, E, k, 1)
+    off = np.concatenate([np.zeros(300), [40], np.full(700, 41), [150, 151], np.full(400, 299), np.full(200, 300)]).astype(np.int32)
+    S = len(off) - 1
+    cfg, b = moe.moe_balance_config("softmax", 1.0), Buffers(T, E, S)
+    o = _cuda(off)
+    b.forward(cfg, _cuda(l), _cuda(ids), o)
+    c, n, L = _check_forward(b, l, ids, off, k, "softmax", 1.0)
+    d = torch.full((T, E), 3.0, device="cuda")
+    moe.moe_balance_loss_backward(cfg, _cuda(l), k, o, b.counts, b.tokens, None, d)
+    _check_backward(d.double().cpu().numpy(), (0.0, 3.0), l, off, k, c, n, "softmax", 1.0, 1.0, L)
