@@ -128,9 +128,12 @@ __device__ __forceinline__ void norm_row(float (&v)[V][8], const NormArgs& a, co
   }
 }
 
-// S: the residual stream's type; BRANCH: moe_norm_residual.
+// S: the residual stream's type; BRANCH: moe_norm_residual. With 32 elements
+// per lane of branch and residual the compiler saves registers by loading them
+// in turns unless one block per SM is asked for (8192 x 16384: 374 us, so 274);
+// the other variants are faster as they come.
 template <int V, typename S, bool LAYER, bool BRANCH>
-__global__ void __launch_bounds__(kMaxThreads) norm_kernel(const NormArgs a) {
+__global__ void __launch_bounds__(kMaxThreads, BRANCH && V == 4 ? 1 : 0) norm_kernel(const NormArgs a) {
   __shared__ float red[kMaxThreads / 32];
   griddep_wait();
   griddep_launch_dependents();
@@ -231,7 +234,7 @@ int run_norm(const char* who, NormArgs a, bool f32, bool layer, cudaStream_t st)
   // bytes count, fewer warps with more loads each: x alone takes 32 elements
   // per lane (8192 x 4096: 23.1 us, with eight 32.6), with a branch and its norm
   // or long rows sixteen (8192 x 4096: 61 and 59 us, with eight 72 and 60, with
-  // 32 96 and 84: too few warps fit).
+  // 32 65 and 60).
   const int units = (a.H / 8 + 31) / 32;  // warps, with eight elements per lane
   int vec = 1;
   if ((long long)a.T * a.H >= (1 << 22)) {
