@@ -42,6 +42,7 @@ struct BalanceArgs {
   long long ld;
   int T, E, k, S, chunk, chunks;
   int pitch;  // of the partial rows: E rounded up to 4
+  float e_per_k;  // E / k
   bool sigmoid;
   float coef;
   const int32_t *ids, *offsets;
@@ -196,13 +197,13 @@ __device__ __forceinline__ int first_sequence(const BalanceArgs& a, const Offset
 // A warp's 32 experts of sequence s from the sums over its chunks: the outputs,
 // and, returned, what they add to the loss.
 __device__ __forceinline__ float finish_experts(const BalanceArgs& a, int s, int e, float p, int c, int n) {
-  const float mean = n ? p / (float)n : 0.0f;
+  const float each = n ? __frcp_rn((float)n) : 0.0f, mean = p * each;
   if (e < a.E) {
     a.counts[(size_t)s * a.E + e] = c;
     if (a.mean) a.mean[(size_t)s * a.E + e] = mean;
   }
   if (e == 0) a.tokens[s] = n;
-  return warp_sum(e < a.E && n ? (float)c * ((float)a.E / ((float)a.k * (float)n)) * mean : 0.0f);
+  return warp_sum(e < a.E ? (float)c * (a.e_per_k * each) * mean : 0.0f);
 }
 
 // The mean of n sequences' losses from their parts; whole block, in a fixed
@@ -248,14 +249,15 @@ __device__ __forceinline__ int next_sequence(const BalanceArgs& a, const Offsets
 
 // The partial rows of sequence s, all of them written, added in order and
 // finished. A thread takes four experts of every slices-th row, four rows' loads
-// in flight (one after the other they took 1 us each). Whole block; sums (of
-// 8 * kThreads values at least), good: scratch.
+// in flight (one after the other they took 1 us each); up to 32 slices, whose
+// sums are then added one by one. Whole block; sums (of 8 * kThreads values at
+// least), good: scratch.
 template <int kThreads, int kGroups>
 __device__ __forceinline__ void join_rows(const BalanceArgs& a, const Offsets& off, int s, int blocks, float* sums,
                                           int32_t* good) {
-  const int quads = a.pitch / 4, slices = min(kThreads / quads, kGroups);
-  const int slice = (int)threadIdx.x / quads, e0 = 4 * ((int)threadIdx.x - slice * quads);
   const int c0 = off(s) / a.chunk, c1 = (off(s + 1) - 1) / a.chunk + 1;
+  const int quads = a.pitch / 4, slices = max(1, min(min(kThreads / quads, min(kGroups, 32)), c1 - c0));
+  const int slice = (int)threadIdx.x / quads, e0 = 4 * ((int)threadIdx.x - slice * quads);
   int32_t* counts = reinterpret_cast<int32_t*>(sums + 4 * kThreads);
   if (slice < slices) {
     float4 p = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
@@ -298,7 +300,7 @@ __device__ __forceinline__ void join_rows(const BalanceArgs& a, const Offsets& o
     float v = 0.0f;
     int c = 0;
     if (e < a.E)
-#pragma unroll 8
+#pragma unroll 4
       for (int w = 0; w < slices; ++w) {
         v += sums[w * a.pitch + e];
         c += counts[w * a.pitch + e];
@@ -776,6 +778,7 @@ int moe_balance_loss(const moe_balance_cfg* cfg, const void* logits, int logit_t
   a.ld = ld;
   a.T = T; a.E = E; a.k = k; a.S = S;
   a.pitch = (E + 3) / 4 * 4;
+  a.e_per_k = (float)E / (float)k;
   moe::set_chunks(a, false);
   a.sigmoid = cfg->score == MOE_SCORE_SIGMOID;
   a.coef = cfg->coef;
