@@ -35,6 +35,9 @@ constexpr int max_chunks(int E) { return E > 512 ? 304 : 152; }  // not decreasi
 // rounds (256 of 256 experts) take about what the chunks take.
 constexpr int kAloneRounds = 3;
 constexpr int kAloneSequences = 16;
+// Tokens that a lane adds one after the other: equal probabilities (an untrained
+// router) make the rounding errors of a long chain add up, by n / 2 2^-25.
+constexpr int kRun = 256;
 constexpr int kFusedRows = 40960;  // chunks times experts that one launch joins
 
 struct BalanceArgs {
@@ -400,7 +403,8 @@ __global__ void __launch_bounds__(threads_of(NV)) balance_partial_kernel(const B
     const int end = min(p1, t + per);
     constexpr bool kAhead = NV <= 16;
     float x[NV], p[NV] = {};
-    int id = -1, n = 0, j = 0;
+    int id = -1, n = 0, j = 0, run = 0;
+    bool begun = false;  // the row holds the sums of whole runs
     if (t < end) {
       if (kAhead) {
         load_row<L, NV, VEC, F16>(a, t, l, x);
@@ -429,16 +433,22 @@ __global__ void __launch_bounds__(threads_of(NV)) balance_partial_kernel(const B
           if (id >= 0 && id < a.E) atomicAdd(&cnt[j * kE + id], 1);
         }
         ++t;
-        if (t == end || t == pass.hi[j]) {
+        const bool done = t == end || t == pass.hi[j];
+        if (done || ++run == kRun) {
 #pragma unroll
           for (int v = 0; v < NV; ++v) {
-            sums[(grp + j) * kE + expert_of<L, NV, VEC>(l, v)] = p[v];
+            float& sum = sums[(grp + j) * kE + expert_of<L, NV, VEC>(l, v)];
+            sum = begun ? sum + p[v] : p[v];
             p[v] = 0.0f;
           }
-          if (l == 0) good[grp + j] = n;
-          n = 0;
-          ++j;
-          if (t == end) break;
+          run = 0;
+          begun = !done;
+          if (done) {
+            if (l == 0) good[grp + j] = n;
+            n = 0;
+            ++j;
+            if (t == end) break;
+          }
         }
         if (kAhead) {
 #pragma unroll

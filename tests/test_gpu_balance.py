@@ -369,3 +369,16 @@ def test_runs_of_empty_sequences():
     d = torch.full((T, E), 3.0, device="cuda")
     moe.moe_balance_loss_backward(cfg, _cuda(l), k, o, b.counts, b.tokens, None, d)
     _check_backward(d.double().cpu().numpy(), (0.0, 3.0), l, off, k, c, n, "softmax", 1.0, 1.0, L)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_long_sums_of_equal_probabilities(score):
+    # 2^25 tokens of an untrained router: p = 1 / 60, whose rounding errors all have one sign.
+    T, E, k = 1 << 25, 60, 1
+    l = torch.zeros((T, E), dtype=torch.float16, device="cuda")
+    ids = torch.arange(T, dtype=torch.int32, device="cuda").remainder_(E).view(T, 1)
+    cfg, b = moe.moe_balance_config(score, 1.0), Buffers(T, E, 1)
+    b.forward(cfg, l, ids, None)
+    assert int(b.tokens) == T and int(b.counts.sum()) == T
+    assert ((b.mean.double() * E - 1).abs() <= 2.0 ** -17).all()  # 2 sums of some 200 terms, and p's own 2^-20
+    assert abs(float(b.loss) - 1) <= 2.0 ** -16
