@@ -28,8 +28,10 @@ namespace {
 constexpr int kMinChunk = 32;  // tokens
 // Threads of a block by the values a lane holds, so that its registers suffice,
 // and chunks at most: what fills 152 SMs once.
-constexpr int threads_of(int nv) { return nv == 8 ? 1024 : nv == 16 ? 512 : 256; }
+constexpr int threads_of(int nv) { return nv == 8 ? 768 : nv == 16 ? 512 : 256; }
+constexpr int back_threads_of(int nv) { return nv == 32 ? 256 : 512; }
 constexpr int max_chunks(int E) { return E > 512 ? 304 : 152; }  // not decreasing in E
+constexpr int back_chunks(int E) { return E > 256 && E <= 512 ? 152 : 304; }
 // A batch of up to 3 rounds of a block's tokens and 16 sequences is one chunk,
 // and so one block: 256 tokens of 64 experts 6.1 us, in eight chunks 11.9; eight
 // rounds (256 of 256 experts) take about what the chunks take.
@@ -588,8 +590,8 @@ __global__ void __launch_bounds__(32 * kJoinWarps) balance_join_kernel(const Bal
 }
 
 template <int L, int NV, int VEC, bool F16>
-__global__ void __launch_bounds__(threads_of(NV)) balance_back_kernel(const BalanceArgs a) {
-  constexpr int kThreads = threads_of(NV);
+__global__ void __launch_bounds__(back_threads_of(NV)) balance_back_kernel(const BalanceArgs a) {
+  constexpr int kThreads = back_threads_of(NV);
   constexpr int G = 32 / L, kGroups = kThreads / 32 * G;
   __shared__ int32_t offs[kLocalOffsets];
   griddep_wait();
@@ -689,7 +691,7 @@ Ws ws_of(int T, int E, int S) {
 
 template <bool BACK, int L, int NV, int VEC, bool F16>
 cudaError_t launch_tokens(cudaLaunchConfig_t cfg, const BalanceArgs& a) {
-  cfg.blockDim = dim3(threads_of(NV));
+  cfg.blockDim = dim3(BACK ? back_threads_of(NV) : threads_of(NV));
   if (BACK) return cudaLaunchKernelEx(&cfg, balance_back_kernel<L, NV, VEC, F16>, a);
   return cudaLaunchKernelEx(&cfg, balance_partial_kernel<L, NV, VEC, F16>, a);
 }
@@ -732,7 +734,7 @@ int check_balance(const char* who, const moe_balance_cfg* c, const void* logits,
 }
 
 void set_chunks(BalanceArgs& a, bool back) {
-  const int most = max_chunks(a.E);
+  const int most = back ? back_chunks(a.E) : max_chunks(a.E);
   a.chunk = std::max(kMinChunk, (a.T + most - 1) / most);
   if (!back && a.S <= kAloneSequences) {
     const int groups = threads_of(a.E <= 256 ? 8 : a.E <= 512 ? 16 : 32) / (a.E <= 64 ? 8 : a.E <= 128 ? 16 : 32);
