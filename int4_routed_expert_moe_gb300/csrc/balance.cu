@@ -16,6 +16,12 @@
 // above 2^15 + 2^13 of them (chunks times experts) a second launch joins all.
 // No floating-point atomics: the same inputs give the same bits. Backward: one
 // pass, the probabilities recomputed.
+//
+// Measured, us: forward, 32768 x 256 in 16 sequences, 17.3: the tokens' loop ends
+// after 8.5 (4.7 TB/s), then come steps that run once, each a round trip through
+// L2 or more (adding the groups 1, ticket 1.6, joining rows 2 to 4, ticket 1.3,
+// losses 1.3); 32768 x 64 12, 256 x 64 6.4. Backward, 32768 x 256: 14.6 (4.6 TB/s),
+// instruction issue 63 %.
 #include <algorithm>
 
 #include "common.h"
@@ -26,15 +32,15 @@ namespace moe {
 namespace {
 
 constexpr int kMinChunk = 32;  // tokens
-// Threads of a block by the values a lane holds, so that its registers suffice,
-// and chunks at most: what fills 152 SMs once.
+// Threads of a block by the values a lane holds, so that its registers suffice
+// (1024 threads spill: 32768 x 256 19.4 us against 17.1), and chunks at most: what
+// fills 152 SMs once, with two blocks per SM backward.
 constexpr int threads_of(int nv) { return nv == 8 ? 768 : nv == 16 ? 512 : 256; }
 constexpr int back_threads_of(int nv) { return nv == 32 ? 256 : 512; }
 constexpr int max_chunks(int E) { return E > 512 ? 304 : 152; }  // not decreasing in E
 constexpr int back_chunks(int E) { return E > 256 && E <= 512 ? 152 : 304; }
 // A batch of up to 3 rounds of a block's tokens and 16 sequences is one chunk,
-// and so one block: 256 tokens of 64 experts 6.1 us, in eight chunks 11.9; eight
-// rounds (256 of 256 experts) take about what the chunks take.
+// and so one block: 256 tokens of 64 experts 6.4 us, 1024 in 32 chunks 9.3.
 constexpr int kAloneRounds = 3;
 constexpr int kAloneSequences = 16;
 // Tokens that a lane adds one after the other: equal probabilities (an untrained
@@ -79,7 +85,8 @@ constexpr int kLocalOffsets = 1024;
 struct Offsets {
   const BalanceArgs& a;
   const int32_t* local;
-  __device__ __forceinline__ Offsets(const BalanceArgs& a, int32_t* sm) : a(a), local(a.S < kLocalOffsets ? sm : nullptr) {
+  __device__ __forceinline__ Offsets(const BalanceArgs& a, int32_t* sm)
+      : a(a), local(a.S < kLocalOffsets ? sm : nullptr) {
     if (local) {
       for (int i = threadIdx.x; i <= a.S; i += blockDim.x) sm[i] = offset_at(a, i);
       __syncthreads();
