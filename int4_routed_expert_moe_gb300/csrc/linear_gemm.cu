@@ -61,6 +61,12 @@ struct TileArgs {
   bool y_tma, r_tma; // pair kernel: rows of y / the residual that TMA can address
 };
 
+// A block of these kernels takes more than half of an SM's shared memory, and so
+// do the library's other kernels with tensor memory: no two are on an SM at
+// once, whatever streams they come from. With two there, the blocks of two
+// clusters could each hold the columns that the other waits for.
+constexpr size_t kSmShared = 228 * 1024;
+
 // Geometry by tile width. Warp 0 issues TMA, warp 1 owns tensor memory and
 // issues the MMAs, the others run the epilogue.
 template <int NT>
@@ -75,6 +81,7 @@ struct Geo {
   static constexpr uint32_t tmem_cols = 2 * NT;
   static constexpr uint32_t off_ctrl = (uint32_t)stages * stage;
   static constexpr size_t smem = (size_t)off_ctrl + 1024 + 1024;  // control block, alignment
+  static_assert(2 * smem > kSmShared, "no second block with tensor memory on the SM");
   static constexpr int red_pitch = NT + 4;                        // floats per row of a partial tile
   static_assert((size_t)BM * red_pitch * 4 <= off_ctrl, "partial tile fits the stage area");
 };
@@ -334,6 +341,7 @@ struct Pair {
   static constexpr uint32_t off_ctrl = off_out + epi * 4096;
   static constexpr size_t smem = (size_t)off_ctrl + 1024 + 1024;
   static_assert(smem <= 232448, "shared memory of a block");
+  static_assert(2 * smem > kSmShared, "no second block with tensor memory on the SM");
 };
 
 __device__ __forceinline__ void mma_f16_pair(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,

@@ -8,7 +8,7 @@
 // output is written once. A row is shared by whole warps, eight consecutive
 // elements per lane and step; a 1 x 128 scale block is then sixteen lanes of a
 // warp. Measured: 8192 x 4096, FP32 stream, channel gate, FP16 and codes out
-// 68 us, 6.4 TB/s, 95 % of the measured copy rate; 8192 x 4096 FP16 x alone 23 us
+// 66.8 us, 6.55 TB/s, 97 % of the measured copy rate; 8192 x 4096 FP16 x alone 23 us
 // (partly in L2); one token of 2048 1.8 us.
 #include <algorithm>
 
@@ -130,7 +130,7 @@ __device__ __forceinline__ void norm_row(float (&v)[V][8], const NormArgs& a, co
 
 // S: the residual stream's type; BRANCH: moe_norm_residual. With 32 elements
 // per lane of branch and residual the compiler saves registers by loading them
-// in turns unless one block per SM is asked for (8192 x 16384: 374 us, so 274);
+// in turns unless one block per SM is asked for (8192 x 16384: 374 us, so 277);
 // the other variants are faster as they come.
 template <int V, typename S, bool LAYER, bool BRANCH>
 __global__ void __launch_bounds__(kMaxThreads, BRANCH && V == 4 ? 1 : 0) norm_kernel(const NormArgs a) {

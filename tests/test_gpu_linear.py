@@ -226,3 +226,23 @@ def test_refusals():
 def test_every_variant_of_the_weight_stream(T, N, K):
     _run(T, N, K, "none", True, True, True)
     _run(T, N, K, "silu", False, False, False, seed=3)
+
+
+def test_all_kernels_at_once():
+    """Each kernel on a stream of its own, all running together: the bits of a call alone."""
+    shapes = [(4, 256, 2048), (16, 2048, 4096), (60, 512, 2048), (64, 2048, 2048), (600, 1024, 512), (2048, 2048, 512)]
+    runs = []
+    for T, N, K in shapes:
+        x, w, b, _ = _ops(T, N, K)
+        for dt in (torch.float16, torch.float32):
+            y, ws = torch.empty((T, N), dtype=dt, device="cuda"), _work(T, N, K)
+            moe.moe_linear(x, w, b, y, ws, "silu")
+            runs.append((x, w, b, y, ws, y.clone(), torch.cuda.Stream()))
+            y.zero_()
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for x, w, b, y, ws, _, st in runs:
+            moe.moe_linear(x, w, b, y, ws, "silu", None, st)
+    torch.cuda.synchronize()
+    for _, _, _, y, ws, want, _ in runs:
+        assert torch.equal(y, want) and moe.moe_workspace_flags(ws) == 0
