@@ -99,6 +99,12 @@ int moe_block_forward(const moe_block* b, void* h, int stream_type, int T, int32
   void *n = ws + w.n, *y = ws + w.y, *ysh = Is ? ws + w.ysh : nullptr;
   if (!logits) logits = reinterpret_cast<float*>(ws + w.logits);
   int32_t* shared_flags = Is ? flags(w.shared) : nullptr;
+  auto layer = [&](bool check_only) {
+    return moe::layer_scored(who, &b->shape, n, &b->route, logits, MOE_F32, E, T, E, b->top_k, b->route_bias, ids,
+                             weights, b->pool, b->slot_of, b->n_slots, ysh, y, ws + w.experts, w.experts_bytes,
+                             MOE_PATH_AUTO, stream, check_only);
+  };
+  if ((rc = layer(true)) != MOE_OK) return rc;  // the experts' path has limits of its own
   if ((rc = moe::block_norm_in(&b->norm, h, stream_type, T, H, b->norm_w, b->norm_b, n, shared_flags, st)) != MOE_OK)
     return rc;
   if ((rc = moe_linear(n, H, T, H, b->gate_w, E, b->gate_b, MOE_ACT_NONE, nullptr, 0, logits, MOE_F32, E, workspace,
@@ -107,10 +113,7 @@ int moe_block_forward(const moe_block* b, void* h, int stream_type, int T, int32
   if (Is && (rc = moe_shared_forward(n, T, H, Is, b->shared_g, b->shared_u, b->shared_d, ysh, ws + w.shared,
                                      w.shared_bytes, stream)) != MOE_OK)
     return rc;
-  if ((rc = moe_layer_forward_scored(&b->shape, n, &b->route, logits, MOE_F32, E, T, E, b->top_k, b->route_bias, ids,
-                                     weights, b->pool, b->slot_of, b->n_slots, ysh, y, ws + w.experts,
-                                     w.experts_bytes, MOE_PATH_AUTO, stream)) != MOE_OK)
-    return rc;
+  if ((rc = layer(false)) != MOE_OK) return rc;
   return moe::block_norm_out(&b->norm, y, h, stream_type, T, H, b->post_w, b->post_b, b->scale, b->residual_scale,
                              flags(0), flags(w.experts), shared_flags, st);
 }

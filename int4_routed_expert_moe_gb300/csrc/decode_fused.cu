@@ -1318,13 +1318,13 @@ size_t fused_workspace_bytes(int H, int I, int T, int k) {
 
 int fused_forward_routed(const ForwardArgs& fa, const float* logits, int renorm, int32_t* ids_out,
                          float* wts_out) {
-  int dev = 0, sms = 0;
-  int rc = device_sms(&dev, &sms);
-  if (rc != MOE_OK) return rc;
   const int xc = (fa.H + 1023) / 1024, hc = (fa.I + 1023) / 1024;
   if (xc > 4 || hc > 2) return fail(MOE_ERR_UNSUPPORTED, "streamed decode: H <= 4096 and I <= 2048 only");
   if (fa.T > kMaxT || fa.T * fa.k > kMaxP || fa.E > kMaxE)
     return fail(MOE_ERR_UNSUPPORTED, "streamed decode: T <= %d, T*k <= %d and E <= %d only", kMaxT, kMaxP, kMaxE);
+  int dev = 0, sms = 0;
+  const int rc = device_sms(&dev, &sms);
+  if (rc != MOE_OK) return rc;
   StreamParams a;
   a.H = fa.H; a.I = fa.I; a.g = fa.g; a.T = fa.T; a.k = fa.k; a.E = fa.E; a.n_slots = fa.n_slots;
   a.P = fa.T * fa.k;

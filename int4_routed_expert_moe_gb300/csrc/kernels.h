@@ -96,6 +96,13 @@ int grouped_forward(const ForwardArgs& a);
 int check_route_cfg(const char* who, const moe_route_cfg* c, const void* logits, int logit_type, long long ld, int T,
                     int E, int k);
 
+// moe_layer_forward_scored; check_only: its argument checks alone, nothing is
+// enqueued. `who` is named in errors.
+int layer_scored(const char* who, const moe_expert_shape* s, const void* x, const moe_route_cfg* cfg, const void* logits,
+                 int logit_type, long long ld, int T, int E, int k, const float* bias, int32_t* ids, float* weights,
+                 const void* pool, const int32_t* slot_of, int n_slots, const void* y_shared, void* y, void* workspace,
+                 size_t workspace_bytes, int path, void* stream, bool check_only);
+
 // FP16 to E4M3 with block scales (see moe_quantize_fp8); arguments checked by the caller.
 int launch_quantize_fp8(const __half* x, int rows, int cols, int block_rows, uint8_t* q, float* scales,
                         cudaStream_t st);

@@ -158,3 +158,15 @@ def test_block_arguments():
     assert moe.moe_block_workspace_bytes(b, -1) == 0
     assert moe.moe_block_workspace_bytes(block(shape=moe.moe_expert_shape(100, 128, 64)), 4) == 0
     assert moe.moe_block_workspace_bytes(b, 4) > moe.moe_block_workspace_bytes(block(), 4) > 4 * (256 * 4 + 16 * 4)
+
+
+def test_block_checks_the_experts_path_before_any_launch():
+    # Small batches whose picks' intermediates exceed a block's shared memory on the GEMV path. Without a GPU a
+    # launch would end in MOE_ERR_CUDA.
+    P, none = 4096, None
+    for inter, k in ((4096, 32), (8192, 16)):
+        b = moe.moe_block(moe.moe_expert_shape(64, inter, 64), 64, k, 64, 0, moe.moe_norm_config(), moe.moe_route_config(),
+                          1.0, 1.0, P, none, P, none, none, P, P, none, none, none, none, none)
+        for T in (1, 2, 8):
+            assert lib.moe_block_forward(b, P, 0, T, P, P, none, P, 1 << 40, none) == moe.MOE_ERR_UNSUPPORTED, (inter, k, T)
+            assert "GEMV path" in moe.moe_last_error()

@@ -213,3 +213,28 @@ def test_refusals(pool):
     with pytest.raises(moe.MoeError):  # an RMS norm has no bias
         moe.moe_block_forward(b, h, ids, w, ws)
     moe.moe_block_forward(m.block, h[:0], ids[:0], w[:0], ws)
+
+
+def test_a_refused_batch_leaves_the_buffers_as_they_were():
+    # 32 picks of inter 4096 exceed the GEMV path's shared memory; the same block serves batches of the grouped path.
+    shape, experts, k = (256, 4096, 64), 64, 32
+    one = torch.zeros(moe.moe_expert_block_bytes(shape), dtype=torch.uint8, device="cuda")
+    slot_of = torch.zeros(experts, dtype=torch.int32, device="cuda")
+    half = lambda *s: torch.ones(s, dtype=torch.float16, device="cuda")
+    b = moe.moe_block_config(shape, k, moe.moe_norm_config(), half(256), half(experts, 256), moe.moe_route_config(), one,
+                             slot_of, 1, shared=(half(128, 256), half(128, 256), half(256, 128)))
+    ws = torch.zeros(moe.moe_block_workspace_bytes(b, 20), dtype=torch.uint8, device="cuda")
+    for T, refused in ((2, True), (20, False)):
+        h, logits = torch.full((T, 256), 2.0, device="cuda"), torch.full((T, experts), 9.0, device="cuda")
+        ids, w = torch.full((T, k), -9, dtype=torch.int32, device="cuda"), torch.full((T, k), 9.0, device="cuda")
+        before = ws.clone()
+        if not refused:
+            moe.moe_block_forward(b, h, ids, w, ws, logits)
+            assert (ids >= 0).all() and (logits != 9.0).all() and moe.moe_workspace_flags(ws) == 0
+            continue
+        with pytest.raises(moe.MoeError) as e:
+            moe.moe_block_forward(b, h, ids, w, ws, logits)
+        assert e.value.status == moe.MOE_ERR_UNSUPPORTED
+        torch.cuda.synchronize()
+        assert (h == 2.0).all() and (logits == 9.0).all() and (ids == -9).all() and (w == 9.0).all()
+        assert torch.equal(ws, before)
