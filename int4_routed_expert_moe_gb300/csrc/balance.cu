@@ -771,7 +771,7 @@ struct Launch {
 extern "C" {
 
 size_t moe_balance_workspace_bytes(int T, int E, int S) {
-  if (T < 0 || E < 1 || E > 1024 || S < 1 || S > 65535) return 0;
+  if (T < 0 || T > (1 << 27) || E < 1 || E > 1024 || S < 1 || S > 65535) return 0;
   return moe::ws_of(T, E, S).total;
 }
 

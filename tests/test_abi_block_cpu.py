@@ -170,3 +170,10 @@ def test_block_checks_the_experts_path_before_any_launch():
         for T in (1, 2, 8):
             assert lib.moe_block_forward(b, P, 0, T, P, P, none, P, 1 << 40, none) == moe.MOE_ERR_UNSUPPORTED, (inter, k, T)
             assert "GEMV path" in moe.moe_last_error()
+
+
+def test_balance_workspace_of_more_tokens_than_a_call_takes():
+    most = 1 << 27
+    assert moe.moe_balance_workspace_bytes(most, 1024, 65535) > 0
+    for T in (most + 1, 1 << 30, (1 << 31) - 32, (1 << 31) - 1):
+        assert moe.moe_balance_workspace_bytes(T, 256, 4) == 0, T
