@@ -73,7 +73,9 @@ int check_block(const char* who, const moe_block* b, int stream_type, int T) {
 extern "C" {
 
 size_t moe_block_workspace_bytes(const moe_block* b, int T) {
-  if (!b || !moe::valid_shape(&b->shape) || T < 0 || b->top_k < 1 || b->experts < 1 || b->shared_inter < 0) return 0;
+  if (!b || !moe::valid_shape(&b->shape) || T < 0 || b->top_k < 1 || b->top_k > 32 || b->experts < 1 ||
+      b->experts > 1024 || b->shared_inter < 0 || b->shared_inter > 65536 || (long long)T * b->top_k > 65536)
+    return 0;
   return moe::block_ws(b, T).total;
 }
 

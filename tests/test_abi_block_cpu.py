@@ -177,3 +177,12 @@ def test_balance_workspace_of_more_tokens_than_a_call_takes():
     assert moe.moe_balance_workspace_bytes(most, 1024, 65535) > 0
     for T in (most + 1, 1 << 30, (1 << 31) - 32, (1 << 31) - 1):
         assert moe.moe_balance_workspace_bytes(T, 256, 4) == 0, T
+
+
+def test_block_workspace_of_arguments_that_a_call_refuses():
+    def size(T, k=8, experts=64, Is=0):
+        b = moe.moe_block(moe.moe_expert_shape(256, 128, 64), experts, k, 64, Is)
+        return moe.moe_block_workspace_bytes(b, T)
+    assert 0 < size(1) < size(8192) and size(2048, 32, 1024, 65536) > 0
+    for a in ((8193,), (1 << 28,), ((1 << 31) - 1,), (2049, 32), (1, 33), (1, 8, 1025), (1, 8, (1 << 31) - 1), (1, 8, 64, 65600)):
+        assert size(*a) == 0, a
