@@ -474,9 +474,10 @@ int moe_norm_residual(const moe_norm_cfg* cfg, const void* branch, const void* r
  * y        device, y_type MOE_F16 or MOE_F32, row t at y + t * ldy (ldy >= N);
  *          columns past N are left as they were; overlaps neither x nor w
  * Products and sums in FP32, bias, activation and residual too; one rounding.
- * (Above 16 tokens the tensor cores cut the running sum off, not round it,
- * every 16 terms: 2^-24 of it on average. FP32 results add up sums of 512 terms
- * in registers; FP16 results take all of K in one.)
+ * (The tensor cores cut the running sum off, not round it, every 16 terms:
+ * 3.5 2^-24 of it on average. Up to 16 tokens sums of 64 terms are added up in
+ * FP32; above, FP32 results add up sums of 512 terms, and FP16 results take all
+ * of K in one.)
  * NaN in x W^T gives NaN for every activation.
  * workspace >= moe_linear_workspace_bytes(T, N, K), 256-aligned, zero-filled
  * before its first use; its first 4 bytes are the sticky error word (bit 2: a

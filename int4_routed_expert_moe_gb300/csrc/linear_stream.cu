@@ -7,12 +7,16 @@
 // The dot products run on m16n8k16 MMAs (16 rows by 8 tokens), whose order
 // along K is free as long as both operands agree: lane (g, q) loads the pieces
 // at columns 8 q and 32 + 8 q of rows g and g + 8 and of token g, and words 2 i
-// and 2 i + 1 of a piece are the operands of MMA i. The warps' sums are added
-// in warp order.
+// and 2 i + 1 of a piece are the operands of MMA i. Each step's MMAs start from
+// zero, and a warp adds its steps in FP32 (an MMA cuts the running sum off: in one
+// accumulator for all of a warp's K, 8192 terms of K = 65536, terms of one sign
+// were 875 2^-24 off, so 8 2^-24, and a router's logits over K = 2048 3.5e-7, so
+// 1.3e-7); the sums take the time of nothing else. The warps' sums are added in
+// warp order.
 //
-// Measured, us: one token, 256 x 2048 2.4 (a launch's latency), 4096 x 4096 7.4,
-// 8192 x 8192 22.1 (6.1 TB/s, 90 % of the measured copy rate); 16 tokens 3.0,
-// 8.8 and 24.4.
+// Measured, us: one token, 256 x 2048 2.4 (a launch's latency), 4096 x 4096 6.6,
+// 8192 x 8192 22.3 (6.0 TB/s, 89 % of the measured copy rate); 16 tokens 2.9,
+// 7.9 and 24.9.
 #include "common.h"
 #include "device.cuh"
 #include "kernels.h"
@@ -33,9 +37,10 @@ __device__ __forceinline__ void mma_m16n8k16(float (&c)[4], uint32_t a0, uint32_
 }
 __device__ __forceinline__ uint32_t word(const uint4& v, int i) { return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w; }
 
-// NB: tiles of 8 tokens. DEPTH: steps whose loads are on their way.
+// NB: tiles of 8 tokens. DEPTH: steps whose loads are on their way; with one, four
+// blocks per SM (with 68 registers three fit: 16 tokens of 8192 x 8192 34.8 us).
 template <int NB, int DEPTH, int kWarps>
-__global__ void __launch_bounds__(32 * kWarps, 16 / kWarps) linear_stream_kernel(const LinearArgs a) {
+__global__ void __launch_bounds__(32 * kWarps, DEPTH == 1 ? 4 : 16 / kWarps) linear_stream_kernel(const LinearArgs a) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
   const int n0 = blockIdx.x * 16, steps = (a.K + kStep - 1) / kStep;
   const __half* lo = n0 + g < a.N ? a.w + (size_t)(n0 + g) * a.K : nullptr;
@@ -66,13 +71,17 @@ __global__ void __launch_bounds__(32 * kWarps, 16 / kWarps) linear_stream_kernel
       const int s = s0 + d * kWarps;
       if (s >= steps) break;
 #pragma unroll
-      for (int i = 0; i < NB; ++i)
+      for (int i = 0; i < NB; ++i) {
+        float m[4] = {};
 #pragma unroll
         for (int p = 0; p < 2; ++p)
 #pragma unroll
           for (int j = 0; j < 2; ++j)
-            mma_m16n8k16(c[i], word(wl[d][p], 2 * j), word(wh[d][p], 2 * j), word(wl[d][p], 2 * j + 1),
+            mma_m16n8k16(m, word(wl[d][p], 2 * j), word(wh[d][p], 2 * j), word(wl[d][p], 2 * j + 1),
                          word(wh[d][p], 2 * j + 1), word(x[d][i][p], 2 * j), word(x[d][i][p], 2 * j + 1));
+#pragma unroll
+        for (int e = 0; e < 4; ++e) c[i][e] += m[e];
+      }
       load(d, s + DEPTH * kWarps);
     }
   }
