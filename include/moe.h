@@ -476,8 +476,9 @@ int moe_norm_residual(const moe_norm_cfg* cfg, const void* branch, const void* r
  * Products and sums in FP32, bias, activation and residual too; one rounding.
  * (The tensor cores cut the running sum off, not round it, every 16 terms:
  * 3.5 2^-24 of it on average. Up to 16 tokens sums of 64 terms are added up in
- * FP32; above, FP32 results add up sums of 512 terms, and FP16 results take all
- * of K in one.)
+ * FP32; above, FP32 results add up sums of 512 terms and FP16 results of 4096.
+ * With K = 65536 and terms of one sign, the worst case, that comes to 8 2^-24,
+ * 59 2^-24 and, beside the rounding, 440 2^-24 of the result.)
  * NaN in x W^T gives NaN for every activation.
  * workspace >= moe_linear_workspace_bytes(T, N, K), 256-aligned, zero-filled
  * before its first use; its first 4 bytes are the sticky error word (bit 2: a

@@ -27,11 +27,14 @@ namespace {
 constexpr int BM = kLinearTokens;
 constexpr int BK = 64;
 constexpr uint32_t kABytes = BM * BK * 2;
-// FP32 results: an accumulator takes 8 steps (512 of K). The tensor cores cut
-// the running sum off every 16 terms, and the errors add up along K: a router's
-// logits over K = 2048 are 2.3e-6 off when one accumulator takes all of K.
-// Below the rounding of an FP16 result (2.1e-4) that does not show.
+// An accumulator takes 8 steps (512 of K) for FP32 results, 64 (4096) for FP16.
+// The tensor cores cut the running sum off every 16 terms, by 3.5 2^-24 of it on
+// average, and the errors add up along K: a router's logits over K = 2048 are
+// 2.3e-6 off when one accumulator takes all of K (with segments 6.4e-7), and terms
+// of one sign, whose cuts all go one way, 7080 2^-24 over K = 65536 (58 and 440),
+// nearly as much as FP16's rounding, 2^-11.
 constexpr int kSegment = 8;
+constexpr int kSegment16 = 64;
 
 __device__ __forceinline__ uint32_t cluster_rank() {
   uint32_t r;
@@ -75,7 +78,7 @@ struct Geo {
   static constexpr int cols = NT / (epi / 4);  // per epilogue warp
   static constexpr int threads = 64 + 32 * epi;
   static constexpr int kb = NT == 128 ? 2 : 4;  // steps per stage
-  static_assert(kSegment % kb == 0, "a segment is whole stages");
+  static_assert(kSegment % kb == 0 && kSegment16 % kb == 0, "a segment is whole stages");
   static constexpr uint32_t step = kABytes + (uint32_t)NT * BK * 2, stage = kb * step;
   static constexpr int stages = NT == 128 ? 3 : 2;
   static constexpr uint32_t tmem_cols = 2 * NT;
@@ -333,7 +336,7 @@ struct Pair {
   static constexpr int epi = 8, threads = 384;
   static constexpr int cols = NT / 2;  // per epilogue warp
   static constexpr int kb = NT == 256 ? 1 : 2;  // steps per stage (256: two 3 % slower, 128: one 17 % slower)
-  static_assert(kSegment % kb == 0, "a segment is whole stages");
+  static_assert(kSegment % kb == 0 && kSegment16 % kb == 0, "a segment is whole stages");
   static constexpr uint32_t step = kABytes + (uint32_t)(NT / 2) * BK * 2, stage = kb * step;
   static constexpr int stages = NT == 256 ? 6 : 4;
   static constexpr uint32_t tmem_cols = 2 * NT;
@@ -369,7 +372,7 @@ __device__ __forceinline__ void place(const TileArgs& t, int tile, int& m, int& 
   n = r / wide;
 }
 
-template <typename Y, int NT>
+template <typename Y, int NT, bool SEG>
 __global__ void __launch_bounds__(Pair<NT>::threads, 1)
     linear_pair_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_w,
                        const __grid_constant__ CUtensorMap map_y, const __grid_constant__ CUtensorMap map_r,
@@ -408,9 +411,9 @@ __global__ void __launch_bounds__(Pair<NT>::threads, 1)
 
   const int nb = ta.nb;
   const int first = (int)blockIdx.x / 2, stride = (int)gridDim.x / 2;
-  // FP32 results: sums of segments in registers, 128 of them with 256 columns.
+  // Sums of segments in registers, 128 of them with 256 columns.
   // 384 x 168 registers at launch = 128 x 72 + 256 x 216.
-  constexpr bool SEG = sizeof(Y) == 4, kSplitRegs = SEG && NT == 256;
+  constexpr bool kSplitRegs = SEG && NT == 256;
   if (kSplitRegs && warp < 4) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
   if (warp == 0) {
     // Both blocks' loads complete on the leading block's barrier.
@@ -661,7 +664,7 @@ int launch_gemm(const LinearArgs& a, int splits, int sms, int dev, cudaStream_t 
   while (box < BM && box < a.T) box *= 2;
   TileArgs t = {};
   t.nb = (a.K + BK - 1) / BK;
-  t.seg = SEG ? kSegment : t.nb;
+  t.seg = !SEG ? t.nb : a.y32 ? kSegment : kSegment16;
   t.mt = (a.T + BM - 1) / BM;
   t.tiles = t.mt * ((a.N + NT - 1) / NT);
   t.splits = splits;
@@ -676,24 +679,27 @@ int launch_gemm(const LinearArgs& a, int splits, int sms, int dev, cudaStream_t 
   return MOE_OK;
 }
 
+// Whether a tile's sum is taken in segments.
+bool segments(const LinearArgs& a) { return a.y32 || a.K > kSegment16 * BK; }
+
 template <int NT>
 int launch_gemm(const LinearArgs& a, int splits, int sms, int dev, cudaStream_t st) {
-  return a.y32 ? launch_gemm<NT, true>(a, splits, sms, dev, st) : launch_gemm<NT, false>(a, splits, sms, dev, st);
+  return segments(a) ? launch_gemm<NT, true>(a, splits, sms, dev, st) : launch_gemm<NT, false>(a, splits, sms, dev, st);
 }
 
-template <typename Y, int NT>
+template <typename Y, int NT, bool SEG>
 int launch_pair(const LinearArgs& a, int sms, int dev, cudaStream_t st) {
   static std::mutex mu;
   static bool set[kMaxDevices] = {};
   {
     std::lock_guard<std::mutex> lock(mu);
     if (!set[dev]) {
-      MOE_CUDA_TRY(cudaFuncSetAttribute(linear_pair_kernel<Y, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+      MOE_CUDA_TRY(cudaFuncSetAttribute(linear_pair_kernel<Y, NT, SEG>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                         (int)Pair<NT>::smem));
       // The register split must not ask for more than the block is launched with: it would wait forever.
       cudaFuncAttributes fa;
-      MOE_CUDA_TRY(cudaFuncGetAttributes(&fa, linear_pair_kernel<Y, NT>));
-      if (sizeof(Y) == 4 && NT == 256 && fa.numRegs * Pair<NT>::threads < 128 * 72 + 256 * 216)
+      MOE_CUDA_TRY(cudaFuncGetAttributes(&fa, linear_pair_kernel<Y, NT, SEG>));
+      if (SEG && NT == 256 && fa.numRegs * Pair<NT>::threads < 128 * 72 + 256 * 216)
         return fail(MOE_ERR_UNSUPPORTED, "moe_linear: the pair kernel was built with %d registers per thread", fa.numRegs);
       set[dev] = true;
     }
@@ -701,7 +707,7 @@ int launch_pair(const LinearArgs& a, int sms, int dev, cudaStream_t st) {
   constexpr bool f32 = sizeof(Y) == 4;
   TileArgs t = {};
   t.nb = (a.K + BK - 1) / BK;
-  t.seg = f32 ? kSegment : t.nb;
+  t.seg = !SEG ? t.nb : f32 ? kSegment : kSegment16;
   t.mt = (a.T + 255) / 256;
   t.nt = (a.N + NT - 1) / NT;
   t.tiles = t.mt * t.nt;
@@ -719,15 +725,19 @@ int launch_pair(const LinearArgs& a, int sms, int dev, cudaStream_t st) {
   if (t.y_tma && (rc = row_map(&my, a.y, f32, a.N, a.T, a.ldy, 32)) != MOE_OK) return rc;
   if (t.r_tma && (rc = row_map(&mr, a.residual, f32, a.N, a.T, a.ldr, 32)) != MOE_OK) return rc;
   const Launch l((unsigned)(2 * std::min(t.tiles, sms / 2)), Pair<NT>::threads, Pair<NT>::smem, 2, st);
-  const cudaError_t e = cudaLaunchKernelEx(&l.cfg, linear_pair_kernel<Y, NT>, mx, mw, my, mr, a, t);
+  const cudaError_t e = cudaLaunchKernelEx(&l.cfg, linear_pair_kernel<Y, NT, SEG>, mx, mw, my, mr, a, t);
   if (e != cudaSuccess) return fail(MOE_ERR_CUDA, "moe_linear launch: %s", cudaGetErrorString(e));
   return MOE_OK;
 }
 
+template <int NT>
+int launch_pair(const LinearArgs& a, int sms, int dev, cudaStream_t st) {
+  if (a.y32) return launch_pair<float, NT, true>(a, sms, dev, st);
+  return segments(a) ? launch_pair<__half, NT, true>(a, sms, dev, st) : launch_pair<__half, NT, false>(a, sms, dev, st);
+}
+
 int launch_plan(const LinearArgs& a, const LinearPlan& p, int sms, int dev, cudaStream_t st) {
-  if (p.pair && p.nt == 256)
-    return a.y32 ? launch_pair<float, 256>(a, sms, dev, st) : launch_pair<__half, 256>(a, sms, dev, st);
-  if (p.pair) return a.y32 ? launch_pair<float, 128>(a, sms, dev, st) : launch_pair<__half, 128>(a, sms, dev, st);
+  if (p.pair) return p.nt == 256 ? launch_pair<256>(a, sms, dev, st) : launch_pair<128>(a, sms, dev, st);
   switch (p.nt) {
     case 128: return launch_gemm<128>(a, p.splits, sms, dev, st);
     case 64: return launch_gemm<64>(a, p.splits, sms, dev, st);
