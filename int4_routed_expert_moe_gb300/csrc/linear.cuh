@@ -44,6 +44,32 @@ __device__ __forceinline__ float sigmoid_times(float v, float m) {
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + e));
   return m * r;
 }
+// v Phi(v) = max(v, 0) - |v| e^(-v^2/2) t q(t), t = 1 / (1 + 0.34 |v|), where
+// t q(t) stands for e^(v^2/2) erfc(|v| / sqrt 2) / 2: no difference of numbers
+// near 1 (v / 2 (1 + erf) is 2^-24 |v| / 2 off however small the result: FP16
+// results from v = -3.7 down were 4 half steps off). q was fitted for the smallest
+// relative error (least squares, the points weighted by their errors: Lawson's
+// method), 2.5e-8 up to |v| = 13.3, where e^(-v^2/2) ends; all in all within
+// (12 + 1.5 v^2) 2^-24 of the result. -infinity gives NaN, as the product of its
+// factors does. 8192 x 8192 FP32 results of K = 1024, us: 157, with erff 181, with
+// erfcf 370.
+__device__ __forceinline__ float gelu(float v) {
+  float a, z, t;
+  asm("min.NaN.f32 %0, %1, 0f41800000;" : "=f"(a) : "f"(v));  // 16: infinity times 0 is NaN
+  a = fabsf(a);
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(z) : "f"(v * v * -0.72134752f));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(t) : "f"(fmaf(a, 0.34f, 1.0f)));
+  float q = -0.026471842f;
+  q = fmaf(q, t, 0.14114988f);
+  q = fmaf(q, t, -0.2764137f);
+  q = fmaf(q, t, 0.20577717f);
+  q = fmaf(q, t, -0.047084384f);
+  q = fmaf(q, t, 0.11631409f);
+  q = fmaf(q, t, 0.11496757f);
+  q = fmaf(q, t, 0.13614237f);
+  q = fmaf(q, t, 0.13561885f);
+  return fmaf(-z, a * t * q, fmaxf(v, 0.0f));
+}
 // The activations in FP32, of N values at a time. NaN gives NaN.
 template <bool FAST, int N>
 __device__ __forceinline__ void activate(int act, float (&v)[N]) {
@@ -58,7 +84,7 @@ __device__ __forceinline__ void activate(int act, float (&v)[N]) {
       break;
     case MOE_ACT_GELU:
 #pragma unroll
-      for (int i = 0; i < N; ++i) v[i] = 0.5f * v[i] * (1.0f + erff(v[i] * 0.70710678f));
+      for (int i = 0; i < N; ++i) v[i] = gelu(v[i]);
       break;
     case MOE_ACT_GELU_TANH:  // (1 + tanh u) / 2 = 1 / (1 + e^-2u)
 #pragma unroll
