@@ -24,6 +24,7 @@
 // instruction issue 63 %.
 #include <algorithm>
 
+#include "balance_plan.h"
 #include "common.h"
 #include "device.cuh"
 #include "kernels.h"
@@ -31,22 +32,9 @@
 namespace moe {
 namespace {
 
-constexpr int kMinChunk = 32;  // tokens
-// Threads of a block by the values a lane holds, so that its registers suffice
-// (1024 threads spill: 32768 x 256 19.4 us against 17.1), and chunks at most: what
-// fills 152 SMs once, with two blocks per SM backward.
-constexpr int threads_of(int nv) { return nv == 8 ? 768 : nv == 16 ? 512 : 256; }
-constexpr int back_threads_of(int nv) { return nv == 32 ? 256 : 512; }
-constexpr int max_chunks(int E) { return E > 512 ? 304 : 152; }  // not decreasing in E
-constexpr int back_chunks(int E) { return E > 256 && E <= 512 ? 152 : 304; }
-// A batch of up to 3 rounds of a block's tokens and 16 sequences is one chunk,
-// and so one block: 256 tokens of 64 experts 6.4 us, 1024 in 32 chunks 9.3.
-constexpr int kAloneRounds = 3;
-constexpr int kAloneSequences = 16;
 // Tokens that a lane adds one after the other: equal probabilities (an untrained
 // router) make the rounding errors of a long chain add up, by n / 2 2^-25.
 constexpr int kRun = 256;
-constexpr int kFusedRows = 40960;  // chunks times experts that one launch joins
 
 struct BalanceArgs {
   const void* logits;
@@ -379,7 +367,7 @@ template <int L, int NV, int VEC, bool F16>
 __global__ void __launch_bounds__(threads_of(NV)) balance_partial_kernel(const BalanceArgs a) {
   constexpr int kThreads = threads_of(NV), kWarps = kThreads / 32;
   constexpr int kGroups = kWarps * (32 / L);  // in a block
-  constexpr int kE = L * NV, M = 1024 / kE;   // experts at most, sequences of a pass
+  constexpr int kE = L * NV, M = sequences_of(L, NV);  // experts at most, sequences of a pass
   // Rows group + sequence, as the partial rows in memory.
   __shared__ __align__(16) float sums[(kGroups + M) * kE];
   static_assert((kGroups + M) * kE >= 8 * kThreads, "scratch of the joining");
@@ -741,14 +729,10 @@ int check_balance(const char* who, const moe_balance_cfg* c, const void* logits,
 }
 
 void set_chunks(BalanceArgs& a, bool back) {
-  const int most = back ? back_chunks(a.E) : max_chunks(a.E);
-  a.chunk = std::max(kMinChunk, (a.T + most - 1) / most);
-  if (!back && a.S <= kAloneSequences) {
-    const int groups = threads_of(a.E <= 256 ? 8 : a.E <= 512 ? 16 : 32) / (a.E <= 64 ? 8 : a.E <= 128 ? 16 : 32);
-    if (a.T <= kAloneRounds * groups) a.chunk = kAloneRounds * groups;
-  }
-  a.chunks = std::max(1, (a.T + a.chunk - 1) / a.chunk);
-  a.fused = a.chunks * a.E <= kFusedRows;
+  const BalancePlan p = balance_plan(a.T, a.E, a.S, back);
+  a.chunk = p.chunk;
+  a.chunks = p.chunks;
+  a.fused = p.fused;
 }
 
 struct Launch {
