@@ -235,7 +235,9 @@ int moe_token_sort(const int32_t* ids, int T, int k, int E, int32_t* offsets,
  *             forms its output rows of the down projection and the top-k
  *             combine. Falls back to the unfused kernels beyond its limits
  *             (H > 4096, I > 2048, more than 16 tokens or 256 pairs,
- *             E > 1024, or shared memory).
+ *             E > 1024, or shared memory). Those hold the picks' intermediates
+ *             of a token in a block's shared memory: k * I above about
+ *             90,000 is MOE_ERR_UNSUPPORTED (also under MOE_PATH_AUTO).
  *           MOE_PATH_GROUPED: token-sorted tensor-core grouped GEMM: pairs
  *             sorted by expert, tiles of up to 128 pairs; tcgen05 MMAs with
  *             the expert rows as the 128-row operand (expanded from INT4 to
@@ -442,7 +444,8 @@ int moe_shared_forward_fp8(const void* x, int T, int H, int Is, const void* wg, 
  * h may be the residual's own buffer, y that of branch or of an FP16 x; other
  * overlaps are not allowed.
  * A row with an infinity or NaN gives what the formulas give; a row whose sum
- * of squares is beyond FP32 has the reciprocal 0.
+ * of squares is beyond FP32 has the reciprocal 0, a layer norm's row whose own
+ * sum is gives NaN, and squares below FP32 count as 0.
  * Limits: H a multiple of 8 up to 16384 (of 16 with q); buffers 16-byte
  * aligned, token gates and scales 4-byte; eps >= 0; eps, offset, scale and
  * residual_scale finite. T = 0 enqueues nothing.
@@ -522,7 +525,9 @@ int moe_linear(const void* x, long long ldx, int T, int K, const void* w, int N,
  *          added to if accumulate. Rows of a sequence's tokens that n_s leaves
  *          out get 0 (or stay); rows of no sequence stay as they were.
  * FP32 per token; sums over tokens in a fixed order that depends on T, E and
- * the offsets alone: the same inputs give the same bits.
+ * the offsets alone: the same inputs give the same bits. P and the loss are within
+ * (64 + 4 |l|) 2^-24 of themselves, |l| the largest finite logit's magnitude; a
+ * gradient within (32 + 4 |l|) 2^-24 of g coef / (S' n_s) p_te (f_se + sum_j f_sj p_tj).
  * workspace >= moe_balance_workspace_bytes(T, E, S), 256-aligned, zero-filled
  * before its first use and left reusable. Calls that share one must be ordered.
  * Limits: T <= 2^27, T * k <= 2^31 - 1, E <= 1024, k <= min(E, 32),

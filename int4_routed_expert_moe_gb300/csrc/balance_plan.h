@@ -8,8 +8,9 @@ namespace moe {
 
 constexpr int kMinChunk = 32;  // tokens
 // Threads of a block by the values a lane holds, so that its registers suffice
-// (1024 threads spill: 32768 x 256 19.4 us against 17.1), and chunks at most: what
-// fills 152 SMs once, with two blocks per SM backward.
+// (1024 threads spill: 32768 x 256 19.4 us against 17.1; backward with 32 values and
+// 16-byte loads 12 to 16 bytes of a thread do), and chunks at most: what fills the
+// 152 SMs of a GB300 once, with two blocks per SM backward.
 constexpr int threads_of(int nv) { return nv == 8 ? 768 : nv == 16 ? 512 : 256; }
 constexpr int back_threads_of(int nv) { return nv == 32 ? 256 : 512; }
 constexpr int max_chunks(int E) { return E > 512 ? 304 : 152; }  // not decreasing in E

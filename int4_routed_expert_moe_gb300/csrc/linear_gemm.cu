@@ -411,8 +411,8 @@ __global__ void __launch_bounds__(Pair<NT>::threads, 1)
 
   const int nb = ta.nb;
   const int first = (int)blockIdx.x / 2, stride = (int)gridDim.x / 2;
-  // Sums of segments in registers, 128 of them with 256 columns.
-  // 384 x 168 registers at launch = 128 x 72 + 256 x 216.
+  // Sums of segments in registers, 128 of them with 256 columns (a thread spills 32
+  // to 40 bytes). 384 x 168 registers at launch = 128 x 72 + 256 x 216.
   constexpr bool kSplitRegs = SEG && NT == 256;
   if (kSplitRegs && warp < 4) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
   if (warp == 0) {

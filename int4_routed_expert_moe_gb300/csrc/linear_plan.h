@@ -16,11 +16,13 @@ struct LinearPlan {
   int nt, splits;
 };
 // The cheapest by a model of the time (us); nb: steps of 64 along K. Fitted to
-// runs of every choice at 13 batch sizes from 17 to 8192 against 12 matrices
-// from 64 x 2048 to 8192 x 8192 (us measured by choice, e.g. 64 tokens, 2048 x
-// 2048: 64/4 6.6, 32/1 7.2, 128/4 7.5, pairs 13.8 and 8.6; 8192 tokens, 256 x
-// 2048: pairs of 128 columns 10.4, 128/1 12.6, 64/1 16.0, pairs of 256 16.0); over
-// them its choice is 0.5 % slower than the best:
+// runs of every choice, FP16 results, operands in L2 from the run before, at 13
+// batch sizes from 17 to 8192 against 12 matrices from 64 x 2048 to 8192 x 8192
+// (us measured by choice, e.g. 64 tokens, 2048 x 2048: 64/4 6.6, 32/1 7.2, 128/4
+// 7.5, pairs 13.8 and 8.6; 8192 tokens, 256 x 2048: pairs of 128 columns 10.4,
+// 128/1 12.6, 64/1 16.0, pairs of 256 16.0); over them its choice is 0.5 % slower
+// than the best. x from memory and FP32 results take longer (the last pairs of 128
+// columns 13.0 with FP32 results and a bias, 14.9 with x from memory too):
 //   single blocks: 3.75 to start and end; a step takes its barriers and MMAs
 //   (0.113 to 0.23), or what its bytes need at 153 GB/ms per SM and 20.7 GB/ms
 //   in all; joining a split costs 0.37, 0.15 per block and 0.02 per column of a

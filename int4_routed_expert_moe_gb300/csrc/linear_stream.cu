@@ -25,7 +25,7 @@ namespace moe {
 namespace {
 
 constexpr int kStep = 64;
-constexpr int kSms = 152;
+constexpr int kSms = 152;  // of a GB300: where the variants below change over
 
 __device__ __forceinline__ void mma_m16n8k16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                              uint32_t b0, uint32_t b1) {
