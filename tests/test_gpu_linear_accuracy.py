@@ -19,7 +19,7 @@ import pytest
 import torch
 
 from tests import test_gpu_linear as tl
-from tests.linear_accuracy_shapes import LONG, STREAM
+from tests.linear_accuracy_shapes import LONG, SEGMENTED, STREAM
 
 pytestmark = pytest.mark.gpu
 
@@ -85,3 +85,26 @@ def test_router_logits(T, N):
     exact = x.double() @ w.double().t()
     rms = lambda v: float(np.sqrt(float((v * v).mean())))
     assert rms(y.double() - exact) <= 1.5e-6 * rms(exact), rms(y.double() - exact) / rms(exact)
+
+
+@pytest.mark.parametrize("plan", sorted(LONG), ids=lambda p: f"{p[0]}x{p[1]}")
+def test_long_sums_through_the_epilogue(plan):
+    # FP16 results that are added up from segments, with bias, activation and residual.
+    tl._run(*LONG[plan][0], "silu", True, True, False)
+
+
+@pytest.mark.parametrize("plan", sorted(SEGMENTED), ids=lambda p: f"{p[0]}x{p[1]}")
+@pytest.mark.parametrize("pad,rpad", [(8, 8), (3, 8), (8, 3), (1, 5), (4, 4)])
+def test_strides_of_segmented_pairs(plan, pad, rpad):
+    for T, N, K in SEGMENTED[plan]:
+        x, w, b, r = tl._ops(T, N, K)
+        R = torch.full((T, N + rpad), 5.0, dtype=torch.float16, device="cuda")
+        Y = torch.full((T, N + pad), 7.0, dtype=torch.float16, device="cuda")
+        R[:, :N] = r.half()
+        ws = tl._work(T, N, K)
+        moe.moe_linear(x, w, b, Y[:, :N], ws, "gelu", R[:, :N])
+        tl._check(Y[:, :N], x, w, b, "gelu", r.half(), False)
+        assert (Y[:, N:] == 7.0).all() and (R[:, N:] == 5.0).all()
+        moe.moe_linear(x, w, b, R[:, :N], ws, "gelu", R[:, :N])  # in place
+        assert torch.equal(R[:, :N], Y[:, :N]) and (R[:, N:] == 5.0).all()
+        assert moe.moe_workspace_flags(ws) == 0
